@@ -538,7 +538,7 @@ def write_traffic(fetch_db, write_db):
     for match, fname, srcs, alg in (
             (lambda n: n.startswith("gemm_f32_direct<64, 64, true, false, 2,")
              and ("@" not in n or n.endswith(" @%dwg" % (GEMM_N // 64) ** 2)),
-             "traffic_gemm_f32_2048.json", ("gemm_f32.hip",), 3 * 4 * GEMM_N * GEMM_N),
+             "traffic_gemm_f32_2048.json", ("gemm_f32.hip", "gemm_f32_tile.hpp"), 3 * 4 * GEMM_N * GEMM_N),
             (lambda n: n.startswith("gemv_packed_flat<2, 1, 1,"),
              "traffic_gemv_q2_12288x1536.json", q2_srcs, Q2_ALG_BYTES),
             (lambda n: n.startswith("gemv_q2_idot<3,") and n.split(" @")[0].endswith(", 64, false>"),
@@ -1023,7 +1023,7 @@ def main():
     gemm_us = win["gemm_f32"]["mean_us"]
     gemm_tflops = GEMM_FLOPS / gemm_us / 1e6
     psha = src_sha("gemv_packed.hip", "wave.hpp")
-    gemm_traffic = traffic_from_profile("traffic_gemm_f32_2048.json", src_sha("gemm_f32.hip"))
+    gemm_traffic = traffic_from_profile("traffic_gemm_f32_2048.json", src_sha("gemm_f32.hip", "gemm_f32_tile.hpp"))
     q2_traffic = traffic_from_profile("traffic_gemv_q2_12288x1536.json", psha)
     qb_traffic = traffic_from_profile("traffic_gemv_q2_batched_12288x1536.json", psha)
     q4_traffic = traffic_from_profile("traffic_gemv_q4_12288x1536.json", psha)

@@ -30,7 +30,12 @@ GG_ERR_SCRATCH = -5
 ENTRY_POINTS = ("gemm_f32", "gemm_f32_tn", "gemm_f32_nt", "gemm_f32_ex", "gemv_f32",
                 "gemv_f32_batched", "gemv_q2", "gemv_q2_batched", "gemv_q2_batched_ws",
                 "gemv_q2_batched_ws_size", "gemv_q2_batched_noalloc", "gemv_q4",
-                "gemv_q4_batched", "gg_strerror")
+                "gemv_q4_batched", "linear_f32", "linear_f32_bwd", "linear_f32_bwd_ws_size",
+                "rmsnorm_f32", "rmsnorm_mx8", "rmsnorm_f32_bwd", "rmsnorm_f32_bwd_ws_size",
+                "linear_q2_mx8", "linear_q4_mx8", "gg_strerror")
+
+# enum gg_act by name
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu_tanh": 2, "gelu_erf": 3, "silu": 4}
 
 _lib = None
 
@@ -88,6 +93,29 @@ def load(path: str = LIB_PATH):
     lib.gemv_q2_batched_noalloc.restype = ctypes.c_int
     lib.gemv_q2_batched_ws_size.argtypes = [i64, i64, i64]
     lib.gemv_q2_batched_ws_size.restype = i64
+    i32 = ctypes.c_int
+    lib.linear_f32.argtypes = [i32, i32, i64, i64, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64,
+                               vp, i64, vp]
+    lib.linear_f32.restype = i32
+    lib.linear_f32_bwd.argtypes = [i32, i32, i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp,
+                                   i64, vp, i64, vp, i64, vp, vp, i64, vp]
+    lib.linear_f32_bwd.restype = i32
+    lib.linear_f32_bwd_ws_size.argtypes = [i32, i64, i64]
+    lib.linear_f32_bwd_ws_size.restype = i64
+    lib.rmsnorm_f32.argtypes = [i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, vp]
+    lib.rmsnorm_f32.restype = i32
+    lib.rmsnorm_mx8.argtypes = [i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, i64, vp]
+    lib.rmsnorm_mx8.restype = i32
+    lib.rmsnorm_f32_bwd.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp,
+                                    vp, i64, vp]
+    lib.rmsnorm_f32_bwd.restype = i32
+    lib.rmsnorm_f32_bwd_ws_size.argtypes = [i64, i64]
+    lib.rmsnorm_f32_bwd_ws_size.restype = i64
+    for name in ("linear_q2_mx8", "linear_q4_mx8"):
+        f = getattr(lib, name)
+        f.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp,
+                      i64, vp, i64, vp, i64, vp]
+        f.restype = i32
     lib.gg_strerror.argtypes = [ctypes.c_int]
     lib.gg_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -371,3 +399,273 @@ def gemv_q2_batched_noalloc(Qs, Ss, xs, ys=None, stream=None):
 def gemv_q4_batched(Qs, Ss, xs, ys=None, stream=None):
     """As gemv_q2_batched for 4-bit codes (Q uint8 M x >= ceil(K/2))."""
     return _packed_batched("gemv_q4_batched", Qs, Ss, xs, ys, stream)
+
+
+# ----------------------------------------------------- dense layers, norm --
+
+def _arg(t, shape, dtype, name, dev):
+    """(address, leading dimension) of a row-major tensor (or vector) of this
+    shape and type on device number `dev`; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current GPU device" % name)
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError("%s must have a contiguous last dimension" % name)
+    if len(shape) == 1:
+        return t.data_ptr(), shape[0]
+    return t.data_ptr(), st[0] if shape[0] > 1 else max(shape[1], 1)
+
+
+def _new(shape, dtype, like, stream):
+    """A new tensor that belongs to the stream the call runs on, so that its
+    memory is neither taken from nor given back to work of another stream."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _matrix(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    return tuple(t.shape)
+
+
+def _activation(act):
+    try:
+        return ACTIVATIONS[act]
+    except KeyError:
+        raise ValueError("act must be one of %s" % ", ".join(ACTIVATIONS)) from None
+
+
+def _workspace(ws, need, dev, like, stream):
+    torch = _torch()
+    if ws is None:
+        ws = _new((need,), torch.uint8, like, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on the current GPU device")
+    n = ws.numel() * ws.element_size()
+    return ws, ws.data_ptr() if n else None, n
+
+
+def _ws_size(name, *sizes):
+    n = getattr(load(), name)(*sizes)
+    if n < 0:
+        raise GGError(n, name)
+    return n
+
+
+def linear_f32(X, W, bias=None, act="none", residual=None, Z=None, Y=None, trans_w=False,
+               stream=None):
+    """Y = act(X.op(W) + bias) + residual, fp32: X (M x K), W (K x N, or N x K
+    when trans_w), bias (N,), residual and Y (M x N).  act is a name of
+    ACTIVATIONS.  Z (M x N), when given, receives the pre-activation that
+    linear_f32_bwd takes.  Y may be the residual itself."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    M, K = _matrix(X, "X")
+    wshape = _matrix(W, "W")
+    N = wshape[0] if trans_w else wshape[1]
+    px, ldx = _arg(X, (M, K), f32, "X", dev)
+    pw, ldw = _arg(W, (N, K) if trans_w else (K, N), f32, "W", dev)
+    pb, _ = _arg(bias, (N,), f32, "bias", dev)
+    pr, ldr = _arg(residual, (M, N), f32, "residual", dev)
+    pz, ldz = _arg(Z, (M, N), f32, "Z", dev)
+    if Y is None:
+        Y = _new((M, N), f32, X, stream)
+    py, ldy = _arg(Y, (M, N), f32, "Y", dev)
+    _check(load().linear_f32(int(bool(trans_w)), _activation(act), M, N, K, px, ldx, pw, ldw, pb,
+                             pr, ldr, pz, ldz, py, ldy, _stream(stream)), "linear_f32")
+    return Y
+
+
+def linear_f32_bwd_ws_size(act, M, N):
+    """Bytes of workspace linear_f32_bwd needs for an M x N output."""
+    return _ws_size("linear_f32_bwd_ws_size", _activation(act), M, N)
+
+
+def linear_f32_bwd(dY, X, W, Z=None, act="none", trans_w=False, dX=None, dW=None, db=None,
+                   want=("dX", "dW", "db"), accumulate=False, workspace=None, stream=None):
+    """Gradients (dX, dW, db) of linear_f32 from dY (M x N) and the kept
+    pre-activation Z (not needed for act "none"); the residual's gradient is
+    dY itself.  Gradients not named in `want` are not computed and returned
+    as None; outputs not given are allocated.  accumulate: dW and db, which
+    must then be given, are added to."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    M, N = _matrix(dY, "dY")
+    wx, ww, wb = (n in want for n in ("dX", "dW", "db"))
+    K = _matrix(X, "X")[1] if X is not None else _matrix(W, "W")[1 if trans_w else 0]
+    if (wx and W is None) or (ww and X is None):
+        raise ValueError("dX needs W and dW needs X")
+    wshape = (N, K) if trans_w else (K, N)
+    a = _activation(act)
+    if a and Z is None:
+        raise ValueError("act %r needs Z" % act)
+    if accumulate and ((ww and dW is None) or (wb and db is None)):
+        raise ValueError("accumulate needs the gradients to add to")
+    pd, lddy = _arg(dY, (M, N), f32, "dY", dev)
+    pz, ldz = _arg(Z if a else None, (M, N), f32, "Z", dev)
+    px, ldx = _arg(X, (M, K), f32, "X", dev)
+    pw, ldw = _arg(W, wshape, f32, "W", dev)
+    dX = None if not wx else _new((M, K), f32, dY, stream) if dX is None else dX
+    dW = None if not ww else _new(wshape, f32, dY, stream) if dW is None else dW
+    db = None if not wb else _new((N,), f32, dY, stream) if db is None else db
+    pdx, lddx = _arg(dX, (M, K), f32, "dX", dev)
+    pdw, lddw = _arg(dW, wshape, f32, "dW", dev)
+    pdb, _ = _arg(db, (N,), f32, "db", dev)
+    need = _ws_size("linear_f32_bwd_ws_size", a, M, N)
+    keep, pws, nws = _workspace(workspace, need, dev, dY, stream)
+    _check(load().linear_f32_bwd(int(bool(trans_w)), a, int(bool(accumulate)), M, N, K, pd, lddy,
+                                 pz, ldz, px, ldx, pw, ldw, pdx, lddx, pdw, lddw, pdb, pws, nws,
+                                 _stream(stream)), "linear_f32_bwd")
+    return dX, dW, db
+
+
+def rmsnorm_f32(X, gamma=None, eps=1e-5, residual=None, S=None, Y=None, rstd=None, stream=None):
+    """(Y, S, rstd) with S = X + residual, rstd = 1 / sqrt(mean of S^2 over a
+    row + eps) and Y = S * rstd * gamma, fp32, rows of X (M x K).  Without a
+    residual (and with no S given) S is X itself and nothing is written for
+    it.  S may be given as X or the residual itself, to update it in place."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    M, K = _matrix(X, "X")
+    px, ldx = _arg(X, (M, K), f32, "X", dev)
+    pr, ldr = _arg(residual, (M, K), f32, "residual", dev)
+    pg, _ = _arg(gamma, (K,), f32, "gamma", dev)
+    if S is None and residual is not None:
+        S = _new((M, K), f32, X, stream)
+    Y = _new((M, K), f32, X, stream) if Y is None else Y
+    rstd = _new((M,), f32, X, stream) if rstd is None else rstd
+    ps, lds = _arg(S, (M, K), f32, "S", dev)
+    py, ldy = _arg(Y, (M, K), f32, "Y", dev)
+    pt, _ = _arg(rstd, (M,), f32, "rstd", dev)
+    _check(load().rmsnorm_f32(M, K, px, ldx, pr, ldr, pg, float(eps), ps, lds, py, ldy, pt,
+                              _stream(stream)), "rmsnorm_f32")
+    return Y, X if S is None else S, rstd
+
+
+def _bytes(t):
+    """A float8 tensor as its bytes; a uint8 tensor as it is."""
+    torch = _torch()
+    if t is not None and t.dtype in (torch.float8_e4m3fn, torch.float8_e8m0fnu):
+        return t.view(torch.uint8)
+    return t
+
+
+def rmsnorm_mx8(X, gamma=None, eps=1e-5, residual=None, S=None, Q=None, E=None, stream=None):
+    """(Q, E, S): the norm of rmsnorm_f32 with its output in 8 bits, Q (M x K)
+    e4m3 bytes and E (M x ceil(K/32)) powers of two, as uint8 (view them as
+    torch.float8_e4m3fn and torch.float8_e8m0fnu for their values)."""
+    torch = _torch()
+    f32, u8, dev = torch.float32, torch.uint8, torch.cuda.current_device()
+    M, K = _matrix(X, "X")
+    px, ldx = _arg(X, (M, K), f32, "X", dev)
+    pr, ldr = _arg(residual, (M, K), f32, "residual", dev)
+    pg, _ = _arg(gamma, (K,), f32, "gamma", dev)
+    if S is None and residual is not None:
+        S = _new((M, K), f32, X, stream)
+    Q = _new((M, K), u8, X, stream) if Q is None else _bytes(Q)
+    E = _new((M, -(-K // 32)), u8, X, stream) if E is None else _bytes(E)
+    ps, lds = _arg(S, (M, K), f32, "S", dev)
+    pq, ldq = _arg(Q, (M, K), u8, "Q", dev)
+    pe, lde = _arg(E, (M, -(-K // 32)), u8, "E", dev)
+    _check(load().rmsnorm_mx8(M, K, px, ldx, pr, ldr, pg, float(eps), ps, lds, pq, ldq, pe, lde,
+                              _stream(stream)), "rmsnorm_mx8")
+    return Q, E, X if S is None else S
+
+
+def rmsnorm_f32_bwd_ws_size(M, K):
+    """Bytes of workspace rmsnorm_f32_bwd needs for dgamma."""
+    return _ws_size("rmsnorm_f32_bwd_ws_size", M, K)
+
+
+def rmsnorm_f32_bwd(dY, S, gamma, rstd, dS=None, dX=None, dgamma=None, want=("dX", "dgamma"),
+                    accumulate=False, workspace=None, stream=None):
+    """Gradients (dX, dgamma) of rmsnorm_f32 from dY (M x K), with the S and
+    rstd that it returned; dX is the gradient of X and of the residual alike.
+    dS: the gradient that reaches S past the norm; dX may be dS itself.
+    Gradients not named in `want` are returned as None.  accumulate: dgamma,
+    which must then be given, is added to."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    M, K = _matrix(dY, "dY")
+    wx, wg = "dX" in want, "dgamma" in want
+    if accumulate and wg and dgamma is None:
+        raise ValueError("accumulate needs the gradient to add to")
+    pd, lddy = _arg(dY, (M, K), f32, "dY", dev)
+    ps, lds = _arg(S, (M, K), f32, "S", dev)
+    pg, _ = _arg(gamma, (K,), f32, "gamma", dev)
+    pt, _ = _arg(rstd, (M,), f32, "rstd", dev)
+    pds, ldds = _arg(dS, (M, K), f32, "dS", dev)
+    dX = None if not wx else _new((M, K), f32, dY, stream) if dX is None else dX
+    dgamma = None if not wg else _new((K,), f32, dY, stream) if dgamma is None else dgamma
+    pdx, lddx = _arg(dX, (M, K), f32, "dX", dev)
+    pdg, _ = _arg(dgamma, (K,), f32, "dgamma", dev)
+    need = _ws_size("rmsnorm_f32_bwd_ws_size", M, K) if wg else 0
+    keep, pws, nws = _workspace(workspace, need, dev, dY, stream)
+    _check(load().rmsnorm_f32_bwd(int(bool(accumulate)), M, K, pd, lddy, ps, lds, pg, pt, pds,
+                                  ldds, pdx, lddx, pdg, pws, nws, _stream(stream)),
+           "rmsnorm_f32_bwd")
+    return dX, dgamma
+
+
+def _packed_linear(name, bits, X8, XE, Q, S, bias, act, residual, Y, Y8, YE, out, stream):
+    torch = _torch()
+    f32, u8, dev = torch.float32, torch.uint8, torch.cuda.current_device()
+    if out not in ("f32", "mx8", "both"):
+        raise ValueError("out must be f32, mx8 or both")
+    X8, XE = _bytes(X8), _bytes(XE)
+    M, K = _matrix(X8, "X8")
+    N = _matrix(Q, "Q")[0]
+    if S.dtype is torch.int16:
+        S = S.view(torch.float16)
+    px, ldx = _arg(X8, (M, K), u8, "X8", dev)
+    pe, ldxe = _arg(XE, (M, -(-K // 32)), u8, "XE", dev)
+    # codes and scales may be wider than K needs
+    pq, ldq = _arg(Q[:, :-(-K * bits // 8)], (N, -(-K * bits // 8)), u8, "Q", dev)
+    ps, lds = _arg(S[:, :-(-K // 64)], (N, -(-K // 64)), torch.float16, "S", dev)
+    pb, _ = _arg(bias, (N,), f32, "bias", dev)
+    pr, ldr = _arg(residual, (M, N), f32, "residual", dev)
+    Y = None if out == "mx8" else _new((M, N), f32, X8, stream) if Y is None else Y
+    if out == "f32":
+        Y8 = YE = None
+    else:
+        Y8 = _new((M, N), u8, X8, stream) if Y8 is None else _bytes(Y8)
+        YE = _new((M, -(-N // 32)), u8, X8, stream) if YE is None else _bytes(YE)
+    py, ldy = _arg(Y, (M, N), f32, "Y", dev)
+    p8, ldy8 = _arg(Y8, (M, N), u8, "Y8", dev)
+    pye, ldye = _arg(YE, (M, -(-N // 32)), u8, "YE", dev)
+    _check(getattr(load(), name)(_activation(act), M, N, K, px, ldx, pe, ldxe, pq, ldq, ps, lds,
+                                 pb, pr, ldr, py, ldy, p8, ldy8, pye, ldye, _stream(stream)), name)
+    return Y if out == "f32" else (Y8, YE) if out == "mx8" else (Y, Y8, YE)
+
+
+def linear_q2_mx8(X8, XE, Q, S, bias=None, act="none", residual=None, Y=None, Y8=None, YE=None,
+                  out="f32", stream=None):
+    """Y = act(X.W^T + bias) + residual with X in 8 bits (X8 (M x K), XE (M x
+    ceil(K/32)), as rmsnorm_mx8 returns them) and W (N x K) as gemv_q2's codes
+    Q (N x >= ceil(K/4)) and scales S (N x >= ceil(K/64)).  out: "f32" returns Y,
+    "mx8" the result in 8 bits (Y8, YE) for a following layer, "both" (Y, Y8,
+    YE).  Y may be the residual itself."""
+    return _packed_linear("linear_q2_mx8", 2, X8, XE, Q, S, bias, act, residual, Y, Y8, YE, out,
+                          stream)
+
+
+def linear_q4_mx8(X8, XE, Q, S, bias=None, act="none", residual=None, Y=None, Y8=None, YE=None,
+                  out="f32", stream=None):
+    """As linear_q2_mx8 for gemv_q4's codes, Q (N x >= ceil(K/2))."""
+    return _packed_linear("linear_q4_mx8", 4, X8, XE, Q, S, bias, act, residual, Y, Y8, YE, out,
+                          stream)

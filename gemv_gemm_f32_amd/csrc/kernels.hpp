@@ -94,4 +94,75 @@ hipError_t launch_gemv_q4(int count, int M, int K, const uint8_t *const *Q, int6
                           const uint16_t *const *S, int64_t lds, const float *const *x,
                           float *const *y, hipStream_t stream);
 
+// Y = act(X.op(W) + bias) + R, fp32; op(W) = W^T with W stored N x K when
+// trans_w, else W stored K x N.  Z (may be NULL) receives the pre-activation.
+hipError_t launch_linear(bool trans_w, int act, int M, int N, int K, const float *X, int64_t ldx,
+                         const float *W, int64_t ldw, const float *bias, const float *R,
+                         int64_t ldr, float *Z, int64_t ldz, float *Y, int64_t ldy, int num_cus,
+                         hipStream_t stream);
+
+// Its gradients; each of dX, dW and db may be NULL.  ws holds
+// linear_bwd_workspace_floats floats.
+hipError_t launch_linear_bwd(bool trans_w, int act, bool accumulate, int M, int N, int K,
+                             const float *dY, int64_t lddy, const float *Z, int64_t ldz,
+                             const float *X, int64_t ldx, const float *W, int64_t ldw, float *dX,
+                             int64_t lddx, float *dW, int64_t lddw, float *db, float *ws,
+                             int num_cus, hipStream_t stream);
+// Row stride of dZ in the workspace, and the rows of one chunk of column
+// sums: at most 64 chunks, of a multiple of 16 rows.
+inline int64_t dz_stride(int64_t N) { return (N + 3) & ~int64_t(3); }
+inline int dz_chunk(int M) { return (int)((((int64_t)M + 63) / 64 + 15) & ~int64_t(15)); }
+inline unsigned __int128 linear_bwd_workspace_floats(bool identity, int64_t M, int64_t N) {
+    return (identity ? 0 : (unsigned __int128)M * dz_stride(N)) + (unsigned __int128)64 * N;
+}
+
+// out[c] = (accumulate ? out[c] : 0) + the n partial sums of column c < N.
+hipError_t launch_column_sum(int n, int N, const float *partial, bool accumulate, float *out,
+                             hipStream_t stream);
+
+// S = X + R (R may be NULL); y = S * rstd * gamma with rstd = 1 / sqrt(mean
+// of S^2 over the row + eps), as fp32 in Y or as e4m3 bytes in Q with e8m0
+// bytes in E (mx8.hpp).  S, gamma and rstd may be NULL; S may be X or R.
+struct RmsNorm {
+    int M, K;
+    const float *X, *R, *gamma;
+    float *S, *Y, *rstd;
+    uint8_t *Q, *E;
+    int64_t ldx, ldr, lds, ldy, ldq, lde;
+    float eps;
+};
+hipError_t launch_rmsnorm(const RmsNorm &a, int num_cus, hipStream_t stream);
+
+// dX = rstd * (gamma * dY - xhat * mean(gamma * dY * xhat)) + dS with xhat =
+// S * rstd, and dgamma = sum over rows of dY * xhat.  gamma, dS, dX and
+// dgamma may be NULL; dX may be dS.  ws holds rmsnorm_bwd_workspace_floats
+// floats where dgamma is wanted.
+struct RmsNormBwd {
+    int M, K;
+    const float *dY, *S, *gamma, *rstd, *dS;
+    float *dX, *dgamma, *ws;
+    int64_t lddy, lds, ldds, lddx;
+    bool accumulate;
+};
+hipError_t launch_rmsnorm_bwd(const RmsNormBwd &a, hipStream_t stream);
+// Partial sums of dgamma: one row of K per workgroup.
+constexpr int RMSNORM_BWD_GROUPS = 512;
+inline int64_t rmsnorm_bwd_workspace_floats(int64_t M, int64_t K) {
+    return (M < RMSNORM_BWD_GROUPS ? M : RMSNORM_BWD_GROUPS) * K;
+}
+
+// Y = act(X8.W^T + bias) + R with X8 in 8 bits (mx8.hpp) and W (N x K) as
+// 2-bit or 4-bit codes with one binary16 scale per 64 columns; to fp32 Y, or
+// to 8 bits (Y8, YE), or both.
+struct PackedLinear {
+    int act, M, N, K;
+    const uint8_t *X, *XE, *Q;
+    const uint16_t *S;
+    const float *bias, *R;
+    float *Y;
+    uint8_t *Y8, *YE;
+    int64_t ldx, ldxe, ldq, lds, ldr, ldy, ldy8, ldye;
+};
+hipError_t launch_packed_linear(int bits, const PackedLinear &a, int num_cus, hipStream_t stream);
+
 }  // namespace gg

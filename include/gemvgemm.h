@@ -70,6 +70,17 @@ enum gg_status {
                                 than the fixed scratch buffer holds           */
 };
 
+/* Activations of the dense layers.  GELU_TANH is 0.5 z (1 + tanh(sqrt(2/pi)
+ * (z + 0.044715 z^3))), GELU_ERF is 0.5 z (1 + erf(z / sqrt(2))), SILU is
+ * z / (1 + exp(-z)).  ReLU's derivative at 0 is 0. */
+enum gg_act {
+    GG_ACT_NONE = 0,
+    GG_ACT_RELU = 1,
+    GG_ACT_GELU_TANH = 2,
+    GG_ACT_GELU_ERF = 3,
+    GG_ACT_SILU = 4
+};
+
 /*
  * C[M x N] = A[M x K] . B[K x N]
  *
@@ -302,6 +313,148 @@ int gemv_q4_batched(int64_t count, int64_t M, int64_t K,
                     const uint8_t *const *Q, int64_t ldq,
                     const uint16_t *const *S, int64_t lds,
                     const float *const *x, float *const *y, gg_stream_t stream);
+
+/*
+ * Dense layer: Y[M x N] = act(Z) + R with Z = X . op(W) + bias, fp32.
+ *
+ * A product with what surrounds it in a transformer block ("I built a GPT-2
+ * in the browser, then made it 2.6x-12.1x faster", section "The architecture
+ * in 60 seconds"): bias, activation and residual are applied to the sums
+ * before they are stored.
+ *   op(W) = W (stored K x N, ldw >= N)    if trans_w == 0,
+ *           W^T (stored N x K, ldw >= K)  if trans_w == 1.
+ *   act: one of enum gg_act.  bias (N floats), R (ldr >= N) and Z (ldz >= N)
+ *   may each be NULL: no bias, no residual, pre-activations not kept; the
+ *   leading dimension of an absent operand is ignored.  linear_f32_bwd needs
+ *   Z for every activation but GG_ACT_NONE.
+ * Y may be R itself (same pointer and leading dimension): the residual is
+ * then updated in place.  Any other overlap of Y or Z with an input or with
+ * each other gives GG_ERR_ALIAS.  With K = 0, Z is the bias.
+ * Accuracy: Z as gemm_f32's result plus one rounding for the bias; the
+ * activation adds at most 2^-19 |z|, the residual one rounding.  Non-finite inputs
+ * follow IEEE arithmetic through the formulas above; an activation of minus
+ * infinity is NaN except for ReLU's 0.
+ */
+int linear_f32(int trans_w, int act, int64_t M, int64_t N, int64_t K,
+               const float *X, int64_t ldx, const float *W, int64_t ldw,
+               const float *bias, const float *R, int64_t ldr,
+               float *Z, int64_t ldz, float *Y, int64_t ldy, gg_stream_t stream);
+
+/*
+ * Gradients of linear_f32 from dY[M x N], with dZ = dY * act'(Z):
+ *   dX[M x K] = dZ . op(W)^T        (overwritten)
+ *   dW = X^T . dZ (K x N), or dZ^T . X (N x K) if trans_w == 1
+ *   db[N] = sum of dZ's rows
+ *   accumulate == 1: dW and db are added to what they hold (gradients of
+ *   several micro-batches); 0: overwritten.  Other values are invalid.
+ * R's gradient is dY itself and is not copied.  dX, dW and db may each be
+ * NULL (not wanted); W is read only for dX and X only for dW, and either may
+ * be NULL otherwise.  Z may be NULL for GG_ACT_NONE and is not read then.
+ *   workspace: DEVICE memory of at least linear_f32_bwd_ws_size(act, M, N)
+ *   bytes, 16-byte aligned, disjoint from every other operand; NULL if that
+ *   size is 0.  Its contents on entry do not matter and on return are
+ *   unspecified; it must not be used by other work until this call's work on
+ *   `stream` has finished.  Calls on different streams need different
+ *   workspaces, and so do graphs that may run at the same time.
+ * dX, dW, db and the workspace must be disjoint from each other and from
+ * every input.  GG_ERR_LAUNCH may leave the call's earlier launches queued.
+ * Sums are fp32 in a fixed order: results are reproducible bit for bit.
+ */
+int linear_f32_bwd(int trans_w, int act, int accumulate, int64_t M, int64_t N, int64_t K,
+                   const float *dY, int64_t lddy, const float *Z, int64_t ldz,
+                   const float *X, int64_t ldx, const float *W, int64_t ldw,
+                   float *dX, int64_t lddx, float *dW, int64_t lddw, float *db,
+                   void *workspace, int64_t workspace_bytes, gg_stream_t stream);
+
+/*
+ * Bytes of workspace linear_f32_bwd needs, or GG_ERR_INVALID_ARG for an
+ * unknown activation, a negative or oversized size, or a result past 2^62.
+ */
+int64_t linear_f32_bwd_ws_size(int act, int64_t M, int64_t N);
+
+/*
+ * Root-mean-square norm of the rows of S = X + R:
+ *   rstd_i = 1 / sqrt((1/K) sum_k S_ik^2 + eps),  Y_ik = S_ik rstd_i gamma_k
+ *   X, R, S, Y: M x K with leading dimensions >= K;  gamma: K floats;
+ *   rstd: M floats.  R may be NULL (S = X), gamma may be NULL (ones), S and
+ *   rstd may be NULL (not kept; rmsnorm_f32_bwd takes both).  eps: finite
+ *   and not negative.
+ * S may be X itself or R itself (same pointer and leading dimension), which
+ * updates a residual stream in place; any other overlap of an output with an
+ * input or another output gives GG_ERR_ALIAS.  K = 0 writes nothing.
+ * Squares and their sum are fp32: a row whose mean square leaves fp32's
+ * range gives rstd = 0.  A row of zeros with eps = 0 gives NaN; a NaN or an
+ * infinity makes its own row's rstd NaN or 0, and no other row's.
+ */
+int rmsnorm_f32(int64_t M, int64_t K, const float *X, int64_t ldx, const float *R, int64_t ldr,
+                const float *gamma, float eps, float *S, int64_t lds, float *Y, int64_t ldy,
+                float *rstd, gg_stream_t stream);
+
+/*
+ * The same norm with Y in 8 bits, as the packed layers below take it:
+ *   Y_ik is stored as e4m3(Q[i*ldq + k]) * 2^(E[i*lde + k/32] - 127)
+ *   Q: ldq >= K bytes per row;  E: lde >= ceil(K/32) bytes per row.
+ * E holds, per block of 32 columns, the smallest power of two (at least
+ * 2^-126) that keeps the block's largest |Y| within 448, the largest e4m3
+ * value; Y is rounded once, to the nearest e4m3 value (ties to even).  A
+ * block that holds a NaN or an infinity gets E = 255 and bytes 0x7f (both
+ * NaN).  Bytes of Q past column K are not written.
+ */
+int rmsnorm_mx8(int64_t M, int64_t K, const float *X, int64_t ldx, const float *R, int64_t ldr,
+                const float *gamma, float eps, float *S, int64_t lds,
+                uint8_t *Q, int64_t ldq, uint8_t *E, int64_t lde, gg_stream_t stream);
+
+/*
+ * Gradients of rmsnorm_f32 from dY[M x K], with xhat = S * rstd:
+ *   dX = rstd * (gamma dY - xhat * (1/K) sum_k gamma_k dY_ik xhat_ik) + dS
+ *   dgamma[K] = sum over rows of dY * xhat
+ * dX is the gradient of X and of R alike; dS[M x K] is the gradient that
+ * reaches S past the norm (the residual stream's), NULL for none, and dX may
+ * be dS itself (same pointer and leading dimension).  S and rstd are those
+ * that the norm kept; gamma as there.  dX and dgamma may each be NULL (not
+ * wanted).  accumulate == 1: dgamma is added to what it holds.
+ *   workspace: at least rmsnorm_f32_bwd_ws_size(M, K) bytes, 16-byte
+ *   aligned, as for linear_f32_bwd; needed only where dgamma is wanted.
+ */
+int rmsnorm_f32_bwd(int accumulate, int64_t M, int64_t K, const float *dY, int64_t lddy,
+                    const float *S, int64_t lds, const float *gamma, const float *rstd,
+                    const float *dS, int64_t ldds, float *dX, int64_t lddx, float *dgamma,
+                    void *workspace, int64_t workspace_bytes, gg_stream_t stream);
+
+/* Bytes of workspace rmsnorm_f32_bwd needs for dgamma, or
+ * GG_ERR_INVALID_ARG for a negative or oversized size. */
+int64_t rmsnorm_f32_bwd_ws_size(int64_t M, int64_t K);
+
+/*
+ * Dense layer on packed weights and 8-bit rows:
+ *   Y[M x N] = act(X . W^T + bias) + R
+ * W (N x K) is held as gemv_q2 / gemv_q4 hold it (codes Q with ldq, binary16
+ * scales S with lds, one per 64 columns); X (M x K) as rmsnorm_mx8 writes it
+ * (e4m3 bytes X8 with ldx >= K, powers of two XE with ldxe >= ceil(K/32)).
+ * One row of X is a token, more are a prompt's or a batch's.
+ *   act, bias and R (fp32, ldr >= N) as in linear_f32.  The result goes to Y
+ *   (fp32, ldy >= N), or in 8 bits to Y8 (ldy8 >= N) and YE (ldye >=
+ *   ceil(N/32)) for a following packed layer, or to both; Y8 and YE come
+ *   together.  The leading dimension of an absent operand is ignored.
+ * Y may be R itself (same pointer and leading dimension); any other overlap
+ * of an output with an input or another output gives GG_ERR_ALIAS.
+ * Bits of codes for columns past K, scales past ceil(K/64) and bytes of X8
+ * and XE past the row are never used.  Accuracy of the sums (before act and
+ * R) as gemv_q4's, relative to sum_k |w(n,k) x(i,k)|: codes and 8-bit values
+ * enter exactly, sums are fp32.  A NaN in a row of X makes that row of Y
+ * NaN, a NaN scale its own column.
+ */
+int linear_q4_mx8(int act, int64_t M, int64_t N, int64_t K,
+                  const uint8_t *X8, int64_t ldx, const uint8_t *XE, int64_t ldxe,
+                  const uint8_t *Q, int64_t ldq, const uint16_t *S, int64_t lds,
+                  const float *bias, const float *R, int64_t ldr, float *Y, int64_t ldy,
+                  uint8_t *Y8, int64_t ldy8, uint8_t *YE, int64_t ldye, gg_stream_t stream);
+
+int linear_q2_mx8(int act, int64_t M, int64_t N, int64_t K,
+                  const uint8_t *X8, int64_t ldx, const uint8_t *XE, int64_t ldxe,
+                  const uint8_t *Q, int64_t ldq, const uint16_t *S, int64_t lds,
+                  const float *bias, const float *R, int64_t ldr, float *Y, int64_t ldy,
+                  uint8_t *Y8, int64_t ldy8, uint8_t *YE, int64_t ldye, gg_stream_t stream);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *gg_strerror(int status);
