@@ -143,7 +143,9 @@ def _torch():
 def _stream(stream):
     torch = _torch()
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a Stream object takes longer than the
+        # rest of a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -427,7 +429,7 @@ def _new(shape, dtype, like, stream):
     memory is neither taken from nor given back to work of another stream."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):

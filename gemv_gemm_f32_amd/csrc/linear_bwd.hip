@@ -87,21 +87,34 @@ __global__ __launch_bounds__(256) void dz_kernel(int act, int M, int N, int chun
     }
 }
 
-// out[c] = (accumulate ? out[c] : 0) + sum over n of partial[n][c], n in
-// order within each of 4 interleaved runs, then the runs in order.
-__global__ __launch_bounds__(256) void column_sum_kernel(int n, int N, const float *partial,
-                                                         int accumulate, float *out) {
-    __shared__ float red[4][64];
+// out[c] = (accumulate ? out[c] : 0) + sum over i of partial[i][c]: 16
+// interleaved runs of rows per column, each added in order with 8 loads in
+// flight, then the runs in order.
+constexpr int RUNS = 16, INFLIGHT = 8;
+
+__global__ __launch_bounds__(64 * RUNS) void column_sum_kernel(int n, int N, const float *partial,
+                                                               int accumulate, float *out) {
+    __shared__ float red[RUNS][64];
     const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
     for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < N; c0 += (int64_t)gridDim.x * 64) {
         const int64_t col = c0 + tx;
         float sum = 0.f;
-        if (col < N)
-            for (int i = ty; i < n; i += 4) sum += partial[(int64_t)i * N + col];
+        if (col < N) {
+            const float *p = partial + col;
+            for (int i = ty; i < n; i += RUNS * INFLIGHT) {
+                float v[INFLIGHT];
+#pragma unroll
+                for (int u = 0; u < INFLIGHT; ++u)
+                    v[u] = i + RUNS * u < n ? p[(int64_t)(i + RUNS * u) * N] : 0.f;
+#pragma unroll
+                for (int u = 0; u < INFLIGHT; ++u) sum += v[u];
+            }
+        }
         red[ty][tx] = sum;
         __syncthreads();
         if (ty == 0 && col < N) {
-            sum = ((red[0][tx] + red[1][tx]) + red[2][tx]) + red[3][tx];
+#pragma unroll
+            for (int y = 1; y < RUNS; ++y) sum += red[y][tx];
             out[col] = accumulate ? out[col] + sum : sum;
         }
         __syncthreads();
@@ -117,7 +130,7 @@ inline unsigned blocks(int64_t n, int64_t per, int64_t most) {
 
 hipError_t launch_column_sum(int n, int N, const float *partial, bool accumulate, float *out,
                              hipStream_t s) {
-    return launch(column_sum_kernel, dim3(blocks(N, 64, 1 << 20)), dim3(256), s, n, N, partial,
+    return launch(column_sum_kernel, dim3(blocks(N, 64, 1 << 20)), dim3(64 * RUNS), s, n, N, partial,
                   accumulate ? 1 : 0, out);
 }
 
