@@ -26,6 +26,7 @@
 // k may be taken in any order as long as both operands agree.
 #include <hip/hip_runtime.h>
 
+#include <stdlib.h>
 #include <type_traits>
 
 #include "activation.hpp"
@@ -49,14 +50,16 @@ __device__ __forceinline__ unsigned perm(unsigned hi, unsigned lo, unsigned sel)
 #endif
 }
 
-// Four 4-bit codes, one per byte, as the e4m3 bytes of 15 - 2 code: the
-// magnitudes 1, 3, ..., 15 are looked up at code mod 8 (upper codes) or its
-// complement, bit 3 becomes the sign.  The caller's scale is negative.
-__device__ __forceinline__ unsigned e4m3_of_4bit(unsigned c) {
-    const unsigned up = c & 0x08080808u;
-    const unsigned seven = up - (up >> 3);              // 7 in bytes of codes >= 8
-    const unsigned idx = (c ^ ~seven) & 0x07070707u;
-    return perm(0x57555351u, 0x4E4A4438u, idx) | up << 4;
+// Eight 4-bit codes as the e4m3 bytes of 15 - 2 code, even nibbles in lo, odd
+// ones in hi.  The magnitudes 1, 3, ..., 15 are looked up at code mod 8 (upper
+// codes) or its complement, bit 3 becomes the sign; both are found for all
+// eight nibbles at once.  The caller's scale is negative.
+__device__ __forceinline__ void e4m3_of_4bit(unsigned w, unsigned &lo, unsigned &hi) {
+    const unsigned up = w & 0x88888888u;
+    const unsigned seven = up - (up >> 3);              // 7 in nibbles of codes >= 8
+    const unsigned idx = (w ^ ~seven) & 0x77777777u;
+    lo = perm(0x57555351u, 0x4E4A4438u, idx & 0x07070707u) | (up << 4 & 0x80808080u);
+    hi = perm(0x57555351u, 0x4E4A4438u, idx >> 4 & 0x07070707u) | (up & 0x80808080u);
 }
 
 // Four 2-bit codes, one per byte, as the e4m3 bytes of 2 code - 3.
@@ -67,41 +70,26 @@ __device__ __forceinline__ unsigned e4m3_of_2bit(unsigned c) {
 template <int BITS>
 constexpr float code_scale() { return BITS == 4 ? -0.5f : 0.5f; }
 
-// Half-wave h has loaded the 32 codes of block h (BITS dwords); afterwards it
-// has the h-th 16 of block 0 in the lower dwords and of block 1 in the upper.
+// 16 codes (BITS / 2 dwords) as four registers of a matrix operand.
 template <int BITS>
-__device__ __forceinline__ void deal(unsigned (&w)[BITS]) {
-#if defined(__HIP_DEVICE_COMPILE__)
-#pragma unroll
-    for (int i = 0; i < BITS / 2; ++i) {
-        const auto p = __builtin_amdgcn_permlane32_swap(w[i], w[i + BITS / 2], false, false);
-        w[i] = p[0];
-        w[i + BITS / 2] = p[1];
-    }
-#endif
-}
-
-// The 32 codes of one lane (BITS dwords) as a matrix operand.
-template <int BITS>
-__device__ __forceinline__ v8i expand(const unsigned (&w)[BITS]) {
-    v8i o;
+__device__ __forceinline__ v4u expand16(const unsigned *w) {
+    v4u o;
     if constexpr (BITS == 4) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            o[2 * j] = (int)e4m3_of_4bit(w[j] & 0x0F0F0F0Fu);
-            o[2 * j + 1] = (int)e4m3_of_4bit(w[j] >> 4 & 0x0F0F0F0Fu);
+        for (int j = 0; j < 2; ++j) {
+            unsigned lo, hi;
+            e4m3_of_4bit(w[j], lo, hi);
+            o[2 * j] = lo;
+            o[2 * j + 1] = hi;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[4 * j + i] = (int)e4m3_of_2bit(w[j] >> (2 * i) & 0x03030303u);
+        for (int i = 0; i < 4; ++i) o[i] = e4m3_of_2bit(w[0] >> (2 * i) & 0x03030303u);
     }
     return o;
 }
 
-// 16 bytes of x in the order of expand's codes.
+// 16 bytes of x in the order of expand16's codes.
 template <int BITS>
 __device__ __forceinline__ v4u shuffle16(const v4u &d) {
     if constexpr (BITS == 4)
@@ -113,10 +101,7 @@ __device__ __forceinline__ v4u shuffle16(const v4u &d) {
                perm(b1, a1, 0x05040100u), perm(b1, a1, 0x07060302u)};
 }
 
-template <int BITS>
-__device__ __forceinline__ v8i shuffle(const unsigned (&x)[8]) {
-    const v4u lo = shuffle16<BITS>(v4u{x[0], x[1], x[2], x[3]});
-    const v4u hi = shuffle16<BITS>(v4u{x[4], x[5], x[6], x[7]});
+__device__ __forceinline__ v8i join(const v4u &lo, const v4u &hi) {
     return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
@@ -127,6 +112,18 @@ __device__ __forceinline__ v16f mfma(const v8i &a, const v8i &b, int scale_a) {
     const v16f zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #if defined(__HIP_DEVICE_COMPILE__)
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, zero, 0, 0, SEL, scale_a, 0, 127);
+#else
+    return zero;
+#endif
+}
+
+// The same over 128 columns, two weight groups (registers 0-3: the first
+// group, 4-7: the second; block b of 32 takes its power from lanes 16b ..
+// 16b + 15), for 16 rows of x by 16 rows of W.
+__device__ __forceinline__ v4f mfma16(const v8i &a, const v8i &b, int scale_a) {
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, scale_a, 0, 127);
 #else
     return zero;
 #endif
@@ -145,13 +142,32 @@ __device__ __forceinline__ void load_bytes(unsigned (&d)[N / 4], const uint8_t *
     }
 }
 
-// What a finished sum becomes.  All 64 lanes call it together: the half-wave
-// shares a token, its lanes are 32 neighbouring columns n.
-__device__ __forceinline__ float finish(const PackedLinear &a, float sum, int64_t tok, int n,
-                                        float bias, bool live) {
-    float y = 0.f;
-    with_act(a.act, [&](auto t) { y = act_value<decltype(t)::value>(sum + bias); });
-    if (a.R && live) y += a.R[tok * a.ldr + n];
+// 32 codes in one load of 16 (2-bit codes: 8) bytes.
+template <int BITS>
+__device__ __forceinline__ void load_codes(unsigned (&w)[BITS], const uint8_t *p) {
+    if constexpr (BITS == 4) {
+        const v4u q = *reinterpret_cast<const v4u *>(p);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) w[d] = q[d];
+    } else {
+        const v2u q = *reinterpret_cast<const v2u *>(p);
+        w[0] = q[0];
+        w[1] = q[1];
+    }
+}
+
+// What the finished sum of (tok, n) becomes.  For an output in 8 bits the 32
+// lanes of a half-wave call together, on 32 neighbouring columns of a token
+// (`live`: whether the cell exists).
+__device__ __forceinline__ void finish(const PackedLinear &a, float sum, int64_t tok, int64_t n,
+                                       bool live) {
+    float y = 0.f, res = 0.f;
+    if (live) {
+        if (a.bias) sum += a.bias[n];
+        if (a.R) res = a.R[tok * a.ldr + n];
+    }
+    with_act(a.act, [&](auto t) { y = act_value<decltype(t)::value>(sum); });
+    if (a.R) y += res;
     if (a.Y && live) a.Y[tok * a.ldy + n] = y;
     if (a.Y8) {
         const int e = mx8_exponent(half32_max(live ? mag(y) : 0u));
@@ -160,12 +176,11 @@ __device__ __forceinline__ float finish(const PackedLinear &a, float sum, int64_
             if (n % 32 == 0) a.YE[tok * a.ldye + n / 32] = (uint8_t)e;
         }
     }
-    return y;
 }
 
-// The same for a BM x BN tile of sums at (m0, n0) that the 256 threads read
+// The same for a BM x BN tile of sums at (m0, n0) that THREADS threads read
 // back 4 columns at a time: at(row, col) gives 4 sums.
-template <int BM, int BN, class At>
+template <int BM, int BN, int THREADS, class At>
 __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, int64_t n0, int tid,
                                             At at) {
     constexpr int PER_ROW = BN / 4;                    // threads along a row
@@ -184,7 +199,7 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
         for (int c = 0; c < 4; ++c)
             if (c < live) bias[c] = a.bias[n + c];
     with_act(a.act, [&](auto act) {
-        constexpr int ROWS = 256 / PER_ROW;            // rows at a time
+        constexpr int ROWS = THREADS / PER_ROW;            // rows at a time
 #pragma unroll 4
         for (int i = 0; i < BM / ROWS; ++i) {
             const int row = tid / PER_ROW + ROWS * i;
@@ -237,96 +252,150 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
     });
 }
 
-// Up to 32 rows: a workgroup owns 32 columns n, its KS waves
-// share the weight groups in runs of RUN, and their sums meet in LDS, added
-// in wave order.  WIDE: x and codes are loaded 16 (2-bit codes: 8) bytes at
-// a time; else, and in a last group that K cuts short, byte by byte.
-constexpr int KS = 8, RUN = 4;
-
-template <int BITS, bool WIDE>
-__global__ __launch_bounds__(64 * KS) void packed_rows_kernel(PackedLinear a) {
-    __shared__ float red[KS][16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, l32 = lane & 31;
-    constexpr int64_t m0 = 0;
-    const int n0 = blockIdx.x * 32;
-    const int64_t tok = min(m0 + l32, (int64_t)a.M - 1);
-    const int64_t nrow = min(n0 + l32, a.N - 1);
-    const uint8_t *px = a.X + tok * a.ldx, *pe = a.XE + tok * a.ldxe;
-    const uint8_t *pq = a.Q + nrow * a.ldq;
-    const uint16_t *ps = a.S + nrow * a.lds;
-    const int groups = (int)(((int64_t)a.K + 63) / 64);
-    constexpr int CB = 4 * BITS;                      // bytes of 32 codes
-
-    v16f acc;
+// Up to 16 rows: bound by the codes' way from memory, with one row of x by
+// its latency.  No LDS on the way in: a lane loads 32 neighbouring codes of
+// its row of W and expands them in registers.  The 16 x 16 x 128 instruction
+// takes two weight groups, whose scales differ, so it runs once per group with
+// the other group's half of x zero; at 16 rows that costs the same time per
+// weight as 32 x 32 x 64 would, half the multiply-adds, and twice the
+// workgroups.
+//
+// A workgroup owns 16 NH columns n (NH = 2 for an output in 8 bits, whose
+// blocks are 32 wide); its waves split into NH column sets by KW runs of
+// groups, and the runs' sums meet in LDS, added in order.  WIDE: 16 bytes of
+// x, 32 codes and both scales in one load each; else, and where K cuts a
+// group short, byte by byte.
+// Lanes 16q .. 16q + 15 have loaded codes 32q .. 32q + 31 of a pair of
+// groups; afterwards they have codes 16q .. 16q + 15 of the first group in the
+// lower dwords and of the second in the upper.
+template <int BITS>
+__device__ __forceinline__ void deal(unsigned (&w)[BITS]) {
+#if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-    for (int g0 = wave * RUN; g0 < groups; g0 += KS * RUN) {
-        unsigned w[RUN][BITS], x[RUN][8];
-        int e[RUN];
-        float s[RUN];
-#pragma unroll
-        for (int i = 0; i < RUN; ++i) {
-            const int g = min(g0 + i, groups - 1);
-            const int k = 64 * g + 32 * h;            // the codes this lane loads
-            const int have = min(max(a.K - k, 0), 32);
-            const int kx = 64 * g + 16 * h;           // and its bytes of x: 16 here,
-            const int left = a.K - kx;                // 16 from kx + 32
-            s[i] = g0 + i < groups ? (float)__builtin_bit_cast(_Float16, ps[g]) * code_scale<BITS>() : 0.f;
-            e[i] = have > 0 ? pe[2 * g + h] : 127;
-            if (WIDE && have == 32) {
-                if constexpr (BITS == 4) {
-                    const v4u q = *reinterpret_cast<const v4u *>(pq + (k >> 1));
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) w[i][d] = q[d];
-                } else {
-                    const v2u q = *reinterpret_cast<const v2u *>(pq + (k >> 2));
-                    w[i][0] = q[0];
-                    w[i][1] = q[1];
-                }
-            } else {
-                load_bytes<CB>(w[i], pq + (int64_t)k * BITS / 8, (have * BITS + 7) / 8);
-            }
-            if (WIDE && left >= 48) {
-                const v4u x0 = *reinterpret_cast<const v4u *>(px + kx);
-                const v4u x1 = *reinterpret_cast<const v4u *>(px + kx + 32);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    x[i][d] = x0[d];
-                    x[i][4 + d] = x1[d];
-                }
-            } else {
-                unsigned t[4];
-                load_bytes<16>(t, px + kx, left);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) x[i][d] = t[d];
-                load_bytes<16>(t, px + kx + 32, left - 32);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) x[i][4 + d] = t[d];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < RUN; ++i) {
-            deal<BITS>(w[i]);
-            const v16f p = mfma<0>(shuffle<BITS>(x[i]), expand<BITS>(w[i]), e[i]);
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (g0 + i < groups) acc[r] = __builtin_fmaf(p[r], s[i], acc[r]);
-        }
+    for (int i = 0; i < BITS / 2; ++i) {
+        const auto p = __builtin_amdgcn_permlane16_swap(w[i], w[i + BITS / 2], false, false);
+        const auto o = __builtin_amdgcn_permlane32_swap(p[0], p[1], false, false);
+        w[i] = o[0];
+        w[i + BITS / 2] = o[1];
     }
+#endif
+}
+
+// One pair of groups, as loaded, and its products added to the sums.
+template <int BITS>
+struct Pair {
+    unsigned w[BITS], e, s;          // codes, x's power of two, both scales
+    v4u x[2];
+
+    __device__ __forceinline__ void multiply(v4f &acc) {
+        const v4u none = {0, 0, 0, 0};
+        deal<BITS>(w);
+        const v8i b = join(expand16<BITS>(w), expand16<BITS>(w + BITS / 2));
+        const v4f r0 = mfma16(join(shuffle16<BITS>(x[0]), none), b, (int)e);
+        const v4f r1 = mfma16(join(none, shuffle16<BITS>(x[1])), b, (int)e);
+        const float s0 = (float)__builtin_bit_cast(_Float16, (uint16_t)s);
+        const float s1 = (float)__builtin_bit_cast(_Float16, (uint16_t)(s >> 16));
 #pragma unroll
-    for (int r = 0; r < 16; ++r) red[wave][r][lane] = acc[r];
+        for (int r = 0; r < 4; ++r)
+            acc[r] = __builtin_fmaf(r1[r], s1, __builtin_fmaf(r0[r], s0, acc[r]));
+    }
+};
+
+// A lane's pointers to its rows, at one pair of groups.
+template <int BITS>
+struct Rows {
+    const uint8_t *w, *x, *e;
+    const uint16_t *s;
+
+    __device__ __forceinline__ void advance(int64_t pairs) {
+        w += pairs * (16 * BITS);
+        x += pairs * 128;
+        e += pairs * 4;
+        s += pairs * 2;
+    }
+    // N whole pairs, all loads in flight together
+    template <int N>
+    __device__ __forceinline__ void run(v4f &acc) {
+        Pair<BITS> p[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) load_codes<BITS>(p[i].w, w + i * (16 * BITS));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            p[i].x[0] = *reinterpret_cast<const v4u *>(x + i * 128);
+            p[i].x[1] = *reinterpret_cast<const v4u *>(x + i * 128 + 64);
+            p[i].e = e[4 * i];
+            p[i].s = *reinterpret_cast<const unsigned *>(s + 2 * i);
+        }
+        advance(N);
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i].multiply(acc);
+    }
+    // the pair at hand, of which columns 0 .. left - 1 exist, byte by byte
+    __device__ __forceinline__ void part(int64_t left, int q, v4f &acc) {
+        const auto have = [&](int at, int most) {
+            return (int)min(max(left - at, (int64_t)0), (int64_t)most);
+        };
+        Pair<BITS> p;
+        load_bytes<4 * BITS>(p.w, w, (have(32 * q, 32) * BITS + 7) / 8);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            unsigned d[4];
+            load_bytes<16>(d, x + 64 * g, have(64 * g + 16 * q, 16));
+            p.x[g] = v4u{d[0], d[1], d[2], d[3]};
+        }
+        p.e = left > 32 * q ? *e : 127u;
+        p.s = (unsigned)s[0] | (left > 64 ? (unsigned)s[1] << 16 : 0u);
+        advance(1);
+        p.multiply(acc);
+    }
+};
+
+template <int BITS, int NH, int KW, bool WIDE>
+__global__ __launch_bounds__(64 * NH * KW) void packed_rows_kernel(PackedLinear a) {
+    constexpr int NC = 16 * NH;                       // columns
+    __shared__ float red[KW][16][NC];
+    const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nh = wave % NH, kw = wave / NH;
+    const int64_t n0 = (int64_t)blockIdx.x * NC;
+    const int64_t tok = min(l16, a.M - 1);
+    const int64_t nrow = min(n0 + 16 * nh + l16, (int64_t)a.N - 1);
+    const int64_t pairs = ((int64_t)a.K + 127) / 128;
+    // run kw of KW: as even a share as whole pairs allow
+    const int64_t first = pairs * kw / KW, end = pairs * (kw + 1) / KW;
+    // the pairs of it that exist in full, if they may be loaded as a whole
+    int n = WIDE ? (int)max(min(end, (int64_t)a.K / 128) - first, (int64_t)0) : 0;
+    Rows<BITS> rows = {a.Q + nrow * a.ldq + 4 * BITS * q, a.X + tok * a.ldx + 16 * q,
+                       a.XE + tok * a.ldxe + q, a.S + nrow * a.lds};
+    rows.advance(first);
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    int64_t p = first + n;
+    for (; n >= 4; n -= 4) rows.template run<4>(acc);
+    if (n == 3) rows.template run<3>(acc);
+    else if (n == 2) rows.template run<2>(acc);
+    else if (n == 1) rows.template run<1>(acc);
+#pragma unroll 1
+    for (; p < end; ++p) rows.part(a.K - p * 128, q, acc);
+
+#pragma unroll
+    for (int r = 0; r < 4; ++r) red[kw][4 * q + r][16 * nh + l16] = acc[r];
     __syncthreads();
-    const int n = n0 + l32;
-    const float bias = a.bias && n < a.N ? a.bias[n] : 0.f;
+    const int t = threadIdx.x / NC, col = threadIdx.x % NC;
+#pragma unroll 1
+    for (int m = t; m < a.M; m += 64 * NH * KW / NC) {    // uniform per half-wave where NH = 2
+        float sum = red[0][m][col];
 #pragma unroll
-    for (int i = 0; i < 16 / KS; ++i) {
-        const int r = wave * (16 / KS) + i;
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < KS; ++w) sum += red[w][r][lane];
-        const int64_t t = m0 + 8 * (r >> 2) + 4 * h + (r & 3);
-        finish(a, sum, t, n, bias, t < a.M && n < a.N);
+        for (int w = 1; w < KW; ++w) sum += red[w][m][col];
+        finish(a, sum * code_scale<BITS>(), m, n0 + col, n0 + col < a.N);
     }
+}
+
+template <int BITS, int NH, int KW>
+hipError_t launch_rows(const PackedLinear &a, bool wide, hipStream_t s) {
+    const int64_t nb = ((int64_t)a.N + 16 * NH - 1) / (16 * NH);
+    if (nb * 64 * NH * KW > UINT32_MAX) return hipErrorInvalidValue;
+    return launch(wide ? packed_rows_kernel<BITS, NH, KW, true> : packed_rows_kernel<BITS, NH, KW, false>,
+                  dim3((unsigned)nb), dim3(64 * NH * KW), s, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -338,108 +407,111 @@ __global__ __launch_bounds__(64 * KS) void packed_rows_kernel(PackedLinear a) {
 //  * LDS rows hold 128 bytes, 8 chunks of 16; chunk c of row r lies at slot
 //    c ^ (r mod 8), so that the 16-byte fragment reads of 8 neighbouring
 //    rows, and the writes, meet no bank twice.
-//  * The next step's loads are in flight while this step's fragments are
-//    multiplied; one barrier per step.
+//  * Loads run two steps ahead: registers hold the next step while LDS holds
+//    this one; one barrier per step.
 //  * The finished sums pass through LDS, so that bias, residual and the
 //    stores of Y run along rows, 16 bytes per lane.
-constexpr int BN = 128, STEP = 128;
+constexpr int STEP = 128;
 
-// Chunk `c` (16 bytes) of a row of `n` bytes at p, zeros past its end.
-template <bool WIDE>
+// The 16 bytes at `at` of a row of n bytes, zeros past its end.
 __device__ __forceinline__ v4u load_chunk(const uint8_t *p, int64_t at, int64_t n) {
-    if (WIDE && at + 16 <= n) return *reinterpret_cast<const v4u *>(p + at);
     unsigned d[4];
     load_bytes<16>(d, p + at, (int)min(max(n - at, (int64_t)0), (int64_t)16));
     return v4u{d[0], d[1], d[2], d[3]};
 }
 
-template <int BM, int BITS, bool WIDE>
-__global__ __launch_bounds__(256, 2) void packed_tile_kernel(PackedLinear a, int tiles_m) {
-    constexpr int IB = BM / 64, JB = 2;               // 32 x 32 blocks per wave
-    constexpr int XC = BM * 8 / 256;                  // chunks of x per thread
-    constexpr int CODES = 64 / BITS * 2;              // codes per 16-byte chunk: 32, 64
-    constexpr int WPR = STEP / CODES;                 // code chunks per row and step: 4, 2
-    constexpr int WC = BN * WPR / 256;                // code chunks per thread: 2, 1
+// KS groups of WR x WC waves, each wave with IB x JB blocks of 32 x 32.
+template <int BM, int BN, int WR, int WC, int KS, int BITS, bool WIDE>
+__global__ __launch_bounds__(64 * WR * WC * KS, WR * WC * KS >= 8 ? WR * WC * KS / 4 : 2)
+void packed_tile_kernel(PackedLinear a, int tiles_m) {
+    constexpr int THREADS = 64 * WR * WC;             // of a group
+    constexpr int IB = BM / WR / 32, JB = BN / WC / 32;
+    static_assert(IB * WR * 32 == BM && JB * WC * 32 == BN, "waves must cover the tile");
+    constexpr int XC = BM * 8 / THREADS;              // chunks of x per thread
+    constexpr int CB = 4 * BITS;                      // bytes of 32 codes
+    constexpr int WPR = STEP / 32;                    // units of 32 codes per row and step
+    constexpr int WL = BN * WPR / THREADS;            // units per thread
+    static_assert(XC * THREADS == BM * 8 && WL * THREADS == BN * WPR, "loads must split evenly");
+    static_assert(BM <= THREADS && BN <= THREADS, "one scale per thread");
     constexpr int XBYTES = BM * STEP, WBYTES = BN * STEP, STAGE = XBYTES + WBYTES;
-    constexpr int TILE = BM * BN * 4;                 // the finished sums
-    constexpr int SMEM = 2 * STAGE > TILE ? 2 * STAGE : TILE;
+    constexpr int TILE = BM * BN * 4;                 // a group's finished sums
+    constexpr int SMEM = KS * (2 * STAGE > TILE ? 2 * STAGE : TILE);
     __shared__ __attribute__((aligned(16))) char smem[SMEM];
-    __shared__ unsigned scales[2][BM + BN];           // x: 4 e8m0 bytes, W: 2 halves per step
+    __shared__ unsigned all_scales[KS][2][BM + BN];   // x: 4 e8m0 bytes, W: 2 halves per step
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, l32 = lane & 31;
+    const int grp = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / THREADS);
+    const int tid = threadIdx.x % THREADS, lane = tid & 63, wave = tid >> 6, h = lane >> 5,
+              l32 = lane & 31;
+    char *const gsmem = smem + grp * 2 * STAGE;
+    unsigned(*const scales)[BM + BN] = all_scales[grp];
     int t = blockIdx.x;
     if ((gridDim.x & 7) == 0) t = (t & 7) * (gridDim.x >> 3) + (t >> 3);   // runs per XCD
     const int64_t m0 = (int64_t)(t % tiles_m) * BM;
     const int64_t n0 = (int64_t)(t / tiles_m) * BN;
-    const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * 64;
+    const int wm = wave / WC * (32 * IB), wn = wave % WC * (32 * JB);
 
-    const uint8_t *px[XC], *pw[WC];
+    const uint8_t *px[XC], *pw[WL];
 #pragma unroll
-    for (int i = 0; i < XC; ++i) px[i] = a.X + min(m0 + tid / 8 + 32 * i, (int64_t)a.M - 1) * a.ldx;
+    for (int i = 0; i < XC; ++i) px[i] = a.X + min(m0 + tid / 8 + THREADS / 8 * i, (int64_t)a.M - 1) * a.ldx;
 #pragma unroll
-    for (int i = 0; i < WC; ++i)
-        pw[i] = a.Q + min(n0 + tid / WPR + 256 / WPR * i, (int64_t)a.N - 1) * a.ldq;
+    for (int i = 0; i < WL; ++i)
+        pw[i] = a.Q + min(n0 + tid / WPR + THREADS / WPR * i, (int64_t)a.N - 1) * a.ldq;
     // threads below BM fetch a row's powers of two, the next BN a row's scales
-    const bool fetch_e = tid < BM, fetch_s = tid >= 256 - BN;
+    const bool fetch_e = tid < BM, fetch_s = tid >= THREADS - BN;
     const uint8_t *pe = a.XE + min(m0 + (fetch_e ? tid : 0), (int64_t)a.M - 1) * a.ldxe;
-    const uint16_t *ps = a.S + min(n0 + (fetch_s ? tid - (256 - BN) : 0), (int64_t)a.N - 1) * a.lds;
+    const uint16_t *ps = a.S + min(n0 + (fetch_s ? tid - (THREADS - BN) : 0), (int64_t)a.N - 1) * a.lds;
     const int64_t kb = ((int64_t)a.K * BITS + 7) / 8;
     const int64_t eb = ((int64_t)a.K + 31) / 32, sb = ((int64_t)a.K + 63) / 64;
 
-    v4u xr[XC], wr[WC];
+    v4u xr[XC];
+    unsigned wr[WL][BITS];
     unsigned er = 0, sr = 0;
-    auto load = [&](int64_t k0) {
+    // the step at k0; `full` (uniform): all of its 128 columns exist
+    auto load = [&](int64_t k0, bool full) {
+        const int64_t b = k0 / 32, g = k0 / 64;
+        if (WIDE && full) {
 #pragma unroll
-        for (int i = 0; i < XC; ++i) xr[i] = load_chunk<WIDE>(px[i], k0 + 16 * (tid % 8), a.K);
+            for (int i = 0; i < XC; ++i)
+                xr[i] = *reinterpret_cast<const v4u *>(px[i] + k0 + 16 * (tid % 8));
 #pragma unroll
-        for (int i = 0; i < WC; ++i)
-            wr[i] = load_chunk<WIDE>(pw[i], k0 * BITS / 8 + 16 * (tid % WPR), kb);
-        if (fetch_e) {
-            const int64_t b = k0 / 32;
-            if (WIDE && b + 4 <= eb) {
-                er = *reinterpret_cast<const unsigned *>(pe + b);
-            } else {
-                er = 0;
-                for (int i = 0; i < 4; ++i) er |= (b + i < eb ? (unsigned)pe[b + i] : 127u) << (8 * i);
+            for (int i = 0; i < WL; ++i) load_codes<BITS>(wr[i], pw[i] + k0 * BITS / 8 + CB * (tid % WPR));
+            if (fetch_e) er = *reinterpret_cast<const unsigned *>(pe + b);
+            if (fetch_s) sr = *reinterpret_cast<const unsigned *>(ps + g);
+        } else {
+#pragma unroll
+            for (int i = 0; i < XC; ++i) xr[i] = load_chunk(px[i], k0 + 16 * (tid % 8), a.K);
+#pragma unroll
+            for (int i = 0; i < WL; ++i) {
+                const int64_t at = k0 * BITS / 8 + CB * (tid % WPR);
+                load_bytes<CB>(wr[i], pw[i] + at, (int)min(max(kb - at, (int64_t)0), (int64_t)CB));
             }
-        }
-        if (fetch_s) {
-            const int64_t g = k0 / 64;
-            if (WIDE && g + 2 <= sb) sr = *reinterpret_cast<const unsigned *>(ps + g);
-            else sr = (unsigned)ps[g] | (g + 1 < sb ? (unsigned)ps[g + 1] << 16 : 0u);
+            er = sr = 0;
+            if (fetch_e)
+                for (int i = 0; i < 4; ++i) er |= (b + i < eb ? (unsigned)pe[b + i] : 127u) << (8 * i);
+            if (fetch_s) sr = (unsigned)ps[g] | (g + 1 < sb ? (unsigned)ps[g + 1] << 16 : 0u);
         }
     };
     auto slot = [](int row, int c) { return row * STEP + ((c ^ (row & 7)) * 16); };
     auto store = [&](int buf) {
-        char *xs = smem + buf * STAGE, *ws = xs + XBYTES;
+        char *xs = gsmem + buf * STAGE, *ws = xs + XBYTES;
 #pragma unroll
         for (int i = 0; i < XC; ++i)
-            *reinterpret_cast<v4u *>(xs + slot(tid / 8 + 32 * i, tid % 8)) = shuffle16<BITS>(xr[i]);
+            *reinterpret_cast<v4u *>(xs + slot(tid / 8 + THREADS / 8 * i, tid % 8)) = shuffle16<BITS>(xr[i]);
 #pragma unroll
-        for (int i = 0; i < WC; ++i) {
-            const int row = tid / WPR + 256 / WPR * i;
-#pragma unroll
-            for (int c = 0; c < CODES / 32; ++c) {
-                unsigned w[BITS];
-#pragma unroll
-                for (int d = 0; d < BITS; ++d) w[d] = wr[i][c * BITS + d];
-                const v8i o = expand<BITS>(w);
-                const int c0 = (tid % WPR) * (CODES / 16) + 2 * c;
-                *reinterpret_cast<v4u *>(ws + slot(row, c0)) =
-                    v4u{(unsigned)o[0], (unsigned)o[1], (unsigned)o[2], (unsigned)o[3]};
-                *reinterpret_cast<v4u *>(ws + slot(row, c0 + 1)) =
-                    v4u{(unsigned)o[4], (unsigned)o[5], (unsigned)o[6], (unsigned)o[7]};
-            }
+        for (int i = 0; i < WL; ++i) {
+            const int row = tid / WPR + THREADS / WPR * i;
+            const int c = 2 * (tid % WPR);
+            *reinterpret_cast<v4u *>(ws + slot(row, c)) = expand16<BITS>(wr[i]);
+            *reinterpret_cast<v4u *>(ws + slot(row, c + 1)) = expand16<BITS>(wr[i] + BITS / 2);
         }
         if (fetch_e) scales[buf][tid] = er;
-        if (fetch_s) scales[buf][BM + tid - (256 - BN)] = sr;
+        if (fetch_s) scales[buf][BM + tid - (THREADS - BN)] = sr;
     };
     // an operand of group g: chunks 4g + h and 4g + 2 + h of the lane's row
     auto frag = [&](const char *base, int row, int g) {
         const v4u lo = *reinterpret_cast<const v4u *>(base + slot(row, 4 * g + h));
         const v4u hi = *reinterpret_cast<const v4u *>(base + slot(row, 4 * g + 2 + h));
-        return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-                   (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+        return join(lo, hi);
     };
 
     v16f acc[IB][JB];
@@ -450,45 +522,75 @@ __global__ __launch_bounds__(256, 2) void packed_tile_kernel(PackedLinear a, int
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-    if (a.K > 0) {
-        load(0);
-        store(0);
-        __syncthreads();
-    }
+    // this group's steps start at first, first + HOP, ...; every group goes
+    // through the same number of rounds
+    constexpr int HOP = STEP * KS;
+    const int64_t first = (int64_t)grp * STEP;
+    auto fetch_step = [&](int64_t k0) {
+        if (k0 < a.K) load(k0, k0 + STEP <= a.K);
+    };
+    fetch_step(first);
+    if (first < a.K) store(0);
+    fetch_step(first + HOP);
+    __syncthreads();
     int buf = 0;
-    for (int64_t k0 = 0; k0 < a.K; k0 += STEP, buf ^= 1) {
-        const bool more = k0 + STEP < a.K;
-        if (more) load(k0 + STEP);
-        const char *xs = smem + buf * STAGE, *ws = xs + XBYTES;
+    for (int64_t r0 = 0; r0 < a.K; r0 += HOP, buf ^= 1) {
+        const int64_t k0 = r0 + first;
+        // the next step's data, in registers since the last step, go to the
+        // stage that the last step read, and the loads of the one after it
+        // have this whole step to arrive
+        if (k0 + HOP < a.K) store(buf ^ 1);
+        fetch_step(k0 + 2 * HOP);
+        if (KS > 1 && k0 >= a.K) {                    // uniform: no step in the last round
+            __syncthreads();
+            continue;
+        }
+        const char *xs = gsmem + buf * STAGE, *ws = xs + XBYTES;
         unsigned e[IB], s2[JB];
 #pragma unroll
         for (int i = 0; i < IB; ++i) e[i] = scales[buf][wm + 32 * i + l32] >> (8 * h);
 #pragma unroll
         for (int j = 0; j < JB; ++j) s2[j] = scales[buf][BM + wn + 32 * j + l32];
+        // Products and the multiply-adds of the ones before them alternate, two
+        // result tuples in turn: a matrix instruction runs for as long as 16
+        // multiply-adds of a wave, so neither unit waits for the other.
+        v8i fx[2][IB], fw[2][JB];
+        auto fetch = [&](int g) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            v8i fx[IB], fw[JB];
+            for (int i = 0; i < IB; ++i) fx[g][i] = frag(xs, wm + 32 * i + l32, g);
 #pragma unroll
-            for (int i = 0; i < IB; ++i) fx[i] = frag(xs, wm + 32 * i + l32, g);
+            for (int j = 0; j < JB; ++j) fw[g][j] = frag(ws, wn + 32 * j + l32, g);
+        };
+        v16f p[2];
+        constexpr int BLOCKS = 2 * IB * JB;
+        fetch(0);
 #pragma unroll
-            for (int j = 0; j < JB; ++j) fw[j] = frag(ws, wn + 32 * j + l32, g);
-#pragma unroll
-            for (int j = 0; j < JB; ++j) {
+        for (int b = 0; b <= BLOCKS; ++b) {
+            if (b < BLOCKS) {
+                const int g = b / (IB * JB), i = b % IB, j = b / IB % JB;
+                p[b & 1] = g == 0 ? mfma<0>(fx[g][i], fw[g][j], (int)e[i])
+                                  : mfma<2>(fx[g][i], fw[g][j], (int)e[i]);
+            }
+            if (b == 0) fetch(1);
+            __builtin_amdgcn_sched_barrier(0);
+            if (b > 0) {
+                const int c = b - 1, g = c / (IB * JB), i = c % IB, j = c / IB % JB;
                 const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)(s2[j] >> (16 * g)));
 #pragma unroll
-                for (int i = 0; i < IB; ++i) {
-                    const v16f p = g == 0 ? mfma<0>(fx[i], fw[j], (int)e[i]) : mfma<2>(fx[i], fw[j], (int)e[i]);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(p[r], s, acc[i][j][r]);
-                }
+                for (int r = 0; r < 16; ++r)
+                    acc[i][j][r] = __builtin_fmaf(p[c & 1][r], s, acc[i][j][r]);
+                // a use here, or all of this moves past the stores and the
+                // barrier below
+                asm volatile("" : "+v"(acc[i][j]));
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (more) store(buf ^ 1);
         __syncthreads();
     }
 
-    // sums to LDS: row-major, 16-byte chunks of a row rotated by the row so
-    // that the lanes of a store spread over the banks
+    // Sums to LDS, a tile per group: row-major, 16-byte chunks of a row rotated
+    // by the row so that the lanes of a store spread over the banks.  (Every
+    // stage has been read: the last round ended with a barrier.)
     float *tile = reinterpret_cast<float *>(smem);
     auto cell = [](int row, int col) { return row * BN + (col ^ ((row & 7) << 2)); };
 #pragma unroll
@@ -498,43 +600,64 @@ __global__ __launch_bounds__(256, 2) void packed_tile_kernel(PackedLinear a, int
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int row = wm + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                tile[cell(row, wn + 32 * j + l32)] = acc[i][j][r] * code_scale<BITS>();
+                tile[grp * BM * BN + cell(row, wn + 32 * j + l32)] = acc[i][j][r] * code_scale<BITS>();
             }
     __syncthreads();
-    finish_tile<BM, BN>(a, m0, n0, tid, [&](int row, int col) {
-        return *reinterpret_cast<const v4f *>(tile + cell(row, col));
+    finish_tile<BM, BN, THREADS * KS>(a, m0, n0, threadIdx.x, [&](int row, int col) {
+        v4f y = *reinterpret_cast<const v4f *>(tile + cell(row, col));
+#pragma unroll
+        for (int g = 1; g < KS; ++g)                  // in group order
+            y += *reinterpret_cast<const v4f *>(tile + g * BM * BN + cell(row, col));
+        return y;
     });
 }
 
-template <int BM, int BITS>
+template <int BM, int BN, int WR, int WC, int KS, int BITS>
 hipError_t launch_tiles(const PackedLinear &a, bool wide, hipStream_t s) {
     const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
-    if (tm * tn * 256 > UINT32_MAX) return hipErrorInvalidValue;
-    return launch(wide ? packed_tile_kernel<BM, BITS, true> : packed_tile_kernel<BM, BITS, false>,
-                  dim3((unsigned)(tm * tn)), dim3(256), s, a, (int)tm);
+    constexpr int THREADS = 64 * WR * WC * KS;
+    if (tm * tn * THREADS > UINT32_MAX) return hipErrorInvalidValue;
+    return launch(wide ? packed_tile_kernel<BM, BN, WR, WC, KS, BITS, true>
+                       : packed_tile_kernel<BM, BN, WR, WC, KS, BITS, false>,
+                  dim3((unsigned)(tm * tn)), dim3(THREADS), s, a, (int)tm);
 }
 
 template <int BITS>
-hipError_t launch_bits(const PackedLinear &a, hipStream_t s) {
+hipError_t launch_bits(const PackedLinear &a, int num_cus, hipStream_t s) {
     const auto al = [](const void *p, int64_t ld, int64_t b) {
         return reinterpret_cast<uintptr_t>(p) % b == 0 && ld % b == 0;
     };
-    const bool wide = al(a.X, a.ldx, 16) && al(a.Q, a.ldq, 16) && al(a.XE, a.ldxe, 4) &&
+    const auto count = [&](int bm, int bn) {
+        return (((int64_t)a.M + bm - 1) / bm) * (((int64_t)a.N + bn - 1) / bn);
+    };
+    const int64_t cus = num_cus;
+    const bool wide = al(a.X, a.ldx, 16) && al(a.Q, a.ldq, 4 * BITS) && al(a.XE, a.ldxe, 4) &&
                       al(a.S, a.lds * 2, 4);
-    if (a.M > 64) return launch_tiles<128, BITS>(a, wide, s);
-    if (a.M > 32) return launch_tiles<64, BITS>(a, wide, s);
-    const bool wide_rows = al(a.X, a.ldx, 16) && al(a.Q, a.ldq, 4 * BITS);
-    const dim3 grid((unsigned)(((int64_t)a.N + 31) / 32));
-    if ((int64_t)grid.x * 64 * KS > UINT32_MAX) return hipErrorInvalidValue;
-    return launch(wide_rows ? packed_rows_kernel<BITS, true> : packed_rows_kernel<BITS, false>, grid,
-                  dim3(64 * KS), s, a);
+    if (a.M <= 16) {
+                if (const char *v = getenv("VAR")) switch (atoi(v)) {
+            case 4: return a.Y8 ? launch_rows<BITS, 2, 2>(a, wide, s) : launch_rows<BITS, 1, 4>(a, wide, s);
+            case 8: return a.Y8 ? launch_rows<BITS, 2, 4>(a, wide, s) : launch_rows<BITS, 1, 8>(a, wide, s);
+            case 16: return a.Y8 ? launch_rows<BITS, 2, 8>(a, wide, s) : launch_rows<BITS, 1, 16>(a, wide, s);
+        }
+        if (a.Y8) return launch_rows<BITS, 2, 4>(a, wide, s);
+        return launch_rows<BITS, 1, 4>(a, wide, s);
+    }
+    // Tiles by what they leave idle, most cells per tile first:
+    const int64_t big = count(256, 128);
+    if (big >= cus && 4 * ((big + cus - 1) / cus * cus) <= 5 * big)
+        return launch_tiles<256, 128, 4, 2, 1, BITS>(a, wide, s);
+    if (count(32, 64) <= cus) return launch_tiles<32, 64, 1, 2, 4, BITS>(a, wide, s);
+    const int64_t mid = count(64, 64);
+    if (mid <= cus) return launch_tiles<64, 64, 2, 2, 4, BITS>(a, wide, s);
+    if (mid <= 2 * cus) return launch_tiles<64, 64, 2, 2, 2, BITS>(a, wide, s);
+    if (mid <= 3 * cus) return launch_tiles<64, 64, 2, 2, 1, BITS>(a, wide, s);
+    return launch_tiles<128, 64, 2, 2, 1, BITS>(a, wide, s);
 }
 
 }  // namespace
 
 hipError_t launch_packed_linear(int bits, const PackedLinear &a, int num_cus, hipStream_t s) {
-    (void)num_cus;
-    return bits == 2 ? launch_bits<2>(a, s) : launch_bits<4>(a, s);
+    return bits == 2 ? launch_bits<2>(a, num_cus, s) : launch_bits<4>(a, num_cus, s);
 }
 
 }  // namespace gg
