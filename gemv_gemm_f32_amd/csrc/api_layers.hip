@@ -131,7 +131,7 @@ int rmsnorm(int64_t M, int64_t K, const float *X, int64_t ldx, const float *R, i
     if (int st = check_device(&cus)) return st;
     const RmsNorm a{(int)M, (int)K, X, R, gamma, S, Y, rstd, Q, E, ldx, R ? ldr : 0,
                     S ? lds : 0, ldy, ldq, lde, eps};
-    return launch_status(launch_rmsnorm(a, cus, reinterpret_cast<hipStream_t>(stream)));
+    return launch_status(launch_rmsnorm(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

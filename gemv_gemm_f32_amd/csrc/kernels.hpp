@@ -131,7 +131,7 @@ struct RmsNorm {
     int64_t ldx, ldr, lds, ldy, ldq, lde;
     float eps;
 };
-hipError_t launch_rmsnorm(const RmsNorm &a, int num_cus, hipStream_t stream);
+hipError_t launch_rmsnorm(const RmsNorm &a, hipStream_t stream);
 
 // dX = rstd * (gamma * dY - xhat * mean(gamma * dY * xhat)) + dS with xhat =
 // S * rstd, and dgamma = sum over rows of dY * xhat.  gamma, dS, dX and

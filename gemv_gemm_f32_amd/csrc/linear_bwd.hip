@@ -22,14 +22,12 @@ namespace gg {
 namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef v4f v4f_any __attribute__((aligned(4)));   // rows may start at any float
 
 constexpr int COLS = 64;             // columns per workgroup
 constexpr int LANES = COLS / 4;      // threads along a row
 constexpr int ROWS = 256 / LANES;    // rows at a time
 
-// VEC: dY, Z and dZ are 16-byte aligned with leading dimensions that are
-// multiples of 4; else each of a thread's 4 columns is a load of its own.
-template <bool VEC>
 __global__ __launch_bounds__(256) void dz_kernel(int act, int M, int N, int chunk,
                                                  const float *dY, int64_t lddy, const float *Z,
                                                  int64_t ldz, float *dZ, int64_t lddz,
@@ -48,9 +46,9 @@ __global__ __launch_bounds__(256) void dz_kernel(int act, int M, int N, int chun
                 const float *pz = Z + r * ldz + col;
                 float *po = dZ + r * lddz + col;
                 v4f d = {0.f, 0.f, 0.f, 0.f}, z = d;
-                if (VEC && live == 4) {
-                    d = *reinterpret_cast<const v4f *>(pd);
-                    if (ACT != GG_ACT_NONE) z = *reinterpret_cast<const v4f *>(pz);
+                if (live == 4) {
+                    d = *reinterpret_cast<const v4f_any *>(pd);
+                    if (ACT != GG_ACT_NONE) z = *reinterpret_cast<const v4f_any *>(pz);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -62,8 +60,8 @@ __global__ __launch_bounds__(256) void dz_kernel(int act, int M, int N, int chun
                 if constexpr (ACT != GG_ACT_NONE) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) d[c] *= act_slope<ACT>(z[c]);
-                    if (VEC && live == 4) {
-                        *reinterpret_cast<v4f *>(po) = d;
+                    if (live == 4) {
+                        *reinterpret_cast<v4f_any *>(po) = d;
                     } else {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
@@ -150,10 +148,8 @@ hipError_t launch_linear_bwd(bool trans_w, int act, bool accumulate, int M, int 
             dZ = out;
         }
         const int chunk = dz_chunk(M), chunks = (M + chunk - 1) / chunk;
-        const bool vec = ((reinterpret_cast<uintptr_t>(dY) | reinterpret_cast<uintptr_t>(Z)) & 15) == 0 &&
-                         lddy % 4 == 0 && ldz % 4 == 0;
         const dim3 grid(blocks(N, COLS, 1 << 17), chunks);
-        e = launch(vec ? dz_kernel<true> : dz_kernel<false>, grid, dim3(256), s, act, M, N, chunk,
+        e = launch(dz_kernel, grid, dim3(256), s, act, M, N, chunk,
                    dY, lddy, Z, ldz, out, lddz, db ? partial : nullptr);
         if (e != hipSuccess) return e;
         if (db) e = launch_column_sum(chunks, N, partial, accumulate, db, s);

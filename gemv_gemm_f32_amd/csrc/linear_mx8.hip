@@ -26,7 +26,6 @@
 // k may be taken in any order as long as both operands agree.
 #include <hip/hip_runtime.h>
 
-#include <stdlib.h>
 #include <type_traits>
 
 #include "activation.hpp"
@@ -39,7 +38,12 @@ namespace {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
+// rows may start at any byte: the same loads, without the promise of alignment
+typedef v4u v4u_any __attribute__((aligned(1)));
+typedef v2u v2u_any __attribute__((aligned(1)));
+typedef unsigned u32_any __attribute__((aligned(1)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef v4f v4f_any __attribute__((aligned(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ unsigned perm(unsigned hi, unsigned lo, unsigned sel) {
@@ -146,11 +150,11 @@ __device__ __forceinline__ void load_bytes(unsigned (&d)[N / 4], const uint8_t *
 template <int BITS>
 __device__ __forceinline__ void load_codes(unsigned (&w)[BITS], const uint8_t *p) {
     if constexpr (BITS == 4) {
-        const v4u q = *reinterpret_cast<const v4u *>(p);
+        const v4u q = *reinterpret_cast<const v4u_any *>(p);
 #pragma unroll
         for (int d = 0; d < 4; ++d) w[d] = q[d];
     } else {
-        const v2u q = *reinterpret_cast<const v2u *>(p);
+        const v2u q = *reinterpret_cast<const v2u_any *>(p);
         w[0] = q[0];
         w[1] = q[1];
     }
@@ -187,12 +191,6 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
     const int col = tid % PER_ROW * 4;
     const int64_t n = n0 + col;
     const int live = (int)min(max((int64_t)a.N - n, (int64_t)0), (int64_t)4);
-    const auto wide = [](const void *p, int64_t ld, int bytes) {
-        return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * 4 % bytes == 0;
-    };
-    // uniform: whole 16-byte accesses
-    const bool vr = n0 + BN <= a.N && wide(a.R, a.ldr, 16), vy = n0 + BN <= a.N && wide(a.Y, a.ldy, 16);
-    const bool v8 = n0 + BN <= a.N && reinterpret_cast<uintptr_t>(a.Y8) % 4 == 0 && a.ldy8 % 4 == 0;
     v4f bias = {0.f, 0.f, 0.f, 0.f};
     if (a.bias)
 #pragma unroll
@@ -209,8 +207,8 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
             v4f res = {0.f, 0.f, 0.f, 0.f};
             if (a.R) {
                 const float *p = a.R + m * a.ldr + n;
-                if (vr && w == 4) {
-                    res = *reinterpret_cast<const v4f *>(p);
+                if (w == 4) {
+                    res = *reinterpret_cast<const v4f_any *>(p);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -224,8 +222,8 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
             }
             if (a.Y) {
                 float *p = a.Y + m * a.ldy + n;
-                if (vy && w == 4) {
-                    *reinterpret_cast<v4f *>(p) = y;
+                if (w == 4) {
+                    *reinterpret_cast<v4f_any *>(p) = y;
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -239,8 +237,8 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
                 const int e = mx8_exponent(oct_max(top));
                 const unsigned q = mx8_pack4(y[0], y[1], y[2], y[3], e);
                 uint8_t *p = a.Y8 + m * a.ldy8 + n;
-                if (v8 && w == 4) {
-                    *reinterpret_cast<unsigned *>(p) = q;
+                if (w == 4) {
+                    *reinterpret_cast<u32_any *>(p) = q;
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -262,9 +260,9 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
 //
 // A workgroup owns 16 NH columns n (NH = 2 for an output in 8 bits, whose
 // blocks are 32 wide); its waves split into NH column sets by KW runs of
-// groups, and the runs' sums meet in LDS, added in order.  WIDE: 16 bytes of
-// x, 32 codes and both scales in one load each; else, and where K cuts a
-// group short, byte by byte.
+// groups, and the runs' sums meet in LDS, added in order.  Loads are 16 bytes
+// of x, 32 codes and both scales each; a pair that K cuts short is loaded byte
+// by byte.
 // Lanes 16q .. 16q + 15 have loaded codes 32q .. 32q + 31 of a pair of
 // groups; afterwards they have codes 16q .. 16q + 15 of the first group in the
 // lower dwords and of the second in the upper.
@@ -321,10 +319,10 @@ struct Rows {
         for (int i = 0; i < N; ++i) load_codes<BITS>(p[i].w, w + i * (16 * BITS));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            p[i].x[0] = *reinterpret_cast<const v4u *>(x + i * 128);
-            p[i].x[1] = *reinterpret_cast<const v4u *>(x + i * 128 + 64);
+            p[i].x[0] = *reinterpret_cast<const v4u_any *>(x + i * 128);
+            p[i].x[1] = *reinterpret_cast<const v4u_any *>(x + i * 128 + 64);
             p[i].e = e[4 * i];
-            p[i].s = *reinterpret_cast<const unsigned *>(s + 2 * i);
+            p[i].s = *reinterpret_cast<const u32_any *>(s + 2 * i);
         }
         advance(N);
 #pragma unroll
@@ -350,7 +348,7 @@ struct Rows {
     }
 };
 
-template <int BITS, int NH, int KW, bool WIDE>
+template <int BITS, int NH, int KW>
 __global__ __launch_bounds__(64 * NH * KW) void packed_rows_kernel(PackedLinear a) {
     constexpr int NC = 16 * NH;                       // columns
     __shared__ float red[KW][16][NC];
@@ -363,8 +361,8 @@ __global__ __launch_bounds__(64 * NH * KW) void packed_rows_kernel(PackedLinear 
     const int64_t pairs = ((int64_t)a.K + 127) / 128;
     // run kw of KW: as even a share as whole pairs allow
     const int64_t first = pairs * kw / KW, end = pairs * (kw + 1) / KW;
-    // the pairs of it that exist in full, if they may be loaded as a whole
-    int n = WIDE ? (int)max(min(end, (int64_t)a.K / 128) - first, (int64_t)0) : 0;
+    // the pairs of it that exist in full
+    int n = (int)max(min(end, (int64_t)a.K / 128) - first, (int64_t)0);
     Rows<BITS> rows = {a.Q + nrow * a.ldq + 4 * BITS * q, a.X + tok * a.ldx + 16 * q,
                        a.XE + tok * a.ldxe + q, a.S + nrow * a.lds};
     rows.advance(first);
@@ -391,16 +389,17 @@ __global__ __launch_bounds__(64 * NH * KW) void packed_rows_kernel(PackedLinear 
 }
 
 template <int BITS, int NH, int KW>
-hipError_t launch_rows(const PackedLinear &a, bool wide, hipStream_t s) {
+hipError_t launch_rows(const PackedLinear &a, hipStream_t s) {
     const int64_t nb = ((int64_t)a.N + 16 * NH - 1) / (16 * NH);
     if (nb * 64 * NH * KW > UINT32_MAX) return hipErrorInvalidValue;
-    return launch(wide ? packed_rows_kernel<BITS, NH, KW, true> : packed_rows_kernel<BITS, NH, KW, false>,
-                  dim3((unsigned)nb), dim3(64 * NH * KW), s, a);
+    return launch(packed_rows_kernel<BITS, NH, KW>, dim3((unsigned)nb), dim3(64 * NH * KW), s, a);
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: a workgroup of 4 waves owns BM rows of x by 128 columns n and
-// walks k in steps of 128 (two weight groups), double-buffered in LDS.
+// More than 16 rows: a workgroup owns BM rows of x by BN columns n and walks k
+// in steps of 128 (two weight groups), double-buffered in LDS.  Bound by the
+// vector unit: 16 multiply-adds per matrix instruction (which takes as long),
+// and the expansion of the codes.
 //
 //  * Codes are expanded once per workgroup, on their way into LDS, and then
 //    feed the BM / 32 row blocks; x's bytes are permuted on the same way.
@@ -409,6 +408,8 @@ hipError_t launch_rows(const PackedLinear &a, bool wide, hipStream_t s) {
 //    rows, and the writes, meet no bank twice.
 //  * Loads run two steps ahead: registers hold the next step while LDS holds
 //    this one; one barrier per step.
+//  * Where tiles are few, KS groups of waves share a tile's steps, each with
+//    its own stages, and their sums are added in group order.
 //  * The finished sums pass through LDS, so that bias, residual and the
 //    stores of Y run along rows, 16 bytes per lane.
 constexpr int STEP = 128;
@@ -421,7 +422,7 @@ __device__ __forceinline__ v4u load_chunk(const uint8_t *p, int64_t at, int64_t 
 }
 
 // KS groups of WR x WC waves, each wave with IB x JB blocks of 32 x 32.
-template <int BM, int BN, int WR, int WC, int KS, int BITS, bool WIDE>
+template <int BM, int BN, int WR, int WC, int KS, int BITS>
 __global__ __launch_bounds__(64 * WR * WC * KS, WR * WC * KS >= 8 ? WR * WC * KS / 4 : 2)
 void packed_tile_kernel(PackedLinear a, int tiles_m) {
     constexpr int THREADS = 64 * WR * WC;             // of a group
@@ -469,14 +470,14 @@ void packed_tile_kernel(PackedLinear a, int tiles_m) {
     // the step at k0; `full` (uniform): all of its 128 columns exist
     auto load = [&](int64_t k0, bool full) {
         const int64_t b = k0 / 32, g = k0 / 64;
-        if (WIDE && full) {
+        if (full) {
 #pragma unroll
             for (int i = 0; i < XC; ++i)
-                xr[i] = *reinterpret_cast<const v4u *>(px[i] + k0 + 16 * (tid % 8));
+                xr[i] = *reinterpret_cast<const v4u_any *>(px[i] + k0 + 16 * (tid % 8));
 #pragma unroll
             for (int i = 0; i < WL; ++i) load_codes<BITS>(wr[i], pw[i] + k0 * BITS / 8 + CB * (tid % WPR));
-            if (fetch_e) er = *reinterpret_cast<const unsigned *>(pe + b);
-            if (fetch_s) sr = *reinterpret_cast<const unsigned *>(ps + g);
+            if (fetch_e) er = *reinterpret_cast<const u32_any *>(pe + b);
+            if (fetch_s) sr = *reinterpret_cast<const u32_any *>(ps + g);
         } else {
 #pragma unroll
             for (int i = 0; i < XC; ++i) xr[i] = load_chunk(px[i], k0 + 16 * (tid % 8), a.K);
@@ -613,45 +614,53 @@ void packed_tile_kernel(PackedLinear a, int tiles_m) {
 }
 
 template <int BM, int BN, int WR, int WC, int KS, int BITS>
-hipError_t launch_tiles(const PackedLinear &a, bool wide, hipStream_t s) {
+hipError_t launch_tiles(const PackedLinear &a, hipStream_t s) {
     const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
     constexpr int THREADS = 64 * WR * WC * KS;
     if (tm * tn * THREADS > UINT32_MAX) return hipErrorInvalidValue;
-    return launch(wide ? packed_tile_kernel<BM, BN, WR, WC, KS, BITS, true>
-                       : packed_tile_kernel<BM, BN, WR, WC, KS, BITS, false>,
-                  dim3((unsigned)(tm * tn)), dim3(THREADS), s, a, (int)tm);
+    return launch(packed_tile_kernel<BM, BN, WR, WC, KS, BITS>, dim3((unsigned)(tm * tn)),
+                  dim3(THREADS), s, a, (int)tm);
 }
 
 template <int BITS>
 hipError_t launch_bits(const PackedLinear &a, int num_cus, hipStream_t s) {
-    const auto al = [](const void *p, int64_t ld, int64_t b) {
-        return reinterpret_cast<uintptr_t>(p) % b == 0 && ld % b == 0;
-    };
     const auto count = [&](int bm, int bn) {
         return (((int64_t)a.M + bm - 1) / bm) * (((int64_t)a.N + bn - 1) / bn);
     };
     const int64_t cus = num_cus;
-    const bool wide = al(a.X, a.ldx, 16) && al(a.Q, a.ldq, 4 * BITS) && al(a.XE, a.ldxe, 4) &&
-                      al(a.S, a.lds * 2, 4);
+    // Up to 16 rows.  Runs of k per column set by what fills the CUs: 4 where
+    // there is a workgroup per CU (one row, 4 bits, 12288 x 1536: 5.6 us in 4,
+    // 6.9 in 8, 7.5 in 16), else as many as the rows are long enough for (1536 x
+    // 12288: 12.3 us in 4, 11.6 in 8, 9.8 in 16; 768 x 768: 3.4, 3.3, 3.6).
+    // With an output in 8 bits there are two column sets (12288 x 1536: 6.6 us
+    // in 2, 6.3 in 4, 7.5 in 8; 1536 x 12288: 22, 24, 16).
     if (a.M <= 16) {
-                if (const char *v = getenv("VAR")) switch (atoi(v)) {
-            case 4: return a.Y8 ? launch_rows<BITS, 2, 2>(a, wide, s) : launch_rows<BITS, 1, 4>(a, wide, s);
-            case 8: return a.Y8 ? launch_rows<BITS, 2, 4>(a, wide, s) : launch_rows<BITS, 1, 8>(a, wide, s);
-            case 16: return a.Y8 ? launch_rows<BITS, 2, 8>(a, wide, s) : launch_rows<BITS, 1, 16>(a, wide, s);
-        }
-        if (a.Y8) return launch_rows<BITS, 2, 4>(a, wide, s);
-        return launch_rows<BITS, 1, 4>(a, wide, s);
+        const bool lengthy = a.K >= 4096;
+        if (a.Y8)
+            return count(16, 32) < cus && lengthy ? launch_rows<BITS, 2, 8>(a, s)
+                                                  : launch_rows<BITS, 2, 4>(a, s);
+        if (count(16, 16) >= cus) return launch_rows<BITS, 1, 4>(a, s);
+        return lengthy ? launch_rows<BITS, 1, 16>(a, s) : launch_rows<BITS, 1, 8>(a, s);
     }
-    // Tiles by what they leave idle, most cells per tile first:
-    const int64_t big = count(256, 128);
+    // More rows: tiles by how they fill the CUs (4 bits, us).
+    //  - 256 x 128 where a round of them leaves at most a fifth of the CUs idle:
+    //    2048 x 4096 x 4096 67 against 85 in 128 x 64;
+    //  - 32 x 64 in four k-groups where they fit one per CU: 128 x 4096 x 4096
+    //    13.9 against 17.4 in 64 x 64, 500 x 768 x 768 6.3 against 7.9;
+    //  - 64 x 64 in four k-groups, one per CU (64 x 12288 x 1536 10.5 against
+    //    11.0 in two and 13.3 in one, 500 x 1536 x 12288 39 / 48 / 69), in two
+    //    at two per CU (128 x 12288 x 1536 14.4 against 18.8 in four and 15.9
+    //    in one), and in one at three (256 x 12288 x 1536 19.5 against 21.3 in
+    //    two and 22.2 in 128 x 64);
+    //  - else 128 x 64 (500 x 12288 x 1536 28.9 against 33.8 in 64 x 64).
+    const int64_t big = count(256, 128), mid = count(64, 64);
     if (big >= cus && 4 * ((big + cus - 1) / cus * cus) <= 5 * big)
-        return launch_tiles<256, 128, 4, 2, 1, BITS>(a, wide, s);
-    if (count(32, 64) <= cus) return launch_tiles<32, 64, 1, 2, 4, BITS>(a, wide, s);
-    const int64_t mid = count(64, 64);
-    if (mid <= cus) return launch_tiles<64, 64, 2, 2, 4, BITS>(a, wide, s);
-    if (mid <= 2 * cus) return launch_tiles<64, 64, 2, 2, 2, BITS>(a, wide, s);
-    if (mid <= 3 * cus) return launch_tiles<64, 64, 2, 2, 1, BITS>(a, wide, s);
-    return launch_tiles<128, 64, 2, 2, 1, BITS>(a, wide, s);
+        return launch_tiles<256, 128, 4, 2, 1, BITS>(a, s);
+    if (count(32, 64) <= cus) return launch_tiles<32, 64, 1, 2, 4, BITS>(a, s);
+    if (mid <= cus) return launch_tiles<64, 64, 2, 2, 4, BITS>(a, s);
+    if (mid <= 2 * cus) return launch_tiles<64, 64, 2, 2, 2, BITS>(a, s);
+    if (mid <= 3 * cus) return launch_tiles<64, 64, 2, 2, 1, BITS>(a, s);
+    return launch_tiles<128, 64, 2, 2, 1, BITS>(a, s);
 }
 
 }  // namespace
