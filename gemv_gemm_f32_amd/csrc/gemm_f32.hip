@@ -13,13 +13,18 @@ namespace {
 struct ScaleAdd {
     float alpha, beta;
 
-    // The N sums of one column that a lane holds: acc[r] belongs to row
+    template <int N>
+    struct Fetched {};
+    template <int N, class Row, class Mine>
+    __device__ __forceinline__ void fetch(Fetched<N> &, int, int, int, Row, Mine) const {}
+
+    // The NS sums of one column that a lane holds: acc[r] belongs to row
     // row(r), if mine(r).
-    template <int N, class Acc, class Row, class Mine>
-    __device__ __forceinline__ void block(const Acc &acc, int col, int M, float *C, int64_t ldc,
-                                          Row row, Mine mine) const {
+    template <int NS, class Acc, class Row, class Mine>
+    __device__ __forceinline__ void block(const Acc &acc, const Fetched<NS> &, int col, int M,
+                                          float *C, int64_t ldc, Row row, Mine mine) const {
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
+        for (int r = 0; r < NS; ++r) {
             if (!mine(r) || row(r) >= M) continue;
             float *c = C + (int64_t)row(r) * ldc + col;
             float v = alpha * acc[r];

@@ -53,7 +53,9 @@
 //  * Edges: rows and columns past M or N are fetched clamped into the matrix
 //    and their results are never stored.
 //  * Epilogue: a type E, given to the kernel as an argument, takes each block
-//    of finished sums (E::block) and stores what becomes of them.
+//    of finished sums (E::block) and stores what becomes of them.  What it
+//    needs from memory it may fetch before the K walk (E::fetch), so that no
+//    wave waits for it at the end.
 //  * Tile order: workgroups are handed to the 8 XCDs round-robin, so the grid
 //    index is remapped to give each XCD a contiguous run of tiles, ordered in
 //    groups of 8 tile rows so that a run shares A row panels and B column
@@ -224,6 +226,18 @@ __global__ __launch_bounds__(THREADS) void gemm_f32_kernel(
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
+    // column and rows of the sums that a lane holds of block (i, j)
+    auto col_of = [&](int j) { return n0 + wn + 32 * j + l32; };
+    auto row_of = [&](int i) {
+        return [=](int r) { return m0 + wm + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3); };
+    };
+    const auto all = [](int) { return true; };
+    typename E::template Fetched<16> pre[IB][JB];
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) epi.fetch(pre[i][j], col_of(j), M, N, row_of(i), all);
+
     const int nk = (K + BK - 1) / BK;
     if (nk > 0) {
         la.load(A, lda, m0, 0, M, K, tid);
@@ -286,12 +300,7 @@ __global__ __launch_bounds__(THREADS) void gemm_f32_kernel(
     for (int i = 0; i < IB; ++i)
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
-            const int col = n0 + wn + 32 * j + l32;
-            if (col >= N) continue;
-            epi.template block<16>(
-                acc[i][j], col, M, C, ldc,
-                [&](int r) { return m0 + wm + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3); },
-                [](int) { return true; });
+            if (col_of(j) < N) epi.block(acc[i][j], pre[i][j], col_of(j), M, C, ldc, row_of(i), all);
         }
 }
 
@@ -493,6 +502,30 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
 #pragma unroll
             for (int r = 0; r < AR; ++r) acc[i][j][r] = 0.f;
 
+    // Which group finishes word e of a lane's accumulators, once the groups'
+    // sums are joined (see below): e * KS / ACCW where every group finishes a
+    // share, else group 0.
+    constexpr bool SPLIT_OUT = KS >= 4 && ACCW >= KS;
+    const auto owner = [](int e) { return SPLIT_OUT ? e * KS / ACCW : 0; };
+    // Accumulator layouts: register r of lane l holds, in a 32 x 32 block,
+    // row 8*(r/4) + 4*(l/32) + r%4 and column l%32; in a 16 x 16 block, row
+    // 4*(l/16) + r and column l%16.
+    auto col_of = [&](int j) { return n0 + wn + MF * j + (lane & (MF - 1)); };
+    auto row_of = [&](int i) {
+        return [=](int r) {
+            return m0 + wm + MF * i +
+                   (MF == 32 ? 8 * (r >> 2) + 4 * h + (r & 3) : 4 * (lane >> 4) + r);
+        };
+    };
+    auto mine = [&](int i, int j) {
+        return [=](int r) { return KS == 1 || owner((i * JB + j) * AR + r) == grp; };
+    };
+    typename E::template Fetched<AR> pre[IB][JB];
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) epi.fetch(pre[i][j], col_of(j), M, N, row_of(i), mine(i, j));
+
     const int nk = (K + BK - 1) / BK;
     const int rounds = (nk + KS - 1) / KS;        // the same for every group
     if (rounds > 0) {
@@ -615,8 +648,6 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
     // Word e of a lane goes to group e * KS / ACCW: ACCW / KS words each,
     // one more for some groups when KS does not divide ACCW (16 words over
     // 6 groups: 3, 3, 2, 3, 3, 2).
-    constexpr bool SPLIT_OUT = KS >= 4 && ACCW >= KS;
-    const auto owner = [](int e) { return e * KS / ACCW; };
     if constexpr (KS > 1) {
         float *red = reinterpret_cast<float *>(smem);
         __syncthreads();                          // every stage read is done
@@ -678,23 +709,12 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
         }
     }
 
-    // Accumulator layouts: register r of lane l holds, in a 32 x 32 block,
-    // row 8*(r/4) + 4*(l/32) + r%4 and column l%32; in a 16 x 16 block, row
-    // 4*(l/16) + r and column l%16.
 #pragma unroll
     for (int i = 0; i < IB; ++i)
 #pragma unroll
-        for (int j = 0; j < JB; ++j) {
-            const int col = n0 + wn + MF * j + (lane & (MF - 1));
-            if (col >= N) continue;
-            epi.template block<AR>(
-                acc[i][j], col, M, C, ldc,
-                [&](int r) {
-                    return m0 + wm + MF * i +
-                           (MF == 32 ? 8 * (r >> 2) + 4 * h + (r & 3) : 4 * (lane >> 4) + r);
-                },
-                [&](int r) { return !SPLIT_OUT || owner((i * JB + j) * AR + r) == grp; });
-        }
+        for (int j = 0; j < JB; ++j)
+            if (col_of(j) < N)
+                epi.block(acc[i][j], pre[i][j], col_of(j), M, C, ldc, row_of(i), mine(i, j));
 }
 
 template <bool AX, bool BX, int BM, int BN, int KS, int WPG, bool KT, int MF, class E>

@@ -25,27 +25,35 @@ struct Layer {
     int64_t ldz;
     int act;
 
-    // The N sums of one column that a lane holds: acc[r] belongs to row
-    // row(r), if mine(r).  The residuals are fetched before any of them is
-    // used, so their latencies overlap.
-    template <int N, class Acc, class Row, class Mine>
-    __device__ __forceinline__ void block(const Acc &acc, int col, int M, float *C, int64_t ldc,
-                                          Row row, Mine mine) const {
-        const float b = bias ? bias[col] : 0.f;
-        float res[N];
+    // Bias and residuals of one column's NS sums, fetched before the K walk.
+    template <int NS>
+    struct Fetched {
+        float bias, res[NS];
+    };
+    template <int NS, class Row, class Mine>
+    __device__ __forceinline__ void fetch(Fetched<NS> &f, int col, int M, int N, Row row,
+                                          Mine mine) const {
+        f.bias = bias && col < N ? bias[col] : 0.f;
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
-            res[r] = 0.f;
-            if (R && mine(r) && row(r) < M) res[r] = R[(int64_t)row(r) * ldr + col];
+        for (int r = 0; r < NS; ++r) {
+            f.res[r] = 0.f;
+            if (R && col < N && mine(r) && row(r) < M) f.res[r] = R[(int64_t)row(r) * ldr + col];
         }
+    }
+
+    // The NS sums of one column that a lane holds: acc[r] belongs to row
+    // row(r), if mine(r).
+    template <int NS, class Acc, class Row, class Mine>
+    __device__ __forceinline__ void block(const Acc &acc, const Fetched<NS> &f, int col, int M,
+                                          float *C, int64_t ldc, Row row, Mine mine) const {
         with_act(act, [&](auto a) {
 #pragma unroll
-            for (int r = 0; r < N; ++r) {
+            for (int r = 0; r < NS; ++r) {
                 if (!mine(r) || row(r) >= M) continue;
-                const float z = acc[r] + b;
+                const float z = acc[r] + f.bias;
                 if (Z) Z[(int64_t)row(r) * ldz + col] = z;
                 const float y = act_value<decltype(a)::value>(z);
-                C[(int64_t)row(r) * ldc + col] = R ? y + res[r] : y;
+                C[(int64_t)row(r) * ldc + col] = R ? y + f.res[r] : y;
             }
         });
     }
