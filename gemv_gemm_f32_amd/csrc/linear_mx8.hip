@@ -5,25 +5,28 @@
 //   w(n, k) = (code - 7.5) s(n, k/64) = (2 code - 15) s/2     (4 bits)
 //   w(n, k) = (code - 1.5) s(n, k/64) = (2 code - 3) s/2      (2 bits)
 //
-// The odd integers up to 15 have 4 significant bits, so 2 code - 15 is an
-// e4m3 number exactly: codes become matrix operands without any rounding.
-// v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 32 rows of x by 32 rows of W
-// over 64 columns, the width of one weight scale, and applies x's two powers
-// of two itself: registers 0-3 of both half-waves are the columns of the first
-// block of 32, whose power lanes 0-31 give, registers 4-7 those of the second,
-// whose power lanes 32-63 give.  What is left per weight group is one fp32
-// multiply-add per sum with s/2.
-// Products are exact in fp32 (4 x 4 significant bits), sums are fp32.
+// Every factor has at most 4 significant bits (the odd integers up to 15, and
+// e4m3 numbers times a power of two), so both operands are bf16 numbers
+// exactly and products are exact in fp32: v_mfma_f32_32x32x16_bf16 sums them in
+// fp32, group by group, and one fp32 multiply-add per sum and group applies
+// s/2.  Nothing is rounded but the sums.
+//
+// The 8-bit matrix instructions (f8f6f4 and fp8) would take both operands as
+// they are, twice as fast, but add products within parts of their k in an
+// adder that keeps 13 bits below the largest product (measured: 448 + 2^-7 =
+// 448): sums of 64 random products were off by 3e-6 relative to their size,
+// 0 with bf16.
 //
 // Rows of x are the instruction's A operand (they spread over a lane's 16
 // sums), rows of W its B operand: a lane belongs to one output column n, so
 // its weight scale is one register and stores of Y run along rows.
 //
-// Codes reach the lanes as they lie in memory and are expanded there by
-// shifts and a byte permutation that looks their e4m3 bytes up; shifting
-// yields them in the order 0, 2, 4, 6, 1, 3, 5, 7 (4 bits) or 0, 4, 8, 12, 1,
-// 5, ... (2 bits), and x's bytes are permuted the same way, since a sum over
-// k may be taken in any order as long as both operands agree.
+// Codes are expanded by shifts and a byte permutation that looks their e4m3
+// bytes up, and e4m3 bytes of both operands are widened two at a time by
+// v_cvt_scalef32_pk_bf16_fp8, which applies x's power of two.  Shifting yields
+// the codes in the order 0, 2, 4, 6, 1, 3, 5, 7 (4 bits) or 0, 4, 8, 12, 1, 5,
+// ... (2 bits), and x's bytes are permuted the same way, since a sum over k
+// may be taken in any order as long as both operands agree.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -35,7 +38,7 @@
 namespace gg {
 namespace {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
 // rows may start at any byte: the same loads, without the promise of alignment
@@ -74,7 +77,7 @@ __device__ __forceinline__ unsigned e4m3_of_2bit(unsigned c) {
 template <int BITS>
 constexpr float code_scale() { return BITS == 4 ? -0.5f : 0.5f; }
 
-// 16 codes (BITS / 2 dwords) as four registers of a matrix operand.
+// 16 codes (BITS / 2 dwords) as e4m3 bytes.
 template <int BITS>
 __device__ __forceinline__ v4u expand16(const unsigned *w) {
     v4u o;
@@ -105,31 +108,37 @@ __device__ __forceinline__ v4u shuffle16(const v4u &d) {
                perm(b1, a1, 0x05040100u), perm(b1, a1, 0x07060302u)};
 }
 
-__device__ __forceinline__ v8i join(const v4u &lo, const v4u &hi) {
-    return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-               (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
-
-// A: x (its powers of two in byte SEL of scale_a), B: W (unscaled); C = 0.
-template <int SEL>
-__device__ __forceinline__ v16f mfma(const v8i &a, const v8i &b, int scale_a) {
-    const v16f zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+// 8 e4m3 bytes times 2^(e - 127) as bf16 (e = 255: NaN).
+__device__ __forceinline__ v4u widen(unsigned lo, unsigned hi, unsigned e) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, zero, 0, 0, SEL, scale_a, 0, 127);
+    const float f = __uint_as_float(e << 23);         // only its exponent counts
+    const auto pk = [f](unsigned w, auto half) {
+        return __builtin_bit_cast(
+            unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, f, decltype(half)::value));
+    };
+    return v4u{pk(lo, std::false_type{}), pk(lo, std::true_type{}), pk(hi, std::false_type{}),
+               pk(hi, std::true_type{})};
 #else
-    return zero;
+    return v4u{0, 0, 0, 0};
 #endif
 }
 
-// The same over 128 columns, two weight groups (registers 0-3: the first
-// group, 4-7: the second; block b of 32 takes its power from lanes 16b ..
-// 16b + 15), for 16 rows of x by 16 rows of W.
-__device__ __forceinline__ v4f mfma16(const v8i &a, const v8i &b, int scale_a) {
-    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ v8b operand(const v4u &x) { return __builtin_bit_cast(v8b, x); }
+
+__device__ __forceinline__ v16f mfma(const v4u &a, const v4u &b, const v16f &c) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, scale_a, 0, 127);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(a), operand(b), c, 0, 0, 0);
 #else
-    return zero;
+    return c;
+#endif
+}
+
+// The same for 16 rows of x by 16 rows of W over 32 columns.
+__device__ __forceinline__ v4f mfma16(const v4u &a, const v4u &b, const v4f &c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(a), operand(b), c, 0, 0, 0);
+#else
+    return c;
 #endif
 }
 
@@ -146,17 +155,19 @@ __device__ __forceinline__ void load_bytes(unsigned (&d)[N / 4], const uint8_t *
     }
 }
 
-// 32 codes in one load of 16 (2-bit codes: 8) bytes.
-template <int BITS>
-__device__ __forceinline__ void load_codes(unsigned (&w)[BITS], const uint8_t *p) {
-    if constexpr (BITS == 4) {
+// D dwords in one load, from any byte.
+template <int D>
+__device__ __forceinline__ void load_codes(unsigned (&w)[D], const uint8_t *p) {
+    if constexpr (D == 4) {
         const v4u q = *reinterpret_cast<const v4u_any *>(p);
 #pragma unroll
         for (int d = 0; d < 4; ++d) w[d] = q[d];
-    } else {
+    } else if constexpr (D == 2) {
         const v2u q = *reinterpret_cast<const v2u_any *>(p);
         w[0] = q[0];
         w[1] = q[1];
+    } else {
+        w[0] = *reinterpret_cast<const u32_any *>(p);
     }
 }
 
@@ -252,11 +263,9 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
 
 // Up to 16 rows: bound by the codes' way from memory, with one row of x by
 // its latency.  No LDS on the way in: a lane loads 32 neighbouring codes of
-// its row of W and expands them in registers.  The 16 x 16 x 128 instruction
-// takes two weight groups, whose scales differ, so it runs once per group with
-// the other group's half of x zero; at 16 rows that costs the same time per
-// weight as 32 x 32 x 64 would, half the multiply-adds, and twice the
-// workgroups.
+// its row of W, half of each of two weight groups after an exchange between
+// lanes, and expands them in registers for the 16 x 16 x 32 instruction, which
+// gives twice the workgroups of 32 x 32 tiles.
 //
 // A workgroup owns 16 NH columns n (NH = 2 for an output in 8 bits, whose
 // blocks are 32 wide); its waves split into NH column sets by KW runs of
@@ -282,20 +291,23 @@ __device__ __forceinline__ void deal(unsigned (&w)[BITS]) {
 // One pair of groups, as loaded, and its products added to the sums.
 template <int BITS>
 struct Pair {
-    unsigned w[BITS], e, s;          // codes, x's power of two, both scales
+    unsigned w[BITS], e, s;          // codes, x's four powers of two, both scales
     v4u x[2];
 
-    __device__ __forceinline__ void multiply(v4f &acc) {
-        const v4u none = {0, 0, 0, 0};
+    __device__ __forceinline__ void multiply(int q, v4f &acc) {
         deal<BITS>(w);
-        const v8i b = join(expand16<BITS>(w), expand16<BITS>(w + BITS / 2));
-        const v4f r0 = mfma16(join(shuffle16<BITS>(x[0]), none), b, (int)e);
-        const v4f r1 = mfma16(join(none, shuffle16<BITS>(x[1])), b, (int)e);
-        const float s0 = (float)__builtin_bit_cast(_Float16, (uint16_t)s);
-        const float s1 = (float)__builtin_bit_cast(_Float16, (uint16_t)(s >> 16));
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            acc[r] = __builtin_fmaf(r1[r], s1, __builtin_fmaf(r0[r], s0, acc[r]));
+        for (int g = 0; g < 2; ++g) {
+            // 16 columns of block 2 g + q / 2
+            const unsigned eg = e >> (16 * g + 8 * (q >> 1)) & 255u;
+            const v4u b = expand16<BITS>(w + g * (BITS / 2)), a = shuffle16<BITS>(x[g]);
+            v4f r = {0.f, 0.f, 0.f, 0.f};
+            r = mfma16(widen(a[0], a[1], eg), widen(b[0], b[1], 127), r);
+            r = mfma16(widen(a[2], a[3], eg), widen(b[2], b[3], 127), r);
+            const float sg = (float)__builtin_bit_cast(_Float16, (uint16_t)(s >> (16 * g)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(r[i], sg, acc[i]);
+        }
     }
 };
 
@@ -313,7 +325,7 @@ struct Rows {
     }
     // N whole pairs, all loads in flight together
     template <int N>
-    __device__ __forceinline__ void run(v4f &acc) {
+    __device__ __forceinline__ void run(int q, v4f &acc) {
         Pair<BITS> p[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) load_codes<BITS>(p[i].w, w + i * (16 * BITS));
@@ -321,12 +333,12 @@ struct Rows {
         for (int i = 0; i < N; ++i) {
             p[i].x[0] = *reinterpret_cast<const v4u_any *>(x + i * 128);
             p[i].x[1] = *reinterpret_cast<const v4u_any *>(x + i * 128 + 64);
-            p[i].e = e[4 * i];
+            p[i].e = *reinterpret_cast<const u32_any *>(e + 4 * i);
             p[i].s = *reinterpret_cast<const u32_any *>(s + 2 * i);
         }
         advance(N);
 #pragma unroll
-        for (int i = 0; i < N; ++i) p[i].multiply(acc);
+        for (int i = 0; i < N; ++i) p[i].multiply(q, acc);
     }
     // the pair at hand, of which columns 0 .. left - 1 exist, byte by byte
     __device__ __forceinline__ void part(int64_t left, int q, v4f &acc) {
@@ -341,10 +353,12 @@ struct Rows {
             load_bytes<16>(d, x + 64 * g, have(64 * g + 16 * q, 16));
             p.x[g] = v4u{d[0], d[1], d[2], d[3]};
         }
-        p.e = left > 32 * q ? *e : 127u;
+        p.e = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) p.e |= (left > 32 * b ? (unsigned)e[b] : 127u) << (8 * b);
         p.s = (unsigned)s[0] | (left > 64 ? (unsigned)s[1] << 16 : 0u);
         advance(1);
-        p.multiply(acc);
+        p.multiply(q, acc);
     }
 };
 
@@ -364,14 +378,14 @@ __global__ __launch_bounds__(64 * NH * KW) void packed_rows_kernel(PackedLinear 
     // the pairs of it that exist in full
     int n = (int)max(min(end, (int64_t)a.K / 128) - first, (int64_t)0);
     Rows<BITS> rows = {a.Q + nrow * a.ldq + 4 * BITS * q, a.X + tok * a.ldx + 16 * q,
-                       a.XE + tok * a.ldxe + q, a.S + nrow * a.lds};
+                       a.XE + tok * a.ldxe, a.S + nrow * a.lds};
     rows.advance(first);
     v4f acc = {0.f, 0.f, 0.f, 0.f};
     int64_t p = first + n;
-    for (; n >= 4; n -= 4) rows.template run<4>(acc);
-    if (n == 3) rows.template run<3>(acc);
-    else if (n == 2) rows.template run<2>(acc);
-    else if (n == 1) rows.template run<1>(acc);
+    for (; n >= 4; n -= 4) rows.template run<4>(q, acc);
+    if (n == 3) rows.template run<3>(q, acc);
+    else if (n == 2) rows.template run<2>(q, acc);
+    else if (n == 1) rows.template run<1>(q, acc);
 #pragma unroll 1
     for (; p < end; ++p) rows.part(a.K - p * 128, q, acc);
 
@@ -397,13 +411,13 @@ hipError_t launch_rows(const PackedLinear &a, hipStream_t s) {
 
 // ---------------------------------------------------------------------------
 // More than 16 rows: a workgroup owns BM rows of x by BN columns n and walks k
-// in steps of 128 (two weight groups), double-buffered in LDS.  Bound by the
-// vector unit: 16 multiply-adds per matrix instruction (which takes as long),
-// and the expansion of the codes.
+// in steps of one weight group, 64, double-buffered in LDS as bf16.  Bound by
+// LDS traffic and the vector unit (expansion, widening, 16 multiply-adds per
+// block of 32 x 32 and group) about equally.
 //
-//  * Codes are expanded once per workgroup, on their way into LDS, and then
-//    feed the BM / 32 row blocks; x's bytes are permuted on the same way.
-//  * LDS rows hold 128 bytes, 8 chunks of 16; chunk c of row r lies at slot
+//  * Codes are expanded, and both operands widened, once per workgroup, on
+//    their way into LDS.
+//  * LDS rows hold 64 values, 8 chunks of 16 bytes; chunk c of row r lies at slot
 //    c ^ (r mod 8), so that the 16-byte fragment reads of 8 neighbouring
 //    rows, and the writes, meet no bank twice.
 //  * Loads run two steps ahead: registers hold the next step while LDS holds
@@ -412,14 +426,7 @@ hipError_t launch_rows(const PackedLinear &a, hipStream_t s) {
 //    its own stages, and their sums are added in group order.
 //  * The finished sums pass through LDS, so that bias, residual and the
 //    stores of Y run along rows, 16 bytes per lane.
-constexpr int STEP = 128;
-
-// The 16 bytes at `at` of a row of n bytes, zeros past its end.
-__device__ __forceinline__ v4u load_chunk(const uint8_t *p, int64_t at, int64_t n) {
-    unsigned d[4];
-    load_bytes<16>(d, p + at, (int)min(max(n - at, (int64_t)0), (int64_t)16));
-    return v4u{d[0], d[1], d[2], d[3]};
-}
+constexpr int STEP = 64, ROWB = 2 * STEP;   // columns of a step, bytes of an LDS row
 
 // KS groups of WR x WC waves, each wave with IB x JB blocks of 32 x 32.
 template <int BM, int BN, int WR, int WC, int KS, int BITS>
@@ -428,91 +435,89 @@ void packed_tile_kernel(PackedLinear a, int tiles_m) {
     constexpr int THREADS = 64 * WR * WC;             // of a group
     constexpr int IB = BM / WR / 32, JB = BN / WC / 32;
     static_assert(IB * WR * 32 == BM && JB * WC * 32 == BN, "waves must cover the tile");
-    constexpr int XC = BM * 8 / THREADS;              // chunks of x per thread
-    constexpr int CB = 4 * BITS;                      // bytes of 32 codes
-    constexpr int WPR = STEP / 32;                    // units of 32 codes per row and step
-    constexpr int WL = BN * WPR / THREADS;            // units per thread
-    static_assert(XC * THREADS == BM * 8 && WL * THREADS == BN * WPR, "loads must split evenly");
+    // a row's step is 4 units of 16 columns: 16 bytes of x, CB bytes of codes
+    constexpr int CB = 2 * BITS;
+    constexpr int XC = BM * 4 / THREADS, WL = BN * 4 / THREADS;   // units per thread
+    static_assert(XC * THREADS == BM * 4 && WL * THREADS == BN * 4, "loads must split evenly");
     static_assert(BM <= THREADS && BN <= THREADS, "one scale per thread");
-    constexpr int XBYTES = BM * STEP, WBYTES = BN * STEP, STAGE = XBYTES + WBYTES;
+    constexpr int XBYTES = BM * ROWB, WBYTES = BN * ROWB, STAGE = XBYTES + WBYTES;
     constexpr int TILE = BM * BN * 4;                 // a group's finished sums
     constexpr int SMEM = KS * (2 * STAGE > TILE ? 2 * STAGE : TILE);
     __shared__ __attribute__((aligned(16))) char smem[SMEM];
-    __shared__ unsigned all_scales[KS][2][BM + BN];   // x: 4 e8m0 bytes, W: 2 halves per step
+    __shared__ unsigned all_scales[KS][2][BN];        // W: a half per row and step
 
     const int grp = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / THREADS);
     const int tid = threadIdx.x % THREADS, lane = tid & 63, wave = tid >> 6, h = lane >> 5,
               l32 = lane & 31;
     char *const gsmem = smem + grp * 2 * STAGE;
-    unsigned(*const scales)[BM + BN] = all_scales[grp];
+    unsigned(*const scales)[BN] = all_scales[grp];
     int t = blockIdx.x;
     if ((gridDim.x & 7) == 0) t = (t & 7) * (gridDim.x >> 3) + (t >> 3);   // runs per XCD
     const int64_t m0 = (int64_t)(t % tiles_m) * BM;
     const int64_t n0 = (int64_t)(t / tiles_m) * BN;
     const int wm = wave / WC * (32 * IB), wn = wave % WC * (32 * JB);
 
-    const uint8_t *px[XC], *pw[WL];
+    const int unit = tid % 4;
+    const uint8_t *px[XC], *pe[XC], *pw[WL];
 #pragma unroll
-    for (int i = 0; i < XC; ++i) px[i] = a.X + min(m0 + tid / 8 + THREADS / 8 * i, (int64_t)a.M - 1) * a.ldx;
+    for (int i = 0; i < XC; ++i) {
+        const int64_t row = min(m0 + tid / 4 + THREADS / 4 * i, (int64_t)a.M - 1);
+        px[i] = a.X + row * a.ldx + 16 * unit;
+        pe[i] = a.XE + row * a.ldxe + unit / 2;
+    }
 #pragma unroll
     for (int i = 0; i < WL; ++i)
-        pw[i] = a.Q + min(n0 + tid / WPR + THREADS / WPR * i, (int64_t)a.N - 1) * a.ldq;
-    // threads below BM fetch a row's powers of two, the next BN a row's scales
-    const bool fetch_e = tid < BM, fetch_s = tid >= THREADS - BN;
-    const uint8_t *pe = a.XE + min(m0 + (fetch_e ? tid : 0), (int64_t)a.M - 1) * a.ldxe;
-    const uint16_t *ps = a.S + min(n0 + (fetch_s ? tid - (THREADS - BN) : 0), (int64_t)a.N - 1) * a.lds;
-    const int64_t kb = ((int64_t)a.K * BITS + 7) / 8;
-    const int64_t eb = ((int64_t)a.K + 31) / 32, sb = ((int64_t)a.K + 63) / 64;
+        pw[i] = a.Q + min(n0 + tid / 4 + THREADS / 4 * i, (int64_t)a.N - 1) * a.ldq + CB * unit;
+    // the first BN threads fetch a row's scale
+    const bool fetch_s = tid < BN;
+    const uint16_t *ps = a.S + min(n0 + (fetch_s ? tid : 0), (int64_t)a.N - 1) * a.lds;
 
     v4u xr[XC];
-    unsigned wr[WL][BITS];
-    unsigned er = 0, sr = 0;
-    // the step at k0; `full` (uniform): all of its 128 columns exist
+    unsigned wr[WL][BITS / 2], er[XC], sr = 0;
+    // the step at k0; `full` (uniform): all of its 64 columns exist
     auto load = [&](int64_t k0, bool full) {
-        const int64_t b = k0 / 32, g = k0 / 64;
+        const int64_t kq = k0 * BITS / 8;
         if (full) {
 #pragma unroll
-            for (int i = 0; i < XC; ++i)
-                xr[i] = *reinterpret_cast<const v4u_any *>(px[i] + k0 + 16 * (tid % 8));
+            for (int i = 0; i < WL; ++i) load_codes<BITS / 2>(wr[i], pw[i] + kq);
 #pragma unroll
-            for (int i = 0; i < WL; ++i) load_codes<BITS>(wr[i], pw[i] + k0 * BITS / 8 + CB * (tid % WPR));
-            if (fetch_e) er = *reinterpret_cast<const u32_any *>(pe + b);
-            if (fetch_s) sr = *reinterpret_cast<const u32_any *>(ps + g);
-        } else {
-#pragma unroll
-            for (int i = 0; i < XC; ++i) xr[i] = load_chunk(px[i], k0 + 16 * (tid % 8), a.K);
-#pragma unroll
-            for (int i = 0; i < WL; ++i) {
-                const int64_t at = k0 * BITS / 8 + CB * (tid % WPR);
-                load_bytes<CB>(wr[i], pw[i] + at, (int)min(max(kb - at, (int64_t)0), (int64_t)CB));
+            for (int i = 0; i < XC; ++i) {
+                xr[i] = *reinterpret_cast<const v4u_any *>(px[i] + k0);
+                er[i] = pe[i][k0 / 32];
             }
-            er = sr = 0;
-            if (fetch_e)
-                for (int i = 0; i < 4; ++i) er |= (b + i < eb ? (unsigned)pe[b + i] : 127u) << (8 * i);
-            if (fetch_s) sr = (unsigned)ps[g] | (g + 1 < sb ? (unsigned)ps[g + 1] << 16 : 0u);
+        } else {
+            const int left = (int)(a.K - k0) - 16 * unit;          // columns of this unit on
+#pragma unroll
+            for (int i = 0; i < WL; ++i)
+                load_bytes<CB>(wr[i], pw[i] + kq, (min(max(left, 0), 16) * BITS + 7) / 8);
+#pragma unroll
+            for (int i = 0; i < XC; ++i) {
+                unsigned d[4];
+                load_bytes<16>(d, px[i] + k0, left);
+                xr[i] = v4u{d[0], d[1], d[2], d[3]};
+                er[i] = left > 0 ? pe[i][k0 / 32] : 127u;
+            }
         }
+        if (fetch_s) sr = ps[k0 / 64];
     };
-    auto slot = [](int row, int c) { return row * STEP + ((c ^ (row & 7)) * 16); };
+    auto slot = [](int row, int c) { return row * ROWB + ((c ^ (row & 7)) * 16); };
+    auto put = [&](char *base, int row, const v4u &bytes, unsigned e) {
+        *reinterpret_cast<v4u *>(base + slot(row, 2 * unit)) = widen(bytes[0], bytes[1], e);
+        *reinterpret_cast<v4u *>(base + slot(row, 2 * unit + 1)) = widen(bytes[2], bytes[3], e);
+    };
     auto store = [&](int buf) {
         char *xs = gsmem + buf * STAGE, *ws = xs + XBYTES;
 #pragma unroll
         for (int i = 0; i < XC; ++i)
-            *reinterpret_cast<v4u *>(xs + slot(tid / 8 + THREADS / 8 * i, tid % 8)) = shuffle16<BITS>(xr[i]);
+            put(xs, tid / 4 + THREADS / 4 * i, shuffle16<BITS>(xr[i]), er[i]);
 #pragma unroll
-        for (int i = 0; i < WL; ++i) {
-            const int row = tid / WPR + THREADS / WPR * i;
-            const int c = 2 * (tid % WPR);
-            *reinterpret_cast<v4u *>(ws + slot(row, c)) = expand16<BITS>(wr[i]);
-            *reinterpret_cast<v4u *>(ws + slot(row, c + 1)) = expand16<BITS>(wr[i] + BITS / 2);
-        }
-        if (fetch_e) scales[buf][tid] = er;
-        if (fetch_s) scales[buf][BM + tid - (THREADS - BN)] = sr;
+        for (int i = 0; i < WL; ++i)
+            put(ws, tid / 4 + THREADS / 4 * i, expand16<BITS>(wr[i]), 127);
+        if (fetch_s) scales[buf][tid] = sr;
     };
-    // an operand of group g: chunks 4g + h and 4g + 2 + h of the lane's row
-    auto frag = [&](const char *base, int row, int g) {
-        const v4u lo = *reinterpret_cast<const v4u *>(base + slot(row, 4 * g + h));
-        const v4u hi = *reinterpret_cast<const v4u *>(base + slot(row, 4 * g + 2 + h));
-        return join(lo, hi);
+    // the operand of 16 columns: part t of the lane's row
+    auto frag = [&](const char *base, int row, int t) {
+        return *reinterpret_cast<const v4u *>(base + slot(row, 2 * t + h));
     };
 
     v16f acc[IB][JB];
@@ -547,39 +552,39 @@ void packed_tile_kernel(PackedLinear a, int tiles_m) {
             continue;
         }
         const char *xs = gsmem + buf * STAGE, *ws = xs + XBYTES;
-        unsigned e[IB], s2[JB];
+        float s[JB];
 #pragma unroll
-        for (int i = 0; i < IB; ++i) e[i] = scales[buf][wm + 32 * i + l32] >> (8 * h);
+        for (int j = 0; j < JB; ++j)
+            s[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)scales[buf][wn + 32 * j + l32]);
+        v4u fx[IB][4], fw[JB][4];
 #pragma unroll
-        for (int j = 0; j < JB; ++j) s2[j] = scales[buf][BM + wn + 32 * j + l32];
-        // Products and the multiply-adds of the ones before them alternate, two
-        // result tuples in turn: a matrix instruction runs for as long as 16
-        // multiply-adds of a wave, so neither unit waits for the other.
-        v8i fx[2][IB], fw[2][JB];
-        auto fetch = [&](int g) {
+        for (int t = 0; t < 4; ++t) {
 #pragma unroll
-            for (int i = 0; i < IB; ++i) fx[g][i] = frag(xs, wm + 32 * i + l32, g);
+            for (int i = 0; i < IB; ++i) fx[i][t] = frag(xs, wm + 32 * i + l32, t);
 #pragma unroll
-            for (int j = 0; j < JB; ++j) fw[g][j] = frag(ws, wn + 32 * j + l32, g);
-        };
+            for (int j = 0; j < JB; ++j) fw[j][t] = frag(ws, wn + 32 * j + l32, t);
+        }
+        // A block's products and the multiply-adds of the block before it
+        // alternate, two result tuples in turn, so neither unit waits for the
+        // other.
         v16f p[2];
-        constexpr int BLOCKS = 2 * IB * JB;
-        fetch(0);
+        constexpr int BLOCKS = IB * JB;
 #pragma unroll
         for (int b = 0; b <= BLOCKS; ++b) {
             if (b < BLOCKS) {
-                const int g = b / (IB * JB), i = b % IB, j = b / IB % JB;
-                p[b & 1] = g == 0 ? mfma<0>(fx[g][i], fw[g][j], (int)e[i])
-                                  : mfma<2>(fx[g][i], fw[g][j], (int)e[i]);
+                v16f q;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) q[r] = 0.f;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) q = mfma(fx[b % IB][t], fw[b / IB][t], q);
+                p[b & 1] = q;
             }
-            if (b == 0) fetch(1);
             __builtin_amdgcn_sched_barrier(0);
             if (b > 0) {
-                const int c = b - 1, g = c / (IB * JB), i = c % IB, j = c / IB % JB;
-                const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)(s2[j] >> (16 * g)));
+                const int c = b - 1, i = c % IB, j = c / IB;
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    acc[i][j][r] = __builtin_fmaf(p[c & 1][r], s, acc[i][j][r]);
+                    acc[i][j][r] = __builtin_fmaf(p[c & 1][r], s[j], acc[i][j][r]);
                 // a use here, or all of this moves past the stores and the
                 // barrier below
                 asm volatile("" : "+v"(acc[i][j]));
