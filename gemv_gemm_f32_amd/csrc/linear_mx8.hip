@@ -142,6 +142,17 @@ __device__ __forceinline__ v4f mfma16(const v4u &a, const v4u &b, const v4f &c) 
 #endif
 }
 
+// A weight scale as fp32, in a register of its own: left to itself the compiler
+// folds the conversion into every multiply-add, and the mixed-precision form
+// takes 4.4 cycles a wave where the plain one takes 2.8.
+__device__ __forceinline__ float scale_of(unsigned half) {
+    float s = (float)__builtin_bit_cast(_Float16, (uint16_t)half);
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(s));
+#endif
+    return s;
+}
+
 // N bytes from p, of which `have` exist; the rest reads as zeros.
 template <int N>
 __device__ __forceinline__ void load_bytes(unsigned (&d)[N / 4], const uint8_t *p, int have) {
@@ -304,7 +315,7 @@ struct Pair {
             v4f r = {0.f, 0.f, 0.f, 0.f};
             r = mfma16(widen(a[0], a[1], eg), widen(b[0], b[1], 127), r);
             r = mfma16(widen(a[2], a[3], eg), widen(b[2], b[3], 127), r);
-            const float sg = (float)__builtin_bit_cast(_Float16, (uint16_t)(s >> (16 * g)));
+            const float sg = scale_of(s >> (16 * g));
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(r[i], sg, acc[i]);
         }
@@ -412,8 +423,8 @@ hipError_t launch_rows(const PackedLinear &a, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // More than 16 rows: a workgroup owns BM rows of x by BN columns n and walks k
 // in steps of one weight group, 64, double-buffered in LDS as bf16.  Bound by
-// LDS traffic and the vector unit (expansion, widening, 16 multiply-adds per
-// block of 32 x 32 and group) about equally.
+// the latency of a step (LDS, expansion, products and barrier in turn) where
+// tiles are few, which is where these are used.
 //
 //  * Codes are expanded, and both operands widened, once per workgroup, on
 //    their way into LDS.
@@ -474,31 +485,32 @@ void packed_tile_kernel(PackedLinear a, int tiles_m) {
 
     v4u xr[XC];
     unsigned wr[WL][BITS / 2], er[XC], sr = 0;
-    // the step at k0; `full` (uniform): all of its 64 columns exist
-    auto load = [&](int64_t k0, bool full) {
-        const int64_t kq = k0 * BITS / 8;
-        if (full) {
+    // a step whose 64 columns all exist, and the last one, cut short by K
+    auto load = [&](int64_t step) {
+        const int64_t k0 = step * STEP, kq = k0 * BITS / 8;
 #pragma unroll
-            for (int i = 0; i < WL; ++i) load_codes<BITS / 2>(wr[i], pw[i] + kq);
+        for (int i = 0; i < WL; ++i) load_codes<BITS / 2>(wr[i], pw[i] + kq);
 #pragma unroll
-            for (int i = 0; i < XC; ++i) {
-                xr[i] = *reinterpret_cast<const v4u_any *>(px[i] + k0);
-                er[i] = pe[i][k0 / 32];
-            }
-        } else {
-            const int left = (int)(a.K - k0) - 16 * unit;          // columns of this unit on
-#pragma unroll
-            for (int i = 0; i < WL; ++i)
-                load_bytes<CB>(wr[i], pw[i] + kq, (min(max(left, 0), 16) * BITS + 7) / 8);
-#pragma unroll
-            for (int i = 0; i < XC; ++i) {
-                unsigned d[4];
-                load_bytes<16>(d, px[i] + k0, left);
-                xr[i] = v4u{d[0], d[1], d[2], d[3]};
-                er[i] = left > 0 ? pe[i][k0 / 32] : 127u;
-            }
+        for (int i = 0; i < XC; ++i) {
+            xr[i] = *reinterpret_cast<const v4u_any *>(px[i] + k0);
+            er[i] = pe[i][k0 / 32];
         }
-        if (fetch_s) sr = ps[k0 / 64];
+        sr = ps[step];
+    };
+    auto load_part = [&](int64_t step) {
+        const int64_t k0 = step * STEP;
+        const int left = (int)(a.K - k0) - 16 * unit;              // columns of this unit on
+#pragma unroll
+        for (int i = 0; i < WL; ++i)
+            load_bytes<CB>(wr[i], pw[i] + k0 * BITS / 8, (min(max(left, 0), 16) * BITS + 7) / 8);
+#pragma unroll
+        for (int i = 0; i < XC; ++i) {
+            unsigned d[4];
+            load_bytes<16>(d, px[i] + k0, left);
+            xr[i] = v4u{d[0], d[1], d[2], d[3]};
+            er[i] = left > 0 ? pe[i][k0 / 32] : 127u;
+        }
+        sr = ps[step];
     };
     auto slot = [](int row, int c) { return row * ROWB + ((c ^ (row & 7)) * 16); };
     auto put = [&](char *base, int row, const v4u &bytes, unsigned e) {
@@ -528,34 +540,12 @@ void packed_tile_kernel(PackedLinear a, int tiles_m) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-    // this group's steps start at first, first + HOP, ...; every group goes
-    // through the same number of rounds
-    constexpr int HOP = STEP * KS;
-    const int64_t first = (int64_t)grp * STEP;
-    auto fetch_step = [&](int64_t k0) {
-        if (k0 < a.K) load(k0, k0 + STEP <= a.K);
-    };
-    fetch_step(first);
-    if (first < a.K) store(0);
-    fetch_step(first + HOP);
-    __syncthreads();
-    int buf = 0;
-    for (int64_t r0 = 0; r0 < a.K; r0 += HOP, buf ^= 1) {
-        const int64_t k0 = r0 + first;
-        // the next step's data, in registers since the last step, go to the
-        // stage that the last step read, and the loads of the one after it
-        // have this whole step to arrive
-        if (k0 + HOP < a.K) store(buf ^ 1);
-        fetch_step(k0 + 2 * HOP);
-        if (KS > 1 && k0 >= a.K) {                    // uniform: no step in the last round
-            __syncthreads();
-            continue;
-        }
+    auto multiply = [&](int buf) {
         const char *xs = gsmem + buf * STAGE, *ws = xs + XBYTES;
         float s[JB];
 #pragma unroll
         for (int j = 0; j < JB; ++j)
-            s[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)scales[buf][wn + 32 * j + l32]);
+            s[j] = scale_of(scales[buf][wn + 32 * j + l32]);
         v4u fx[IB][4], fw[JB][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -591,6 +581,36 @@ void packed_tile_kernel(PackedLinear a, int tiles_m) {
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+    };
+
+    // Group g takes the steps g, g + KS, ...; every group goes through the same
+    // number of rounds.  The next step's data, in registers since the last
+    // round, go to the stage that the last round read, and the loads of the one
+    // after it have this whole round to arrive: they are unconditional (past
+    // the end, the last whole step again), because a load under a branch is
+    // waited for where the branch joins.
+    const int64_t whole = a.K / STEP;
+    int buf = 0;
+    if (whole > 0) {
+        load(min((int64_t)grp, whole - 1));
+        store(0);
+        load(min((int64_t)grp + KS, whole - 1));
+        __syncthreads();
+        for (int64_t s0 = 0; s0 < whole; s0 += KS, buf ^= 1) {
+            store(buf ^ 1);
+            load(min(s0 + grp + 2 * KS, whole - 1));
+            if (KS == 1 || s0 + grp < whole) multiply(buf);        // uniform
+            __syncthreads();
+        }
+    }
+    if (a.K % STEP) {                                 // one more, cut short
+        const bool mine = KS == 1 || whole % KS == grp;
+        if (mine) {
+            load_part(whole);
+            store(buf);
+        }
+        __syncthreads();
+        if (mine) multiply(buf);
         __syncthreads();
     }
 
@@ -616,6 +636,192 @@ void packed_tile_kernel(PackedLinear a, int tiles_m) {
             y += *reinterpret_cast<const v4f *>(tile + g * BM * BN + cell(row, col));
         return y;
     });
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: NW waves, each with 32 columns n of its own and all BM rows of x.
+// A wave expands its own codes in registers, so W needs no LDS and each code
+// feeds BM / 32 blocks; only x passes through LDS, 128 columns at a time.
+// Lanes 0-31 hold codes 0-31 of a group, lanes 32-63 codes 32-63: part t of a
+// group multiplies columns 8 t .. 8 t + 7 of either half.  At BM = 128 the
+// matrix unit (4 x 4 x 32 cycles per wave and group), the vector unit (64
+// instructions of expansion, 64 multiply-adds) and LDS (16 KiB per wave) have
+// about equally much to do; 2048 x 4096 x 4096 runs at 770 TFLOP/s, the
+// matrix unit busy for a third of the time.  MW: waves per SIMD that the
+// registers leave room for; a SIMD issues vector instructions of one wave
+// every 7 cycles, of two or more every 3 to 4.
+constexpr int SPAN = 128, SPANB = 2 * SPAN;           // columns of x in a stage, bytes of a row
+
+template <int BM, int NW, int BITS, int MW = 2>
+__global__ __launch_bounds__(64 * NW, MW) void packed_wide_kernel(PackedLinear a, int tiles_m) {
+    constexpr int THREADS = 64 * NW, BN = 32 * NW, IB = BM / 32;
+    constexpr int XC = BM * (SPAN / 16) / THREADS;    // units of 16 columns of x per thread
+    static_assert(XC * THREADS == BM * (SPAN / 16), "loads must split evenly");
+    constexpr int STAGE = BM * SPANB, TILE = BM * BN * 4;
+    constexpr int SMEM = 2 * STAGE > TILE ? 2 * STAGE : TILE;
+    __shared__ __attribute__((aligned(16))) char smem[SMEM];
+
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tb = blockIdx.x;
+    if ((gridDim.x & 7) == 0) tb = (tb & 7) * (gridDim.x >> 3) + (tb >> 3);   // runs per XCD
+    const int64_t m0 = (int64_t)(tb % tiles_m) * BM, n0 = (int64_t)(tb / tiles_m) * BN;
+
+    const int unit = tid % 8;                         // THREADS is a multiple of 8
+    const uint8_t *px[XC], *pe[XC];
+#pragma unroll
+    for (int i = 0; i < XC; ++i) {
+        const int64_t row = min(m0 + (tid + THREADS * i) / 8, (int64_t)a.M - 1);
+        px[i] = a.X + row * a.ldx + 16 * unit;
+        pe[i] = a.XE + row * a.ldxe + unit / 2;
+    }
+    const int64_t nrow = min(n0 + 32 * wave + l32, (int64_t)a.N - 1);
+    const uint8_t *pq = a.Q + nrow * a.ldq + 4 * BITS * h;
+    const uint16_t *ps = a.S + nrow * a.lds;
+
+    v4u xr[XC];
+    unsigned er[XC];
+    // a span whose 128 columns all exist, and the last one, cut short by K
+    auto load_x = [&](int64_t span) {
+        const int64_t k0 = span * SPAN;
+#pragma unroll
+        for (int i = 0; i < XC; ++i) {
+            xr[i] = *reinterpret_cast<const v4u_any *>(px[i] + k0);
+            er[i] = pe[i][k0 / 32];
+        }
+    };
+    auto load_x_part = [&](int64_t span) {
+        const int64_t k0 = span * SPAN;
+        const int left = (int)(a.K - k0) - 16 * unit;
+#pragma unroll
+        for (int i = 0; i < XC; ++i) {
+            unsigned d[4];
+            load_bytes<16>(d, px[i] + k0, left);
+            xr[i] = v4u{d[0], d[1], d[2], d[3]};
+            er[i] = left > 0 ? pe[i][k0 / 32] : 127u;
+        }
+    };
+    auto slot = [](int row, int c) { return row * SPANB + ((c ^ (row & 15)) * 16); };
+    auto store_x = [&](int buf) {
+        char *xs = smem + buf * STAGE;
+#pragma unroll
+        for (int i = 0; i < XC; ++i) {
+            const int row = (tid + THREADS * i) / 8;
+            const v4u b = shuffle16<BITS>(xr[i]);
+            *reinterpret_cast<v4u *>(xs + slot(row, 2 * unit)) = widen(b[0], b[1], er[i]);
+            *reinterpret_cast<v4u *>(xs + slot(row, 2 * unit + 1)) = widen(b[2], b[3], er[i]);
+        }
+    };
+    // codes and scales of the two groups of a span
+    struct Codes {
+        unsigned w[2][BITS];
+        unsigned s[2];
+    };
+    auto load_w = [&](int64_t span, Codes &c) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            load_codes<BITS>(c.w[g], pq + (span * SPAN + 64 * g) * BITS / 8);
+            c.s[g] = ps[2 * span + g];
+        }
+    };
+    auto load_w_part = [&](int64_t span, Codes &c) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int64_t k0 = span * SPAN + 64 * g;
+            const int left = (int)(a.K - k0);
+            load_bytes<4 * BITS>(c.w[g], pq + k0 * BITS / 8,
+                                 (min(max(left - 32 * h, 0), 32) * BITS + 7) / 8);
+            c.s[g] = left > 0 ? ps[2 * span + g] : 0u;
+        }
+    };
+
+    v16f acc[IB];
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+
+    auto multiply = [&](int buf, Codes &c) {
+        const char *xs = smem + buf * STAGE;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const float s = scale_of(c.s[g]);
+            v4u fw[4];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const v4u e = expand16<BITS>(c.w[g] + v * (BITS / 2));
+                fw[2 * v] = widen(e[0], e[1], 127);
+                fw[2 * v + 1] = widen(e[2], e[3], 127);
+            }
+#pragma unroll
+            for (int i = 0; i < IB; ++i) {
+                v4u fx[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    fx[t] = *reinterpret_cast<const v4u *>(xs + slot(32 * i + l32, 8 * g + 4 * h + t));
+                v16f q;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) q[r] = 0.f;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) q = mfma(fx[t], fw[t], q);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][r] = __builtin_fmaf(q[r], s, acc[i][r]);
+                // a use here, or all of this moves past the barrier
+                asm volatile("" : "+v"(acc[i]));
+            }
+        }
+    };
+
+    // as in the kernel above: x two spans ahead, codes one, loads unconditional
+    const int64_t whole = a.K / SPAN;
+    int buf = 0;
+    Codes cur;
+    if (whole > 0) {
+        load_x(0);
+        load_w(0, cur);
+        store_x(0);
+        load_x(min((int64_t)1, whole - 1));
+        __syncthreads();
+        for (int64_t span = 0; span < whole; ++span, buf ^= 1) {
+            Codes next;
+            load_w(min(span + 1, whole - 1), next);
+            store_x(buf ^ 1);
+            load_x(min(span + 2, whole - 1));
+            multiply(buf, cur);
+            __syncthreads();
+            cur = next;
+        }
+    }
+    if (a.K % SPAN) {                                 // one more, cut short
+        load_x_part(whole);
+        load_w_part(whole, cur);
+        store_x(buf);
+        __syncthreads();
+        multiply(buf, cur);
+        __syncthreads();
+    }
+
+    // sums to LDS, as in the kernel above
+    float *tile = reinterpret_cast<float *>(smem);
+    auto cell = [](int row, int col) { return row * BN + (col ^ ((row & 7) << 2)); };
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            tile[cell(32 * i + 8 * (r >> 2) + 4 * h + (r & 3), 32 * wave + l32)] =
+                acc[i][r] * code_scale<BITS>();
+    __syncthreads();
+    finish_tile<BM, BN, THREADS>(a, m0, n0, tid, [&](int row, int col) {
+        return *reinterpret_cast<const v4f *>(tile + cell(row, col));
+    });
+}
+
+template <int BM, int NW, int BITS, int MW = 2>
+hipError_t launch_wide(const PackedLinear &a, hipStream_t s) {
+    const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + 32 * NW - 1) / (32 * NW);
+    if (tm * tn * 64 * NW > UINT32_MAX) return hipErrorInvalidValue;
+    return launch(packed_wide_kernel<BM, NW, BITS, MW>, dim3((unsigned)(tm * tn)), dim3(64 * NW), s, a,
+                  (int)tm);
 }
 
 template <int BM, int BN, int WR, int WC, int KS, int BITS>
@@ -647,25 +853,25 @@ hipError_t launch_bits(const PackedLinear &a, int num_cus, hipStream_t s) {
         if (count(16, 16) >= cus) return launch_rows<BITS, 1, 4>(a, s);
         return lengthy ? launch_rows<BITS, 1, 16>(a, s) : launch_rows<BITS, 1, 8>(a, s);
     }
-    // More rows: tiles by how they fill the CUs (4 bits, us).
-    //  - 256 x 128 where a round of them leaves at most a fifth of the CUs idle:
-    //    2048 x 4096 x 4096 67 against 85 in 128 x 64;
-    //  - 32 x 64 in four k-groups where they fit one per CU: 128 x 4096 x 4096
-    //    13.9 against 17.4 in 64 x 64, 500 x 768 x 768 6.3 against 7.9;
-    //  - 64 x 64 in four k-groups, one per CU (64 x 12288 x 1536 10.5 against
-    //    11.0 in two and 13.3 in one, 500 x 1536 x 12288 39 / 48 / 69), in two
-    //    at two per CU (128 x 12288 x 1536 14.4 against 18.8 in four and 15.9
-    //    in one), and in one at three (256 x 12288 x 1536 19.5 against 21.3 in
-    //    two and 22.2 in 128 x 64);
-    //  - else 128 x 64 (500 x 12288 x 1536 28.9 against 33.8 in 64 x 64).
-    const int64_t big = count(256, 128), mid = count(64, 64);
+    // More rows, by how the tiles fill the CUs (4 bits, us):
+    //  - a wave per 32 columns, 128 x 256 tiles, where a round of them leaves at
+    //    most a fifth of the CUs idle: 2048 x 4096 x 4096 89 against 107 in
+    //    64 x 128 tiles and 156 in 64 x 64;
+    //  - 32 x 64 tiles in four k-groups where they fit one per CU: 128 x 4096 x
+    //    4096 18.5 against 22.7 in 64 x 64;
+    //  - 64 x 64 in four k-groups, one per CU (64 x 12288 x 1536 12.6 against
+    //    13.2 in two and 17 in one; 500 x 1536 x 12288 56 / 70 / 103), in two at
+    //    two per CU (128 x 12288 x 1536 18.6 against 22.7 in four, and 19.9 in
+    //    64 x 128 with a wave per 32 columns);
+    //  - else 64 x 128 with a wave per 32 columns (256 x 12288 x 1536 25.8
+    //    against 26.8 in 64 x 64; 500 x 12288 x 1536 36.3 against 47).
+    const int64_t big = count(128, 256), mid = count(64, 64);
     if (big >= cus && 4 * ((big + cus - 1) / cus * cus) <= 5 * big)
-        return launch_tiles<256, 128, 4, 2, 1, BITS>(a, s);
+        return launch_wide<128, 8, BITS, 2>(a, s);
     if (count(32, 64) <= cus) return launch_tiles<32, 64, 1, 2, 4, BITS>(a, s);
     if (mid <= cus) return launch_tiles<64, 64, 2, 2, 4, BITS>(a, s);
     if (mid <= 2 * cus) return launch_tiles<64, 64, 2, 2, 2, BITS>(a, s);
-    if (mid <= 3 * cus) return launch_tiles<64, 64, 2, 2, 1, BITS>(a, s);
-    return launch_tiles<128, 64, 2, 2, 1, BITS>(a, s);
+    return launch_wide<64, 4, BITS, 3>(a, s);
 }
 
 }  // namespace
