@@ -135,9 +135,15 @@ def header_functions(path: str = HEADER):
 
 # ------------------------------------------------------------ tensor side --
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -412,7 +418,7 @@ def _arg(t, shape, dtype, name, dev):
         return None, 0
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
     if t.get_device() != dev:
         raise ValueError("%s must be on the current GPU device" % name)
@@ -421,7 +427,24 @@ def _arg(t, shape, dtype, name, dev):
         raise ValueError("%s must have a contiguous last dimension" % name)
     if len(shape) == 1:
         return t.data_ptr(), shape[0]
-    return t.data_ptr(), st[0] if shape[0] > 1 else max(shape[1], 1)
+    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] or 1
+
+
+def _wide(t, rows, cols, dtype, name, dev):
+    """As _arg for rows of at least `cols` entries."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] < cols:
+        raise ValueError("%s must be 2-D with at least %d columns" % (name, cols))
+    return _arg(t, (rows, shape[1]), dtype, name, dev)
+
+
+def _out(t, shape, dtype, name, dev, like, stream):
+    """An output and its (address, leading dimension): the one given, checked,
+    or a new one."""
+    if t is None:
+        t = _new(shape, dtype, like, stream)
+        return t, t.data_ptr(), shape[-1] or 1
+    return (t, *_arg(t, shape, dtype, name, dev))
 
 
 def _new(shape, dtype, like, stream):
@@ -485,9 +508,7 @@ def linear_f32(X, W, bias=None, act="none", residual=None, Z=None, Y=None, trans
     pb, _ = _arg(bias, (N,), f32, "bias", dev)
     pr, ldr = _arg(residual, (M, N), f32, "residual", dev)
     pz, ldz = _arg(Z, (M, N), f32, "Z", dev)
-    if Y is None:
-        Y = _new((M, N), f32, X, stream)
-    py, ldy = _arg(Y, (M, N), f32, "Y", dev)
+    Y, py, ldy = _out(Y, (M, N), f32, "Y", dev, X, stream)
     _check(load().linear_f32(int(bool(trans_w)), _activation(act), M, N, K, px, ldx, pw, ldw, pb,
                              pr, ldr, pz, ldz, py, ldy, _stream(stream)), "linear_f32")
     return Y
@@ -522,12 +543,10 @@ def linear_f32_bwd(dY, X, W, Z=None, act="none", trans_w=False, dX=None, dW=None
     pz, ldz = _arg(Z if a else None, (M, N), f32, "Z", dev)
     px, ldx = _arg(X, (M, K), f32, "X", dev)
     pw, ldw = _arg(W, wshape, f32, "W", dev)
-    dX = None if not wx else _new((M, K), f32, dY, stream) if dX is None else dX
-    dW = None if not ww else _new(wshape, f32, dY, stream) if dW is None else dW
-    db = None if not wb else _new((N,), f32, dY, stream) if db is None else db
-    pdx, lddx = _arg(dX, (M, K), f32, "dX", dev)
-    pdw, lddw = _arg(dW, wshape, f32, "dW", dev)
-    pdb, _ = _arg(db, (N,), f32, "db", dev)
+    none = (None, None, 0)
+    dX, pdx, lddx = _out(dX, (M, K), f32, "dX", dev, dY, stream) if wx else none
+    dW, pdw, lddw = _out(dW, wshape, f32, "dW", dev, dY, stream) if ww else none
+    db, pdb, _ = _out(db, (N,), f32, "db", dev, dY, stream) if wb else none
     need = _ws_size("linear_f32_bwd_ws_size", a, M, N)
     keep, pws, nws = _workspace(workspace, need, dev, dY, stream)
     _check(load().linear_f32_bwd(int(bool(trans_w)), a, int(bool(accumulate)), M, N, K, pd, lddy,
@@ -547,13 +566,11 @@ def rmsnorm_f32(X, gamma=None, eps=1e-5, residual=None, S=None, Y=None, rstd=Non
     px, ldx = _arg(X, (M, K), f32, "X", dev)
     pr, ldr = _arg(residual, (M, K), f32, "residual", dev)
     pg, _ = _arg(gamma, (K,), f32, "gamma", dev)
-    if S is None and residual is not None:
-        S = _new((M, K), f32, X, stream)
-    Y = _new((M, K), f32, X, stream) if Y is None else Y
-    rstd = _new((M,), f32, X, stream) if rstd is None else rstd
-    ps, lds = _arg(S, (M, K), f32, "S", dev)
-    py, ldy = _arg(Y, (M, K), f32, "Y", dev)
-    pt, _ = _arg(rstd, (M,), f32, "rstd", dev)
+    ps = lds = 0
+    if S is not None or residual is not None:
+        S, ps, lds = _out(S, (M, K), f32, "S", dev, X, stream)
+    Y, py, ldy = _out(Y, (M, K), f32, "Y", dev, X, stream)
+    rstd, pt, _ = _out(rstd, (M,), f32, "rstd", dev, X, stream)
     _check(load().rmsnorm_f32(M, K, px, ldx, pr, ldr, pg, float(eps), ps, lds, py, ldy, pt,
                               _stream(stream)), "rmsnorm_f32")
     return Y, X if S is None else S, rstd
@@ -577,13 +594,11 @@ def rmsnorm_mx8(X, gamma=None, eps=1e-5, residual=None, S=None, Q=None, E=None, 
     px, ldx = _arg(X, (M, K), f32, "X", dev)
     pr, ldr = _arg(residual, (M, K), f32, "residual", dev)
     pg, _ = _arg(gamma, (K,), f32, "gamma", dev)
-    if S is None and residual is not None:
-        S = _new((M, K), f32, X, stream)
-    Q = _new((M, K), u8, X, stream) if Q is None else _bytes(Q)
-    E = _new((M, -(-K // 32)), u8, X, stream) if E is None else _bytes(E)
-    ps, lds = _arg(S, (M, K), f32, "S", dev)
-    pq, ldq = _arg(Q, (M, K), u8, "Q", dev)
-    pe, lde = _arg(E, (M, -(-K // 32)), u8, "E", dev)
+    ps = lds = 0
+    if S is not None or residual is not None:
+        S, ps, lds = _out(S, (M, K), f32, "S", dev, X, stream)
+    Q, pq, ldq = _out(_bytes(Q), (M, K), u8, "Q", dev, X, stream)
+    E, pe, lde = _out(_bytes(E), (M, -(-K // 32)), u8, "E", dev, X, stream)
     _check(load().rmsnorm_mx8(M, K, px, ldx, pr, ldr, pg, float(eps), ps, lds, pq, ldq, pe, lde,
                               _stream(stream)), "rmsnorm_mx8")
     return Q, E, X if S is None else S
@@ -612,10 +627,9 @@ def rmsnorm_f32_bwd(dY, S, gamma, rstd, dS=None, dX=None, dgamma=None, want=("dX
     pg, _ = _arg(gamma, (K,), f32, "gamma", dev)
     pt, _ = _arg(rstd, (M,), f32, "rstd", dev)
     pds, ldds = _arg(dS, (M, K), f32, "dS", dev)
-    dX = None if not wx else _new((M, K), f32, dY, stream) if dX is None else dX
-    dgamma = None if not wg else _new((K,), f32, dY, stream) if dgamma is None else dgamma
-    pdx, lddx = _arg(dX, (M, K), f32, "dX", dev)
-    pdg, _ = _arg(dgamma, (K,), f32, "dgamma", dev)
+    none = (None, None, 0)
+    dX, pdx, lddx = _out(dX, (M, K), f32, "dX", dev, dY, stream) if wx else none
+    dgamma, pdg, _ = _out(dgamma, (K,), f32, "dgamma", dev, dY, stream) if wg else none
     need = _ws_size("rmsnorm_f32_bwd_ws_size", M, K) if wg else 0
     keep, pws, nws = _workspace(workspace, need, dev, dY, stream)
     _check(load().rmsnorm_f32_bwd(int(bool(accumulate)), M, K, pd, lddy, ps, lds, pg, pt, pds,
@@ -636,20 +650,16 @@ def _packed_linear(name, bits, X8, XE, Q, S, bias, act, residual, Y, Y8, YE, out
         S = S.view(torch.float16)
     px, ldx = _arg(X8, (M, K), u8, "X8", dev)
     pe, ldxe = _arg(XE, (M, -(-K // 32)), u8, "XE", dev)
-    # codes and scales may be wider than K needs
-    pq, ldq = _arg(Q[:, :-(-K * bits // 8)], (N, -(-K * bits // 8)), u8, "Q", dev)
-    ps, lds = _arg(S[:, :-(-K // 64)], (N, -(-K // 64)), torch.float16, "S", dev)
+    pq, ldq = _wide(Q, N, -(-K * bits // 8), u8, "Q", dev)
+    ps, lds = _wide(S, N, -(-K // 64), torch.float16, "S", dev)
     pb, _ = _arg(bias, (N,), f32, "bias", dev)
     pr, ldr = _arg(residual, (M, N), f32, "residual", dev)
-    Y = None if out == "mx8" else _new((M, N), f32, X8, stream) if Y is None else Y
-    if out == "f32":
-        Y8 = YE = None
-    else:
-        Y8 = _new((M, N), u8, X8, stream) if Y8 is None else _bytes(Y8)
-        YE = _new((M, -(-N // 32)), u8, X8, stream) if YE is None else _bytes(YE)
-    py, ldy = _arg(Y, (M, N), f32, "Y", dev)
-    p8, ldy8 = _arg(Y8, (M, N), u8, "Y8", dev)
-    pye, ldye = _arg(YE, (M, -(-N // 32)), u8, "YE", dev)
+    py = ldy = p8 = ldy8 = pye = ldye = 0
+    if out != "mx8":
+        Y, py, ldy = _out(Y, (M, N), f32, "Y", dev, X8, stream)
+    if out != "f32":
+        Y8, p8, ldy8 = _out(_bytes(Y8), (M, N), u8, "Y8", dev, X8, stream)
+        YE, pye, ldye = _out(_bytes(YE), (M, -(-N // 32)), u8, "YE", dev, X8, stream)
     _check(getattr(load(), name)(_activation(act), M, N, K, px, ldx, pe, ldxe, pq, ldq, ps, lds,
                                  pb, pr, ldr, py, ldy, p8, ldy8, pye, ldye, _stream(stream)), name)
     return Y if out == "f32" else (Y8, YE) if out == "mx8" else (Y, Y8, YE)
