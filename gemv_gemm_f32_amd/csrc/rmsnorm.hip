@@ -385,7 +385,10 @@ hipError_t launch_rmsnorm(const RmsNorm &a, hipStream_t s) {
 }
 
 hipError_t launch_rmsnorm_bwd(const RmsNormBwd &a, hipStream_t s) {
-    const int groups = a.M < RMSNORM_BWD_GROUPS ? a.M : RMSNORM_BWD_GROUPS;
+    // a workgroup per row of the workspace; up to 2,048 columns it takes 4 rows
+    // at a time
+    const int64_t rows = a.K <= 2048 ? ((int64_t)a.M + 3) / 4 : a.M;
+    const int groups = (int)(rows < RMSNORM_BWD_GROUPS ? rows : RMSNORM_BWD_GROUPS);
     if (a.M > 0) {
         const hipError_t e = a.K % 4 ? norm_bwd_of<true>(a, groups, s) : norm_bwd_of<false>(a, groups, s);
         if (e != hipSuccess) return e;
