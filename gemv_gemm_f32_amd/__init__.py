@@ -12,7 +12,9 @@ __all__ = ["binding", "inputs"]
 
 def __getattr__(name):
     if name in ("gemm_f32", "gemm_f32_tn", "gemm_f32_nt", "gemv_f32",
-                "gemv_q2", "GGError"):
+                "gemv_q2", "GGError", "linear_f32", "linear_f32_bwd",
+                "rmsnorm_f32", "rmsnorm_mx8", "rmsnorm_f32_bwd",
+                "linear_q2_mx8", "linear_q4_mx8"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

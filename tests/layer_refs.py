@@ -14,8 +14,9 @@ _erfc = np.vectorize(math.erfc, otypes=[np.float64])
 # |act'| <= 1.13 for all of them (GELU's steepest slope is 1.129)
 STEEP = 1.13
 # An activation's own error relative to |z|: the weight p(z) in [0, 1] that
-# multiplies z is made of an exponential (or erfc), a sum and a quotient; the
-# complementary error function may be 16 units in the last place (2^-19) off.
+# multiplies z is made of an exponential (or an error function, whose rational
+# form is within 1.5e-7 < 2^-22 of 1), a sum and a quotient: a few units in the
+# last place of 1 each, at most 16 of them (2^-19) together.
 ACT_ERR = 2.0 ** -19
 # A slope's own error, absolute: p (1 - p) has an absolute error of a few
 # steps of 1 and is multiplied by at most 20 before it vanishes.

@@ -208,3 +208,10 @@ def test_packed_passes(bits):
     passes_checks(lambda: packed(bits, y=None, y8=P, ldy8=64, ye=WS, ldye=2))
     passes_checks(lambda: packed(bits, K=0, x=None, xe=None, q=None, s=None))
     passes_checks(lambda: packed(bits, x=X + 1, q=Q + 3, xe=E + 1, ldr=-1))
+
+
+@pytest.mark.parametrize("name", ["linear_f32", "linear_f32_bwd", "rmsnorm_f32", "rmsnorm_mx8",
+                                  "rmsnorm_f32_bwd", "linear_q2_mx8", "linear_q4_mx8"])
+def test_package_names(name):
+    import gemv_gemm_f32_amd
+    assert getattr(gemv_gemm_f32_amd, name) is getattr(bd, name)
