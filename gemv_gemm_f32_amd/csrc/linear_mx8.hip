@@ -650,7 +650,7 @@ void packed_tile_kernel(PackedLinear a, int tiles_m) {
 // matrix unit busy for a third of the time.  MW: waves per SIMD that the
 // registers leave room for; a SIMD issues vector instructions of one wave
 // every 7 cycles, of two or more every 3 to 4.
-constexpr int SPAN = 128, SPANB = 2 * SPAN;           // columns of x in a stage, bytes of a row
+constexpr int SPAN = 128, SPANB = 2 * SPAN + 16;      // columns of x in a stage, bytes of a row
 
 template <int BM, int NW, int BITS, int MW = 2>
 __global__ __launch_bounds__(64 * NW, MW) void packed_wide_kernel(PackedLinear a, int tiles_m) {
@@ -658,7 +658,7 @@ __global__ __launch_bounds__(64 * NW, MW) void packed_wide_kernel(PackedLinear a
     constexpr int XC = BM * (SPAN / 16) / THREADS;    // units of 16 columns of x per thread
     static_assert(XC * THREADS == BM * (SPAN / 16), "loads must split evenly");
     constexpr int STAGE = BM * SPANB, TILE = BM * BN * 4;
-    constexpr int SMEM = 2 * STAGE > TILE ? 2 * STAGE : TILE;
+    constexpr int SMEM = 3 * STAGE > TILE ? 3 * STAGE : TILE;
     __shared__ __attribute__((aligned(16))) char smem[SMEM];
 
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, l32 = lane & 31;
@@ -701,7 +701,7 @@ __global__ __launch_bounds__(64 * NW, MW) void packed_wide_kernel(PackedLinear a
             er[i] = left > 0 ? pe[i][k0 / 32] : 127u;
         }
     };
-    auto slot = [](int row, int c) { return row * SPANB + ((c ^ (row & 15)) * 16); };
+    auto slot = [](int row, int c) { return row * SPANB + c * 16; };
     auto store_x = [&](int buf) {
         char *xs = smem + buf * STAGE;
 #pragma unroll
@@ -735,71 +735,140 @@ __global__ __launch_bounds__(64 * NW, MW) void packed_wide_kernel(PackedLinear a
         }
     };
 
-    v16f acc[IB];
+    float acc[IB][16];
 #pragma unroll
     for (int i = 0; i < IB; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
 
-    auto multiply = [&](int buf, Codes &c) {
-        const char *xs = smem + buf * STAGE;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const float s = scale_of(c.s[g]);
-            v4u fw[4];
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const v4u e = expand16<BITS>(c.w[g] + v * (BITS / 2));
-                fw[2 * v] = widen(e[0], e[1], 127);
-                fw[2 * v + 1] = widen(e[2], e[3], 127);
-            }
-#pragma unroll
-            for (int i = 0; i < IB; ++i) {
-                v4u fx[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    fx[t] = *reinterpret_cast<const v4u *>(xs + slot(32 * i + l32, 8 * g + 4 * h + t));
-                v16f q;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) q[r] = 0.f;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) q = mfma(fx[t], fw[t], q);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][r] = __builtin_fmaf(q[r], s, acc[i][r]);
-                // a use here, or all of this moves past the barrier
-                asm volatile("" : "+v"(acc[i]));
-            }
+    // 8 of the 32 codes that a lane holds of a group, as bf16
+    auto expand = [&](const unsigned (&w)[BITS], int f) {
+        if constexpr (BITS == 4) {
+            unsigned lo, hi;
+            e4m3_of_4bit(w[f], lo, hi);
+            return widen(lo, hi, 127);
+        } else {
+            const unsigned c = w[f / 2] >> (4 * (f & 1));
+            return widen(e4m3_of_2bit(c & 0x03030303u), e4m3_of_2bit(c >> 2 & 0x03030303u), 127);
         }
     };
+    // half of a unit of x to its place: 8 columns as bf16
+    auto put_x = [&](int buf, int i, int half) {
+        const int row = (tid + THREADS * i) / 8;
+        const v4u d = shuffle16<BITS>(xr[i]);
+        *reinterpret_cast<v4u *>(smem + buf * STAGE + slot(row, 2 * unit + half)) =
+            widen(d[2 * half], d[2 * half + 1], er[i]);
+    };
 
-    // as in the kernel above: x two spans ahead, codes one, loads unconditional
+    // A span in 8 IB turns, each a product and the vector work that the matrix
+    // unit covers: multiply-adds of the block before (the last one's of the
+    // span before), an eighth of the next group's codes, half a unit of x.  A
+    // block's operand of x is read as the block before it lets go of the
+    // registers.  x is stored two spans ahead, into the third stage, which the
+    // span before this one read, after a barrier in the middle of the span.
+    v4u fx[4], fw[2][4];
+    v16f p[2];
+    float s[2] = {0.f, 0.f};
+    auto read = [&](int st, int b, int t) {
+        fx[t] = *reinterpret_cast<const v4u *>(
+            smem + st * STAGE + slot(32 * (b % IB) + l32, 8 * (b / IB) + 4 * h + t));
+    };
+    auto fma_block = [&](int d, int from, int to, float sg) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (r >= from && r < to) {
+                acc[d % IB][r] = __builtin_fmaf(p[d & 1][r], sg, acc[d % IB][r]);
+                asm volatile("" : "+v"(acc[d % IB][r]));       // here, not later
+            }
+    };
+    // stage `st`, whose first operands are in fx; `more`: x in registers goes
+    // to stage `st2`, and fx gets the first operands of stage `st1`
+    auto multiply = [&](int st, int st1, int st2, const Codes &c, const Codes &next, auto more,
+                        auto load) {
+        constexpr int NB = 2 * IB;
+        const float before = s[1];
+        s[0] = scale_of(c.s[0]);
+        s[1] = scale_of(c.s[1]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int g = b / IB;
+            v16f q;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) q[r] = 0.f;
+            if (decltype(more)::value && b == IB) __syncthreads();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                __builtin_amdgcn_sched_barrier(0);
+                q = mfma(fx[t], fw[g][t], q);
+                if (b + 1 < NB) read(st, b + 1, t);
+                else if (decltype(more)::value) read(st1, 0, t);
+                const int turn = 4 * (b % IB) + t;              // of 4 IB in the group
+                if (turn % IB == 0 && (g == 0 || decltype(more)::value)) {
+                    v4u &f = fw[1 - g][turn / IB];
+                    f = expand(g == 0 ? c.w[1] : next.w[0], turn / IB);
+                    asm volatile("" : "+v"(f));
+                }
+                if (decltype(more)::value && g == 1 && turn % 2 == 1 && turn / 2 < 2 * XC)
+                    put_x(st2, turn / 4, turn / 2 % 2);
+                constexpr int from[5] = {0, 0, 4, 10, 16};
+                fma_block(b == 0 ? NB - 1 : b - 1, from[t], from[t + 1],
+                          b == 0 ? before : s[(b - 1) / IB]);
+            }
+            p[b & 1] = q;
+        }
+        load();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto expand0 = [&](const Codes &c) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) fw[0][f] = expand(c.w[0], f);
+    };
+    auto read0 = [&](int st) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) read(st, 0, t);
+    };
+
+#pragma unroll
+    for (int r = 0; r < 16; ++r) p[1][r] = 0.f;
+    // Loads are unconditional, as in the kernel above: past the end they take
+    // the last whole span again.
     const int64_t whole = a.K / SPAN;
-    int buf = 0;
+    int st = 0, st1 = 1, st2 = 2;
     Codes cur;
     if (whole > 0) {
         load_x(0);
         load_w(0, cur);
         store_x(0);
         load_x(min((int64_t)1, whole - 1));
+        store_x(1);
+        load_x(min((int64_t)2, whole - 1));
+        expand0(cur);
         __syncthreads();
-        for (int64_t span = 0; span < whole; ++span, buf ^= 1) {
+        read0(0);
+        for (int64_t span = 0; span < whole; ++span) {
             Codes next;
             load_w(min(span + 1, whole - 1), next);
-            store_x(buf ^ 1);
-            load_x(min(span + 2, whole - 1));
-            multiply(buf, cur);
-            __syncthreads();
+            multiply(st, st1, st2, cur, next, std::true_type{},
+                     [&] { load_x(min(span + 3, whole - 1)); });
             cur = next;
+            const int done = st;
+            st = st1;
+            st1 = st2;
+            st2 = done;
         }
+        __syncthreads();
     }
     if (a.K % SPAN) {                                 // one more, cut short
         load_x_part(whole);
         load_w_part(whole, cur);
-        store_x(buf);
+        store_x(st1);
+        expand0(cur);
         __syncthreads();
-        multiply(buf, cur);
+        read0(st1);
+        multiply(st1, 0, 0, cur, cur, std::false_type{}, [] {});
         __syncthreads();
     }
+    fma_block(2 * IB - 1, 0, 16, s[1]);
 
     // sums to LDS, as in the kernel above
     float *tile = reinterpret_cast<float *>(smem);
