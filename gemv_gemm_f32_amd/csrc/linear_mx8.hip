@@ -166,6 +166,40 @@ __device__ __forceinline__ void load_bytes(unsigned (&d)[N / 4], const uint8_t *
     }
 }
 
+// 16 bytes less the first n, zeros behind them.
+__device__ __forceinline__ v4u drop_bytes(v4u v, unsigned n) {
+    const v4u none = {0, 0, 0, 0};
+    if (n & 8) v = v4u{v[2], v[3], 0, 0};
+    if (n & 4) v = v4u{v[1], v[2], v[3], 0};
+#if defined(__HIP_DEVICE_COMPILE__)
+    v = v4u{__builtin_amdgcn_alignbyte(v[1], v[0], n), __builtin_amdgcn_alignbyte(v[2], v[1], n),
+            __builtin_amdgcn_alignbyte(v[3], v[2], n), __builtin_amdgcn_alignbyte(0, v[3], n)};
+#endif
+    return n < 16 ? v : none;
+}
+
+// N bytes (8 or 16) from p, of which `have` exist (none if negative), as one
+// load that ends where the row does and drops what comes before p; byte by byte
+// if the row is too short for that.
+template <int N>
+__device__ __forceinline__ void load_cut(unsigned (&d)[N / 4], const uint8_t *p, int have, bool row_long) {
+    if (!row_long) {
+        load_bytes<N>(d, p, have);
+        return;
+    }
+    const int n = max(N - have, 0);
+    if constexpr (N == 16) {
+        const v4u v = drop_bytes(*reinterpret_cast<const v4u_any *>(p - n), (unsigned)n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = v[i];
+    } else {
+        const v2u v = *reinterpret_cast<const v2u_any *>(p - n);
+        const uint64_t b = n < 8 ? ((uint64_t)v[1] << 32 | v[0]) >> (8 * n) : 0;
+        d[0] = (unsigned)b;
+        d[1] = (unsigned)(b >> 32);
+    }
+}
+
 // D dwords in one load, from any byte.
 template <int D>
 __device__ __forceinline__ void load_codes(unsigned (&w)[D], const uint8_t *p) {
@@ -210,6 +244,8 @@ template <int BM, int BN, int THREADS, class At>
 __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, int64_t n0, int tid,
                                             At at) {
     constexpr int PER_ROW = BN / 4;                    // threads along a row
+    constexpr int USED = THREADS < BM * PER_ROW ? THREADS : BM * PER_ROW;
+    if (tid >= USED) return;                           // whole waves
     const int col = tid % PER_ROW * 4;
     const int64_t n = n0 + col;
     const int live = (int)min(max((int64_t)a.N - n, (int64_t)0), (int64_t)4);
@@ -219,7 +255,7 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
         for (int c = 0; c < 4; ++c)
             if (c < live) bias[c] = a.bias[n + c];
     with_act(a.act, [&](auto act) {
-        constexpr int ROWS = THREADS / PER_ROW;            // rows at a time
+        constexpr int ROWS = USED / PER_ROW;               // rows at a time
 #pragma unroll 4
         for (int i = 0; i < BM / ROWS; ++i) {
             const int row = tid / PER_ROW + ROWS * i;
@@ -281,8 +317,7 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
 // A workgroup owns 16 NH columns n (NH = 2 for an output in 8 bits, whose
 // blocks are 32 wide); its waves split into NH column sets by KW runs of
 // groups, and the runs' sums meet in LDS, added in order.  Loads are 16 bytes
-// of x, 32 codes and both scales each; a pair that K cuts short is loaded byte
-// by byte.
+// of x, 32 codes and both scales each.
 // Lanes 16q .. 16q + 15 have loaded codes 32q .. 32q + 31 of a pair of
 // groups; afterwards they have codes 16q .. 16q + 15 of the first group in the
 // lower dwords and of the second in the upper.
@@ -351,17 +386,15 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < N; ++i) p[i].multiply(q, acc);
     }
-    // the pair at hand, of which columns 0 .. left - 1 exist, byte by byte
-    __device__ __forceinline__ void part(int64_t left, int q, v4f &acc) {
-        const auto have = [&](int at, int most) {
-            return (int)min(max(left - at, (int64_t)0), (int64_t)most);
-        };
+    // the pair at hand, of which columns 0 .. left - 1 exist, of a row of K
+    __device__ __forceinline__ void part(int left, int K, int q, v4f &acc) {
+        const bool row_long = K >= 128;
         Pair<BITS> p;
-        load_bytes<4 * BITS>(p.w, w, (have(32 * q, 32) * BITS + 7) / 8);
+        load_cut<4 * BITS>(p.w, w, ((left * BITS + 7) >> 3) - 4 * BITS * q, row_long);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             unsigned d[4];
-            load_bytes<16>(d, x + 64 * g, have(64 * g + 16 * q, 16));
+            load_cut<16>(d, x + 64 * g, left - 64 * g - 16 * q, row_long);
             p.x[g] = v4u{d[0], d[1], d[2], d[3]};
         }
         p.e = 0;
@@ -398,7 +431,7 @@ __global__ __launch_bounds__(64 * NH * KW) void packed_rows_kernel(PackedLinear 
     else if (n == 2) rows.template run<2>(q, acc);
     else if (n == 1) rows.template run<1>(q, acc);
 #pragma unroll 1
-    for (; p < end; ++p) rows.part(a.K - p * 128, q, acc);
+    for (; p < end; ++p) rows.part((int)(a.K - p * 128), a.K, q, acc);
 
 #pragma unroll
     for (int r = 0; r < 4; ++r) red[kw][4 * q + r][16 * nh + l16] = acc[r];
@@ -421,221 +454,209 @@ hipError_t launch_rows(const PackedLinear &a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// More than 16 rows: a workgroup owns BM rows of x by BN columns n and walks k
-// in steps of one weight group, 64, double-buffered in LDS as bf16.  Bound by
-// the latency of a step (LDS, expansion, products and barrier in turn) where
-// tiles are few, which is where these are used.
+// More than 16 rows where tiles are few: bound by the vector unit (about 100
+// instructions of expansion and multiply-adds per 4 products) and by latency.
+// A workgroup owns 32 x 32 cells, and its KW waves split k: each walks its own
+// run of pairs of groups without a barrier, and the runs' sums meet in LDS,
+// added in order.
 //
-//  * Codes are expanded, and both operands widened, once per workgroup, on
-//    their way into LDS.
-//  * LDS rows hold 64 values, 8 chunks of 16 bytes; chunk c of row r lies at slot
-//    c ^ (r mod 8), so that the 16-byte fragment reads of 8 neighbouring
-//    rows, and the writes, meet no bank twice.
-//  * Loads run two steps ahead: registers hold the next step while LDS holds
-//    this one; one barrier per step.
-//  * Where tiles are few, KS groups of waves share a tile's steps, each with
-//    its own stages, and their sums are added in group order.
-//  * The finished sums pass through LDS, so that bias, residual and the
-//    stores of Y run along rows, 16 bytes per lane.
-constexpr int STEP = 64, ROWB = 2 * STEP;   // columns of a step, bytes of an LDS row
-
-// KS groups of WR x WC waves, each wave with IB x JB blocks of 32 x 32.
-template <int BM, int BN, int WR, int WC, int KS, int BITS>
-__global__ __launch_bounds__(64 * WR * WC * KS, WR * WC * KS >= 8 ? WR * WC * KS / 4 : 2)
-void packed_tile_kernel(PackedLinear a, int tiles_m) {
-    constexpr int THREADS = 64 * WR * WC;             // of a group
-    constexpr int IB = BM / WR / 32, JB = BN / WC / 32;
-    static_assert(IB * WR * 32 == BM && JB * WC * 32 == BN, "waves must cover the tile");
-    // a row's step is 4 units of 16 columns: 16 bytes of x, CB bytes of codes
-    constexpr int CB = 2 * BITS;
-    constexpr int XC = BM * 4 / THREADS, WL = BN * 4 / THREADS;   // units per thread
-    static_assert(XC * THREADS == BM * 4 && WL * THREADS == BN * 4, "loads must split evenly");
-    static_assert(BM <= THREADS && BN <= THREADS, "one scale per thread");
-    constexpr int XBYTES = BM * ROWB, WBYTES = BN * ROWB, STAGE = XBYTES + WBYTES;
-    constexpr int TILE = BM * BN * 4;                 // a group's finished sums
-    constexpr int SMEM = KS * (2 * STAGE > TILE ? 2 * STAGE : TILE);
+//  * Loads are 16 bytes per lane with a row's neighbouring units in
+//    neighbouring lanes; lanes whose loads lie in 32 rows each would take four
+//    times as long (64 x 1536 x 12288, 2 bits: 27.7 us against 17.2).  A
+//    stage of LDS of the wave's own deals the bytes out to the lanes that
+//    multiply them; 16-byte units of a row are permuted by the row so that reads
+//    and writes meet no bank twice.
+//  * x's powers of two and W's scales come in one load, powers in the lower
+//    half of the lanes, scales in the upper.
+template <int KW, int BITS, int MW>
+__global__ __launch_bounds__(64 * KW, MW) void packed_block_kernel(PackedLinear a, int tiles_m) {
+    constexpr int THREADS = 64 * KW;
+    // of a wave: 32 rows of 128 columns of x as they are, and of W's codes
+    constexpr int WROW = 16 * BITS, XBYTES = 32 * 128, STAGE = XBYTES + 32 * WROW;
+    constexpr int UNITS = WROW / 16, WL = UNITS / 2;           // 16-byte units of a row, loads
+    constexpr int SMEM = KW * (STAGE > 4096 ? STAGE : 4096);
     __shared__ __attribute__((aligned(16))) char smem[SMEM];
-    __shared__ unsigned all_scales[KS][2][BN];        // W: a half per row and step
+    const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    char *const xs = smem + wave * STAGE, *const ws = xs + XBYTES;
+    int tb = blockIdx.x;
+    if ((gridDim.x & 7) == 0) tb = (tb & 7) * (gridDim.x >> 3) + (tb >> 3);   // runs per XCD
+    const int64_t m0 = (int64_t)(tb % tiles_m) * 32, n0 = (int64_t)(tb / tiles_m) * 32;
+    const int64_t pairs = ((int64_t)a.K + 127) / 128;
+    const int64_t first = pairs * wave / KW, end = pairs * (wave + 1) / KW;
+    const auto xrow = [&](int r) { return min(m0 + r, (int64_t)a.M - 1); };
+    const auto wrow = [&](int r) { return min(n0 + r, (int64_t)a.N - 1); };
 
-    const int grp = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / THREADS);
-    const int tid = threadIdx.x % THREADS, lane = tid & 63, wave = tid >> 6, h = lane >> 5,
-              l32 = lane & 31;
-    char *const gsmem = smem + grp * 2 * STAGE;
-    unsigned(*const scales)[BN] = all_scales[grp];
-    int t = blockIdx.x;
-    if ((gridDim.x & 7) == 0) t = (t & 7) * (gridDim.x >> 3) + (t >> 3);   // runs per XCD
-    const int64_t m0 = (int64_t)(t % tiles_m) * BM;
-    const int64_t n0 = (int64_t)(t / tiles_m) * BN;
-    const int wm = wave / WC * (32 * IB), wn = wave % WC * (32 * JB);
-
-    const int unit = tid % 4;
-    const uint8_t *px[XC], *pe[XC], *pw[WL];
+    const uint8_t *px[4], *pw[WL], *pes;
 #pragma unroll
-    for (int i = 0; i < XC; ++i) {
-        const int64_t row = min(m0 + tid / 4 + THREADS / 4 * i, (int64_t)a.M - 1);
-        px[i] = a.X + row * a.ldx + 16 * unit;
-        pe[i] = a.XE + row * a.ldxe + unit / 2;
-    }
+    for (int j = 0; j < 4; ++j) px[j] = a.X + xrow(lane / 8 + 8 * j) * a.ldx;
 #pragma unroll
-    for (int i = 0; i < WL; ++i)
-        pw[i] = a.Q + min(n0 + tid / 4 + THREADS / 4 * i, (int64_t)a.N - 1) * a.ldq + CB * unit;
-    // the first BN threads fetch a row's scale
-    const bool fetch_s = tid < BN;
-    const uint16_t *ps = a.S + min(n0 + (fetch_s ? tid : 0), (int64_t)a.N - 1) * a.lds;
-
-    v4u xr[XC];
-    unsigned wr[WL][BITS / 2], er[XC], sr = 0;
-    // a step whose 64 columns all exist, and the last one, cut short by K
-    auto load = [&](int64_t step) {
-        const int64_t k0 = step * STEP, kq = k0 * BITS / 8;
-#pragma unroll
-        for (int i = 0; i < WL; ++i) load_codes<BITS / 2>(wr[i], pw[i] + kq);
-#pragma unroll
-        for (int i = 0; i < XC; ++i) {
-            xr[i] = *reinterpret_cast<const v4u_any *>(px[i] + k0);
-            er[i] = pe[i][k0 / 32];
-        }
-        sr = ps[step];
-    };
-    auto load_part = [&](int64_t step) {
-        const int64_t k0 = step * STEP;
-        const int left = (int)(a.K - k0) - 16 * unit;              // columns of this unit on
-#pragma unroll
-        for (int i = 0; i < WL; ++i)
-            load_bytes<CB>(wr[i], pw[i] + k0 * BITS / 8, (min(max(left, 0), 16) * BITS + 7) / 8);
-#pragma unroll
-        for (int i = 0; i < XC; ++i) {
-            unsigned d[4];
-            load_bytes<16>(d, px[i] + k0, left);
-            xr[i] = v4u{d[0], d[1], d[2], d[3]};
-            er[i] = left > 0 ? pe[i][k0 / 32] : 127u;
-        }
-        sr = ps[step];
-    };
-    auto slot = [](int row, int c) { return row * ROWB + ((c ^ (row & 7)) * 16); };
-    auto put = [&](char *base, int row, const v4u &bytes, unsigned e) {
-        *reinterpret_cast<v4u *>(base + slot(row, 2 * unit)) = widen(bytes[0], bytes[1], e);
-        *reinterpret_cast<v4u *>(base + slot(row, 2 * unit + 1)) = widen(bytes[2], bytes[3], e);
-    };
-    auto store = [&](int buf) {
-        char *xs = gsmem + buf * STAGE, *ws = xs + XBYTES;
-#pragma unroll
-        for (int i = 0; i < XC; ++i)
-            put(xs, tid / 4 + THREADS / 4 * i, shuffle16<BITS>(xr[i]), er[i]);
-#pragma unroll
-        for (int i = 0; i < WL; ++i)
-            put(ws, tid / 4 + THREADS / 4 * i, expand16<BITS>(wr[i]), 127);
-        if (fetch_s) scales[buf][tid] = sr;
-    };
-    // the operand of 16 columns: part t of the lane's row
-    auto frag = [&](const char *base, int row, int t) {
-        return *reinterpret_cast<const v4u *>(base + slot(row, 2 * t + h));
+    for (int j = 0; j < WL; ++j) pw[j] = a.Q + wrow(lane / UNITS + 64 / UNITS * j) * a.ldq;
+    // 4 bytes of either: x's powers of two in the lower lanes, scales in the upper
+    pes = h == 0 ? a.XE + xrow(l32) * a.ldxe
+                 : reinterpret_cast<const uint8_t *>(a.S + wrow(l32) * a.lds);
+    const auto xslot = [](int row, int c) { return row * 128 + ((c ^ (row & 7)) * 16); };
+    const auto wslot = [](int row, int c) {
+        return row * WROW + ((c ^ (BITS == 4 ? row >> 2 & 3 : row >> 3 & 1)) * 16);
     };
 
-    v16f acc[IB][JB];
+    struct Regs {
+        v4u x[4], w[WL];
+        unsigned es;
+    };
+    // bytes of a row of x, of codes, and of powers or scales
+    const unsigned rx = a.K, rw = ((int64_t)a.K * BITS + 7) / 8;
+    const unsigned re = h == 0 ? ((unsigned)a.K + 31) / 32 : ((unsigned)a.K + 63) / 64 * 2;
+    // Where K cuts a pair short, loads end where the rows do, and `cut` drops
+    // what they hold of columns before their own.  (K >= 128.)
+    auto load = [&](int64_t pair, Regs &d) {
+        const unsigned p = (unsigned)pair;
+        const unsigned cw = min(p * WROW + 16 * (lane % UNITS), rw - 16);
+        const unsigned cx = min(p * 128 + 16 * (lane % 8), rx - 16);
 #pragma unroll
-    for (int i = 0; i < IB; ++i)
+        for (int j = 0; j < WL; ++j) d.w[j] = *reinterpret_cast<const v4u_any *>(pw[j] + cw);
 #pragma unroll
-        for (int j = 0; j < JB; ++j)
+        for (int j = 0; j < 4; ++j) d.x[j] = *reinterpret_cast<const v4u_any *>(px[j] + cx);
+        d.es = *reinterpret_cast<const u32_any *>(pes + min(p * 4, re - 4));
+    };
+    auto cut = [&](int64_t pair, Regs &d) {
+        const unsigned p = (unsigned)pair;
+        const unsigned ow = p * WROW + 16 * (lane % UNITS), ox = p * 128 + 16 * (lane % 8);
+        const unsigned dw = ow - min(ow, rw - 16), dx = ox - min(ox, rx - 16);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+        for (int j = 0; j < WL; ++j) d.w[j] = drop_bytes(d.w[j], dw);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d.x[j] = drop_bytes(d.x[j], dx);
+        const unsigned de = p * 4 - min(p * 4, re - 4);
+        d.es = de < 4 ? d.es >> (8 * de) : 0u;
+    };
+    // the same for K < 128, byte by byte
+    auto load_short = [&](Regs &d) {
+        const auto bytes = [](const uint8_t *from, int have) {
+            unsigned b[4];
+            load_bytes<16>(b, from, have);
+            return v4u{b[0], b[1], b[2], b[3]};
+        };
+        const int cw = 16 * (lane % UNITS), cx = 16 * (lane % 8);
+#pragma unroll
+        for (int j = 0; j < WL; ++j) d.w[j] = bytes(pw[j] + cw, (int)rw - cw);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d.x[j] = bytes(px[j] + cx, (int)rx - cx);
+        unsigned b[1];
+        load_bytes<4>(b, pes, (int)re);
+        d.es = b[0];
+    };
 
-    auto multiply = [&](int buf) {
-        const char *xs = gsmem + buf * STAGE, *ws = xs + XBYTES;
-        float s[JB];
+    float acc[16];
 #pragma unroll
-        for (int j = 0; j < JB; ++j)
-            s[j] = scale_of(scales[buf][wn + 32 * j + l32]);
-        v4u fx[IB][4], fw[JB][4];
+    for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+    // Registers to this wave's stage: LDS takes a wave's accesses in order, so
+    // that neither these stores nor the reads below need a barrier.
+    auto in_order = [] {
+#if defined(__HIP_DEVICE_COMPILE__)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#endif
+    };
+    auto store = [&](const Regs &d) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<v4u *>(xs + xslot(lane / 8 + 8 * j, lane % 8)) = d.x[j];
 #pragma unroll
-            for (int i = 0; i < IB; ++i) fx[i][t] = frag(xs, wm + 32 * i + l32, t);
+        for (int j = 0; j < WL; ++j)
+            *reinterpret_cast<v4u *>(ws + wslot(lane / UNITS + 64 / UNITS * j, lane % UNITS)) = d.w[j];
+        in_order();
+    };
+    auto multiply = [&](unsigned es) {
+        unsigned e = es, s = es;
+#if defined(__HIP_DEVICE_COMPILE__)
+        const auto o = __builtin_amdgcn_permlane32_swap(es, es, false, false);
+        e = o[0];
+        s = o[1];
+#endif
 #pragma unroll
-            for (int j = 0; j < JB; ++j) fw[j][t] = frag(ws, wn + 32 * j + l32, t);
-        }
-        // A block's products and the multiply-adds of the block before it
-        // alternate, two result tuples in turn, so neither unit waits for the
-        // other.
-        v16f p[2];
-        constexpr int BLOCKS = IB * JB;
+        for (int g = 0; g < 2; ++g) {
+            unsigned w[BITS];
+            if constexpr (BITS == 4) {
+                const v4u q = *reinterpret_cast<const v4u *>(ws + wslot(l32, 2 * g + h));
 #pragma unroll
-        for (int b = 0; b <= BLOCKS; ++b) {
-            if (b < BLOCKS) {
-                v16f q;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) q[r] = 0.f;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) q = mfma(fx[b % IB][t], fw[b / IB][t], q);
-                p[b & 1] = q;
+                for (int i = 0; i < 4; ++i) w[i] = q[i];
+            } else {
+                const v2u q = *reinterpret_cast<const v2u *>(ws + wslot(l32, g) + 8 * h);
+                w[0] = q[0];
+                w[1] = q[1];
             }
-            __builtin_amdgcn_sched_barrier(0);
-            if (b > 0) {
-                const int c = b - 1, i = c % IB, j = c / IB;
+            const unsigned eg = e >> (16 * g + 8 * h) & 255u;
+            v16f q;
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    acc[i][j][r] = __builtin_fmaf(p[c & 1][r], s[j], acc[i][j][r]);
-                // a use here, or all of this moves past the stores and the
-                // barrier below
-                asm volatile("" : "+v"(acc[i][j]));
-                __builtin_amdgcn_sched_barrier(0);
+            for (int r = 0; r < 16; ++r) q[r] = 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const v4u x = shuffle16<BITS>(*reinterpret_cast<const v4u *>(xs + xslot(l32, 4 * g + 2 * h + u)));
+                const v4u b = expand16<BITS>(w + u * (BITS / 2));
+                q = mfma(widen(x[0], x[1], eg), widen(b[0], b[1], 127), q);
+                q = mfma(widen(x[2], x[3], eg), widen(b[2], b[3], 127), q);
             }
+            const float sg = scale_of(s >> (16 * g));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[r] = __builtin_fmaf(q[r], sg, acc[r]);
         }
+        in_order();
     };
-
-    // Group g takes the steps g, g + KS, ...; every group goes through the same
-    // number of rounds.  The next step's data, in registers since the last
-    // round, go to the stage that the last round read, and the loads of the one
-    // after it have this whole round to arrive: they are unconditional (past
-    // the end, the last whole step again), because a load under a branch is
-    // waited for where the branch joins.
-    const int64_t whole = a.K / STEP;
-    int buf = 0;
-    if (whole > 0) {
-        load(min((int64_t)grp, whole - 1));
-        store(0);
-        load(min((int64_t)grp + KS, whole - 1));
-        __syncthreads();
-        for (int64_t s0 = 0; s0 < whole; s0 += KS, buf ^= 1) {
-            store(buf ^ 1);
-            load(min(s0 + grp + 2 * KS, whole - 1));
-            if (KS == 1 || s0 + grp < whole) multiply(buf);        // uniform
-            __syncthreads();
+    // Loads run two pairs ahead; past the end they take the last pair again,
+    // since a load under a branch is waited for where it joins.
+    if (first < end) {
+        Regs d[2];
+        if (a.K < 128) {
+            load_short(d[0]);
+        } else {
+            load(first, d[0]);
+            load(min(first + 1, end - 1), d[1]);
+        }
+        auto step = [&](int64_t p, Regs &r) {
+            const unsigned es = r.es;
+            store(r);
+            load(min(p + 2, end - 1), r);
+            multiply(es);
+        };
+        int64_t p = first;
+        // the last pair or two apart: they load nothing and may be cut short
+        for (; p + 2 < end; p += 2) {
+            step(p, d[0]);
+            step(p + 1, d[1]);
+        }
+        const int64_t whole = a.K / 128;
+        if (a.K >= 128 && p >= whole) cut(p, d[0]);
+        store(d[0]);
+        multiply(d[0].es);
+        if (p + 1 < end) {
+            if (p + 1 >= whole) cut(p + 1, d[1]);
+            store(d[1]);
+            multiply(d[1].es);
         }
     }
-    if (a.K % STEP) {                                 // one more, cut short
-        const bool mine = KS == 1 || whole % KS == grp;
-        if (mine) {
-            load_part(whole);
-            store(buf);
-        }
-        __syncthreads();
-        if (mine) multiply(buf);
-        __syncthreads();
-    }
 
-    // Sums to LDS, a tile per group: row-major, 16-byte chunks of a row rotated
-    // by the row so that the lanes of a store spread over the banks.  (Every
-    // stage has been read: the last round ended with a barrier.)
-    float *tile = reinterpret_cast<float *>(smem);
-    auto cell = [](int row, int col) { return row * BN + (col ^ ((row & 7) << 2)); };
-#pragma unroll
-    for (int i = 0; i < IB; ++i)
-#pragma unroll
-        for (int j = 0; j < JB; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = wm + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                tile[grp * BM * BN + cell(row, wn + 32 * j + l32)] = acc[i][j][r] * code_scale<BITS>();
-            }
     __syncthreads();
-    finish_tile<BM, BN, THREADS * KS>(a, m0, n0, threadIdx.x, [&](int row, int col) {
+    float *tile = reinterpret_cast<float *>(smem);
+    auto cell = [](int row, int col) { return row * 32 + (col ^ ((row & 7) << 2)); };
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+        tile[wave * 1024 + cell(8 * (r >> 2) + 4 * h + (r & 3), l32)] = acc[r] * code_scale<BITS>();
+    __syncthreads();
+    finish_tile<32, 32, THREADS>(a, m0, n0, threadIdx.x, [&](int row, int col) {
         v4f y = *reinterpret_cast<const v4f *>(tile + cell(row, col));
 #pragma unroll
-        for (int g = 1; g < KS; ++g)                  // in group order
-            y += *reinterpret_cast<const v4f *>(tile + g * BM * BN + cell(row, col));
+        for (int w = 1; w < KW; ++w) y += *reinterpret_cast<const v4f *>(tile + w * 1024 + cell(row, col));
         return y;
     });
+}
+
+template <int KW, int BITS, int MW>
+hipError_t launch_block(const PackedLinear &a, hipStream_t s) {
+    const int64_t tm = ((int64_t)a.M + 31) / 32, tn = ((int64_t)a.N + 31) / 32;
+    if (tm * tn * 64 * KW > UINT32_MAX) return hipErrorInvalidValue;
+    return launch(packed_block_kernel<KW, BITS, MW>, dim3((unsigned)(tm * tn)), dim3(64 * KW), s, a, (int)tm);
 }
 
 // ---------------------------------------------------------------------------
@@ -696,7 +717,7 @@ __global__ __launch_bounds__(64 * NW, MW) void packed_wide_kernel(PackedLinear a
 #pragma unroll
         for (int i = 0; i < XC; ++i) {
             unsigned d[4];
-            load_bytes<16>(d, px[i] + k0, left);
+            load_cut<16>(d, px[i] + k0, left, a.K >= 128);
             xr[i] = v4u{d[0], d[1], d[2], d[3]};
             er[i] = left > 0 ? pe[i][k0 / 32] : 127u;
         }
@@ -729,8 +750,8 @@ __global__ __launch_bounds__(64 * NW, MW) void packed_wide_kernel(PackedLinear a
         for (int g = 0; g < 2; ++g) {
             const int64_t k0 = span * SPAN + 64 * g;
             const int left = (int)(a.K - k0);
-            load_bytes<4 * BITS>(c.w[g], pq + k0 * BITS / 8,
-                                 (min(max(left - 32 * h, 0), 32) * BITS + 7) / 8);
+            load_cut<4 * BITS>(c.w[g], pq + k0 * BITS / 8,
+                               ((left * BITS + 7) >> 3) - 4 * BITS * h, a.K >= 128);
             c.s[g] = left > 0 ? ps[2 * span + g] : 0u;
         }
     };
@@ -893,15 +914,6 @@ hipError_t launch_wide(const PackedLinear &a, hipStream_t s) {
                   (int)tm);
 }
 
-template <int BM, int BN, int WR, int WC, int KS, int BITS>
-hipError_t launch_tiles(const PackedLinear &a, hipStream_t s) {
-    const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
-    constexpr int THREADS = 64 * WR * WC * KS;
-    if (tm * tn * THREADS > UINT32_MAX) return hipErrorInvalidValue;
-    return launch(packed_tile_kernel<BM, BN, WR, WC, KS, BITS>, dim3((unsigned)(tm * tn)),
-                  dim3(THREADS), s, a, (int)tm);
-}
-
 template <int BITS>
 hipError_t launch_bits(const PackedLinear &a, int num_cus, hipStream_t s) {
     const auto count = [&](int bm, int bn) {
@@ -922,24 +934,25 @@ hipError_t launch_bits(const PackedLinear &a, int num_cus, hipStream_t s) {
         if (count(16, 16) >= cus) return launch_rows<BITS, 1, 4>(a, s);
         return lengthy ? launch_rows<BITS, 1, 16>(a, s) : launch_rows<BITS, 1, 8>(a, s);
     }
-    // More rows, by how the tiles fill the CUs (4 bits, us):
-    //  - a wave per 32 columns, 128 x 256 tiles, where a round of them leaves at
-    //    most a fifth of the CUs idle: 2048 x 4096 x 4096 89 against 107 in
-    //    64 x 128 tiles and 156 in 64 x 64;
-    //  - 32 x 64 tiles in four k-groups where they fit one per CU: 128 x 4096 x
-    //    4096 18.5 against 22.7 in 64 x 64;
-    //  - 64 x 64 in four k-groups, one per CU (64 x 12288 x 1536 12.6 against
-    //    13.2 in two and 17 in one; 500 x 1536 x 12288 56 / 70 / 103), in two at
-    //    two per CU (128 x 12288 x 1536 18.6 against 22.7 in four, and 19.9 in
-    //    64 x 128 with a wave per 32 columns);
-    //  - else 64 x 128 with a wave per 32 columns (256 x 12288 x 1536 25.8
-    //    against 26.8 in 64 x 64; 500 x 12288 x 1536 36.3 against 47).
-    const int64_t big = count(128, 256), mid = count(64, 64);
+    // More rows (2 bits / 4 bits, us):
+    //  - 32 x 32 cells with a wave per run of k, up to 6 workgroups per CU: 256 x
+    //    4096 x 4096 23.7 / 26.4 against 27.0 / 36.5 in the best shape of the other
+    //    kernel, 384 x 4096 x 4096 32.5 / 35.7 against 33.7 / 37.3, but 512 x 4096 x
+    //    4096 41.0 / 45.4 against 36.3 / 39.7.  Eight runs instead of four where
+    //    there is at most one workgroup per CU and k is long: 64 x 1536 x 12288
+    //    17.2 / 19.1 against 18.7 / 21.1; 128 x 2304 x 768 7.6 / 8.1 against 5.7 / 6.2.
+    //  - else a wave per 32 columns: 128 x 256 tiles where a round of them leaves
+    //    at most a fifth of the CUs idle (2048 x 4096 x 4096 77 / 82 against 99 /
+    //    108 in 64 x 128); 64 x 256 where they fit one per CU and 64 x 128 do not
+    //    (1024 x 4096 x 4096 48.4 / 53.0 against 52.0 / 56.6; 512 x 4096 x 4096 42.6 /
+    //    47.6 against 36.5 / 39.7); else 64 x 128 (500 x 12288 x 1536 32.2 / 35.0
+    //    against 38.1 / 41.8 in 64 x 256).
+    const int64_t cells = count(32, 32), big = count(128, 256);
+    if (cells <= 6 * cus)
+        return cells <= cus && a.K >= 4096 ? launch_block<8, BITS, 2>(a, s) : launch_block<4, BITS, 3>(a, s);
     if (big >= cus && 4 * ((big + cus - 1) / cus * cus) <= 5 * big)
         return launch_wide<128, 8, BITS, 2>(a, s);
-    if (count(32, 64) <= cus) return launch_tiles<32, 64, 1, 2, 4, BITS>(a, s);
-    if (mid <= cus) return launch_tiles<64, 64, 2, 2, 4, BITS>(a, s);
-    if (mid <= 2 * cus) return launch_tiles<64, 64, 2, 2, 2, BITS>(a, s);
+    if (count(64, 128) > cus && count(64, 256) <= cus) return launch_wide<64, 8, BITS, 2>(a, s);
     return launch_wide<64, 4, BITS, 3>(a, s);
 }
 

@@ -208,6 +208,58 @@ def test_k_zero_and_in_place(bits, M):
     assert np.array_equal(host(r), host(fresh))
 
 
+def _poisoned(a, poison, pad=7):
+    """a as the middle of a wider tensor whose other columns hold `poison`."""
+    t = torch()
+    buf = t.full((a.shape[0], a.shape[1] + pad), poison, dtype=t.from_numpy(a[:0]).dtype, device="cuda")
+    buf[:, 1:1 + a.shape[1]].copy_(dev(a))
+    return buf[:, 1:1 + a.shape[1]]
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+@pytest.mark.parametrize("K", [5, 120, 128, 256, 333, 640])
+@pytest.mark.parametrize("M,N", [(520, 4100), (1000, 6200), (2047, 4095)])
+def test_many_rows(bits, M, N, K):
+    """Enough rows and columns for a wave per 32 columns, in each of its three
+    shapes; misaligned rows between NaN bytes."""
+    X8, XE, Q, S, b, R = _inputs(bits, M, N, K)
+    y, e = _ref(bits, X8, XE, Q, S, b, R, "none")
+    Y, Y8, YE = FN[bits](_poisoned(X8, 0x7f), _poisoned(XE, 255), _poisoned(Q, 0xFF), _poisoned(S, 0x7e00),
+                         bias=dev(b), residual=dev(R), out="both")
+    Y = host(Y)
+    lr.within(Y, y, e, "%d bits %dx%dx%d" % (bits, M, N, K))
+    rows = np.r_[0:40, M - 40:M]
+    q, ee = lr.to_mx8(Y[rows].astype(np.float64))
+    assert np.array_equal(host(YE)[rows], ee) and np.array_equal(host(Y8)[rows], q)
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+@pytest.mark.parametrize("M,N,K", [(17, 33, 5), (20, 40, 77), (33, 70, 129), (33, 70, 4099), (20, 97, 5000),
+                                   (64, 500, 4096), (90, 300, 8225), (400, 700, 450)])
+def test_runs_of_k(bits, M, N, K):
+    """A wave per run of k: fewer pairs than runs, ragged last pairs, eight
+    runs; misaligned rows between NaN bytes."""
+    X8, XE, Q, S, b, R = _inputs(bits, M, N, K)
+    y, e = _ref(bits, X8, XE, Q, S, b, None, "none")
+    Y = FN[bits](_poisoned(X8, 0x7f), _poisoned(XE, 255), _poisoned(Q, 0xFF), _poisoned(S, 0x7e00), bias=dev(b))
+    lr.within(host(Y), y, e, "%d bits %dx%dx%d" % (bits, M, N, K))
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+@pytest.mark.parametrize("K", [130, 143, 144, 145, 159, 160, 161, 190, 191, 193, 255])
+@pytest.mark.parametrize("M,N", [(1, 40), (9, 40), (40, 40), (1000, 6200)])
+def test_ragged_rows_exactly(bits, M, N, K):
+    """Rows cut at every kind of place: integers, so that a byte too many or
+    too few shows in full.  (Sums stay below 2^24 halves.)"""
+    rng = np.random.default_rng([2, K])
+    x = rng.integers(-15, 16, (M, K)).astype(np.float64)
+    X8, XE = lr.to_mx8(x)
+    Q = rng.integers(0, 256, (N, -(-K * bits // 8)), dtype=np.uint8)
+    S = np.ones((N, -(-K // 64)), np.float16).view(np.int16)
+    Y = host(FN[bits](_poisoned(X8, 0x7f), _poisoned(XE, 255), _poisoned(Q, 0xFF), _poisoned(S, 0x7e00)))
+    assert np.array_equal(Y.astype(np.float64), x @ lr.weights(Q, S, bits, K).T)
+
+
 def test_against_the_packed_gemv():
     """One row whose 8-bit values are exact: the same sums as gemv_q2 and
     gemv_q4 on fp32 x, within both accuracy bounds."""
