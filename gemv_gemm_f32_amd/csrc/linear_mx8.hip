@@ -337,11 +337,17 @@ __device__ __forceinline__ void deal(unsigned (&w)[BITS]) {
 // One pair of groups, as loaded, and its products added to the sums.
 template <int BITS>
 struct Pair {
-    unsigned w[BITS], e, s;          // codes, x's four powers of two, both scales
-    v4u x[2];
+    unsigned w[BITS], es;            // codes; x's four powers of two in the lower
+    v4u x[2];                        // lanes, both scales in the upper
 
     __device__ __forceinline__ void multiply(int q, v4f &acc) {
         deal<BITS>(w);
+        unsigned e = es, s = es;
+#if defined(__HIP_DEVICE_COMPILE__)
+        const auto both = __builtin_amdgcn_permlane32_swap(es, es, false, false);
+        e = both[0];
+        s = both[1];
+#endif
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             // 16 columns of block 2 g + q / 2
@@ -360,14 +366,12 @@ struct Pair {
 // A lane's pointers to its rows, at one pair of groups.
 template <int BITS>
 struct Rows {
-    const uint8_t *w, *x, *e;
-    const uint16_t *s;
+    const uint8_t *w, *x, *es;
 
     __device__ __forceinline__ void advance(int64_t pairs) {
         w += pairs * (16 * BITS);
         x += pairs * 128;
-        e += pairs * 4;
-        s += pairs * 2;
+        es += pairs * 4;
     }
     // N whole pairs, all loads in flight together
     template <int N>
@@ -379,8 +383,7 @@ struct Rows {
         for (int i = 0; i < N; ++i) {
             p[i].x[0] = *reinterpret_cast<const v4u_any *>(x + i * 128);
             p[i].x[1] = *reinterpret_cast<const v4u_any *>(x + i * 128 + 64);
-            p[i].e = *reinterpret_cast<const u32_any *>(e + 4 * i);
-            p[i].s = *reinterpret_cast<const u32_any *>(s + 2 * i);
+            p[i].es = *reinterpret_cast<const u32_any *>(es + 4 * i);
         }
         advance(N);
 #pragma unroll
@@ -397,10 +400,9 @@ struct Rows {
             load_cut<16>(d, x + 64 * g, left - 64 * g - 16 * q, row_long);
             p.x[g] = v4u{d[0], d[1], d[2], d[3]};
         }
-        p.e = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) p.e |= (left > 32 * b ? (unsigned)e[b] : 127u) << (8 * b);
-        p.s = (unsigned)s[0] | (left > 64 ? (unsigned)s[1] << 16 : 0u);
+        unsigned d[1];
+        load_bytes<4>(d, es, q < 2 ? (left + 31) / 32 : left > 64 ? 4 : 2);
+        p.es = d[0];
         advance(1);
         p.multiply(q, acc);
     }
@@ -422,7 +424,8 @@ __global__ __launch_bounds__(64 * NH * KW) void packed_rows_kernel(PackedLinear 
     // the pairs of it that exist in full
     int n = (int)max(min(end, (int64_t)a.K / 128) - first, (int64_t)0);
     Rows<BITS> rows = {a.Q + nrow * a.ldq + 4 * BITS * q, a.X + tok * a.ldx + 16 * q,
-                       a.XE + tok * a.ldxe, a.S + nrow * a.lds};
+                       q < 2 ? a.XE + tok * a.ldxe
+                             : reinterpret_cast<const uint8_t *>(a.S + nrow * a.lds)};
     rows.advance(first);
     v4f acc = {0.f, 0.f, 0.f, 0.f};
     int64_t p = first + n;
