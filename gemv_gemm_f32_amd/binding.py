@@ -146,12 +146,12 @@ def _torch():
     return _torch_module
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     torch = _torch()
     if stream is None:
         # the handle alone: building a Stream object takes longer than the
         # rest of a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -510,7 +510,7 @@ def linear_f32(X, W, bias=None, act="none", residual=None, Z=None, Y=None, trans
     pz, ldz = _arg(Z, (M, N), f32, "Z", dev)
     Y, py, ldy = _out(Y, (M, N), f32, "Y", dev, X, stream)
     _check(load().linear_f32(int(bool(trans_w)), _activation(act), M, N, K, px, ldx, pw, ldw, pb,
-                             pr, ldr, pz, ldz, py, ldy, _stream(stream)), "linear_f32")
+                             pr, ldr, pz, ldz, py, ldy, _stream(stream, dev)), "linear_f32")
     return Y
 
 
@@ -551,7 +551,7 @@ def linear_f32_bwd(dY, X, W, Z=None, act="none", trans_w=False, dX=None, dW=None
     keep, pws, nws = _workspace(workspace, need, dev, dY, stream)
     _check(load().linear_f32_bwd(int(bool(trans_w)), a, int(bool(accumulate)), M, N, K, pd, lddy,
                                  pz, ldz, px, ldx, pw, ldw, pdx, lddx, pdw, lddw, pdb, pws, nws,
-                                 _stream(stream)), "linear_f32_bwd")
+                                 _stream(stream, dev)), "linear_f32_bwd")
     return dX, dW, db
 
 
@@ -572,7 +572,7 @@ def rmsnorm_f32(X, gamma=None, eps=1e-5, residual=None, S=None, Y=None, rstd=Non
     Y, py, ldy = _out(Y, (M, K), f32, "Y", dev, X, stream)
     rstd, pt, _ = _out(rstd, (M,), f32, "rstd", dev, X, stream)
     _check(load().rmsnorm_f32(M, K, px, ldx, pr, ldr, pg, float(eps), ps, lds, py, ldy, pt,
-                              _stream(stream)), "rmsnorm_f32")
+                              _stream(stream, dev)), "rmsnorm_f32")
     return Y, X if S is None else S, rstd
 
 
@@ -600,7 +600,7 @@ def rmsnorm_mx8(X, gamma=None, eps=1e-5, residual=None, S=None, Q=None, E=None, 
     Q, pq, ldq = _out(_bytes(Q), (M, K), u8, "Q", dev, X, stream)
     E, pe, lde = _out(_bytes(E), (M, -(-K // 32)), u8, "E", dev, X, stream)
     _check(load().rmsnorm_mx8(M, K, px, ldx, pr, ldr, pg, float(eps), ps, lds, pq, ldq, pe, lde,
-                              _stream(stream)), "rmsnorm_mx8")
+                              _stream(stream, dev)), "rmsnorm_mx8")
     return Q, E, X if S is None else S
 
 
@@ -633,7 +633,7 @@ def rmsnorm_f32_bwd(dY, S, gamma, rstd, dS=None, dX=None, dgamma=None, want=("dX
     need = _ws_size("rmsnorm_f32_bwd_ws_size", M, K) if wg else 0
     keep, pws, nws = _workspace(workspace, need, dev, dY, stream)
     _check(load().rmsnorm_f32_bwd(int(bool(accumulate)), M, K, pd, lddy, ps, lds, pg, pt, pds,
-                                  ldds, pdx, lddx, pdg, pws, nws, _stream(stream)),
+                                  ldds, pdx, lddx, pdg, pws, nws, _stream(stream, dev)),
            "rmsnorm_f32_bwd")
     return dX, dgamma
 
@@ -661,7 +661,7 @@ def _packed_linear(name, bits, X8, XE, Q, S, bias, act, residual, Y, Y8, YE, out
         Y8, p8, ldy8 = _out(_bytes(Y8), (M, N), u8, "Y8", dev, X8, stream)
         YE, pye, ldye = _out(_bytes(YE), (M, -(-N // 32)), u8, "YE", dev, X8, stream)
     _check(getattr(load(), name)(_activation(act), M, N, K, px, ldx, pe, ldxe, pq, ldq, ps, lds,
-                                 pb, pr, ldr, py, ldy, p8, ldy8, pye, ldye, _stream(stream)), name)
+                                 pb, pr, ldr, py, ldy, p8, ldy8, pye, ldye, _stream(stream, dev)), name)
     return Y if out == "f32" else (Y8, YE) if out == "mx8" else (Y, Y8, YE)
 
 
