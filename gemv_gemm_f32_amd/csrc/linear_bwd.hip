@@ -36,8 +36,8 @@ __global__ __launch_bounds__(256) void dz_kernel(int act, int M, int N, int chun
     const int tx = threadIdx.x % LANES, ty = threadIdx.x / LANES;
     const int r0 = blockIdx.y * chunk, r1 = min(r0 + chunk, M);
     for (int64_t c0 = (int64_t)blockIdx.x * COLS; c0 < N; c0 += (int64_t)gridDim.x * COLS) {
-        const int col = (int)c0 + 4 * tx;
-        const int live = min(max(N - col, 0), 4);     // columns of this thread that exist
+        const int64_t col = c0 + 4 * tx;
+        const int live = (int)min(max(N - col, (int64_t)0), (int64_t)4);   // columns of this thread that exist
         v4f sum = {0.f, 0.f, 0.f, 0.f};
         with_act(act, [&](auto a) {
             constexpr int ACT = decltype(a)::value;

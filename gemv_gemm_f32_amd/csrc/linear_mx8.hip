@@ -317,7 +317,8 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
 // A workgroup owns 16 NH columns n (NH = 2 for an output in 8 bits, whose
 // blocks are 32 wide); its waves split into NH column sets by KW runs of
 // groups, and the runs' sums meet in LDS, added in order.  Loads are 16 bytes
-// of x, 32 codes and both scales each.
+// of x, 32 codes, and x's powers of two (lower lanes) with both scales (upper).
+//
 // Lanes 16q .. 16q + 15 have loaded codes 32q .. 32q + 31 of a pair of
 // groups; afterwards they have codes 16q .. 16q + 15 of the first group in the
 // lower dwords and of the second in the upper.
@@ -670,10 +671,15 @@ hipError_t launch_block(const PackedLinear &a, hipStream_t s) {
 // group multiplies columns 8 t .. 8 t + 7 of either half.  At BM = 128 the
 // matrix unit (4 x 4 x 32 cycles per wave and group), the vector unit (64
 // instructions of expansion, 64 multiply-adds) and LDS (16 KiB per wave) have
-// about equally much to do; 2048 x 4096 x 4096 runs at 770 TFLOP/s, the
-// matrix unit busy for a third of the time.  MW: waves per SIMD that the
-// registers leave room for; a SIMD issues vector instructions of one wave
-// every 7 cycles, of two or more every 3 to 4.
+// about equally much to do, so products and vector work are interleaved turn
+// by turn: 2048 x 4096 x 4096 takes 77 us at 2 bits and 79 at 4 (890 and 870
+// TFLOP/s, vector issue busy for two thirds of the time and the matrix unit for
+// half), 89 and 93 with a block's products before its vector work.  MW: waves
+// per SIMD that the registers leave room for; a SIMD issues vector
+// instructions of one wave every 7 cycles, of two or more every 3 to 4.
+//
+// A stage's rows are padded by 16 bytes: 8 neighbouring rows' reads meet no
+// bank twice, and every place within a stage is one address and a constant.
 constexpr int SPAN = 128, SPANB = 2 * SPAN + 16;      // columns of x in a stage, bytes of a row
 
 template <int BM, int NW, int BITS, int MW = 2>
