@@ -112,6 +112,15 @@ hipError_t launch_linear_bwd(bool trans_w, int act, bool accumulate, int M, int 
 // sums: at most 64 chunks, of a multiple of 16 rows.
 inline int64_t dz_stride(int64_t N) { return (N + 3) & ~int64_t(3); }
 inline int dz_chunk(int M) { return (int)((((int64_t)M + 63) / 64 + 15) & ~int64_t(15)); }
+inline int dz_chunks(int M) { return (int)(((int64_t)M + dz_chunk(M) - 1) / dz_chunk(M)); }
+// Rows [first, end) of chunk i.  64 bits: chunks of 2^25 rows end at 2^31.
+struct RowRange {
+    int64_t first, end;
+};
+__host__ __device__ inline RowRange dz_rows(int M, int chunk, int64_t i) {
+    const int64_t first = i * chunk, end = first + chunk;
+    return {first, end < M ? end : M};
+}
 inline unsigned __int128 linear_bwd_workspace_floats(bool identity, int64_t M, int64_t N) {
     return (identity ? 0 : (unsigned __int128)M * dz_stride(N)) + (unsigned __int128)64 * N;
 }

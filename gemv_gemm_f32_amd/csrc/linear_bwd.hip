@@ -34,14 +34,14 @@ __global__ __launch_bounds__(256) void dz_kernel(int act, int M, int N, int chun
                                                  float *partial) {
     __shared__ v4f red[256];
     const int tx = threadIdx.x % LANES, ty = threadIdx.x / LANES;
-    const int r0 = blockIdx.y * chunk, r1 = min(r0 + chunk, M);
+    const RowRange rows = dz_rows(M, chunk, blockIdx.y);
     for (int64_t c0 = (int64_t)blockIdx.x * COLS; c0 < N; c0 += (int64_t)gridDim.x * COLS) {
         const int64_t col = c0 + 4 * tx;
         const int live = (int)min(max(N - col, (int64_t)0), (int64_t)4);   // columns of this thread that exist
         v4f sum = {0.f, 0.f, 0.f, 0.f};
         with_act(act, [&](auto a) {
             constexpr int ACT = decltype(a)::value;
-            for (int r = r0 + ty; r < r1; r += ROWS) {
+            for (int64_t r = rows.first + ty; r < rows.end; r += ROWS) {
                 const float *pd = dY + r * lddy + col;
                 const float *pz = Z + r * ldz + col;
                 float *po = dZ + r * lddz + col;
@@ -147,7 +147,7 @@ hipError_t launch_linear_bwd(bool trans_w, int act, bool accumulate, int M, int 
             partial = ws + (int64_t)M * lddz;
             dZ = out;
         }
-        const int chunk = dz_chunk(M), chunks = (M + chunk - 1) / chunk;
+        const int chunk = dz_chunk(M), chunks = dz_chunks(M);
         const dim3 grid(blocks(N, COLS, 1 << 17), chunks);
         e = launch(dz_kernel, grid, dim3(256), s, act, M, N, chunk,
                    dY, lddy, Z, ldz, out, lddz, db ? partial : nullptr);
