@@ -13,6 +13,9 @@ namespace {
 struct ScaleAdd {
     float alpha, beta;
 
+    // the epilogue of the rectangle at (m, n)
+    ScaleAdd from(int64_t, int64_t) const { return *this; }
+
     template <int N>
     struct Fetched {};
     template <int N, class Row, class Mine>

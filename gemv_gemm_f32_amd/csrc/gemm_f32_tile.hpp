@@ -763,18 +763,19 @@ struct Tiles {
     int ksq, ksh, ks;                  // k-groups of quarter, narrow and 64 x 64 tiles
 };
 
-inline Tiles pick_tiles(bool ax, bool bx, int M, int N, int K, const float *A, int64_t lda,
-                        const float *B, int64_t ldb, int num_cus) {
+// (Sizes in 64 bits: those near 2^31 are rounded up to whole tiles.)
+inline Tiles pick_tiles(bool ax, bool bx, int64_t M, int64_t N, int64_t K, const float *A,
+                        int64_t lda, const float *B, int64_t ldb, int num_cus) {
     // The staged path's 16-byte register loads need the operand's contiguous
     // extent, its leading dimension and its base all to be multiples of 4
     // floats; otherwise it loads floats one by one.
-    const int a_contig = ax ? K : M;
-    const int b_contig = bx ? K : N;
+    const int64_t a_contig = ax ? K : M;
+    const int64_t b_contig = bx ? K : N;
     const bool va = aligned16(A) && (lda % 4 == 0) && (a_contig % 4 == 0);
     const bool vb = aligned16(B) && (ldb % 4 == 0) && (b_contig % 4 == 0);
     // The direct path addresses each operand with 32-bit byte offsets.
-    auto extent = [](bool xmajor, int X, int64_t ld, int K) {
-        return xmajor ? ((int64_t)(X - 1) * ld + K) * 4 : ((int64_t)(K - 1) * ld + X) * 4;
+    auto extent = [](bool xmajor, int64_t X, int64_t ld, int64_t K) {
+        return xmajor ? ((X - 1) * ld + K) * 4 : ((K - 1) * ld + X) * 4;
     };
     // Its 16-byte loads need only 4-byte aligned addresses (rows of any
     // width and leading dimension), and the buffer range check is per dword,
@@ -784,13 +785,13 @@ inline Tiles pick_tiles(bool ax, bool bx, int M, int N, int K, const float *A, i
     // Staged path: 128 x 64 tiles when that grid still gives every CU two
     // tiles to interleave; otherwise 64 x 64, which keeps small and K-heavy
     // products (few output tiles) spread over the CUs.
-    const int64_t tiles_128x64 = (int64_t)((M + 127) / 128) * ((N + 63) / 64);
+    const int64_t tiles_128x64 = ((M + 127) / 128) * ((N + 63) / 64);
     const bool big = tiles_128x64 >= 2 * (int64_t)num_cus;
     // Direct path: 64 x 64 tiles with the k-slabs split over KS groups of 4
     // waves, 4 when there are no more tiles than CUs (each CU then runs one
     // tile with 16 waves), else 2; fewer when K has too few slabs to share.
-    const int64_t tiles_64 = (int64_t)((M + 63) / 64) * ((N + 63) / 64);
-    const int slabs = (K + 31) / 32;
+    const int64_t tiles_64 = ((M + 63) / 64) * ((N + 63) / 64);
+    const int slabs = (int)((K + 31) / 32);
     const int ks = tiles_64 <= (int64_t)num_cus && slabs >= 8 ? 4 : (slabs >= 4 ? 2 : 1);
     // Smaller tiles where 64 x 64 balances badly over the CUs.  The largest
     // per-CU share of tiles is ceil(tiles / CUs); a narrow tile (64 x 32 or
@@ -814,9 +815,9 @@ inline Tiles pick_tiles(bool ax, bool bx, int M, int N, int K, const float *A, i
     //    1024 x 2304 x 768 (576 tiles) 43.1 -> 40.6 us and on 1024 x 1216 x
     //    1024 (304 tiles) 35.1 -> 31.2 us; 432, 700, 768 and 1024 tiles
     //    stay on 64 x 64, where narrow tiles measured 6-24% slower.
-    const int64_t tiles_32 = (int64_t)((M + 31) / 32) * ((N + 31) / 32);
-    const int64_t pad_tall = (int64_t)((M + 63) / 64) * ((N + 31) / 32) * 2;   // in 32 x 32 units
-    const int64_t pad_wide = (int64_t)((M + 31) / 32) * ((N + 63) / 64) * 2;
+    const int64_t tiles_32 = ((M + 31) / 32) * ((N + 31) / 32);
+    const int64_t pad_tall = ((M + 63) / 64) * ((N + 31) / 32) * 2;   // in 32 x 32 units
+    const int64_t pad_wide = ((M + 31) / 32) * ((N + 63) / 64) * 2;
     const bool tall = pad_tall < pad_wide || (pad_tall == pad_wide && ax);
     const int64_t tiles_h = (tall ? pad_tall : pad_wide) / 2;
     const auto share = [num_cus](int64_t t) { return (t + num_cus - 1) / num_cus; };
@@ -831,7 +832,7 @@ inline Tiles pick_tiles(bool ax, bool bx, int M, int N, int K, const float *A, i
     // tiles than CUs, 64 x 48 tiles in two k-groups ran slower than narrow
     // tiles on 1024 x 2304 x 768 and 768 x 3072 x 1024 (41.5 against 39.7
     // us, 53.4 against 50.8), so they serve only this case.
-    const int64_t tiles_48 = (int64_t)((M + 63) / 64) * ((N + 47) / 48);
+    const int64_t tiles_48 = ((M + 63) / 64) * ((N + 47) / 48);
     const bool t48 = !small && ks == 4 && tiles_48 <= (int64_t)num_cus && tiles_48 > tiles_64;
     const int ksq = slabs >= 8 ? 8 : (slabs >= 4 ? 4 : (slabs >= 2 ? 2 : 1));
     const int ksh = !small ? ks : (slabs >= 40 ? 6 : (slabs >= 8 ? 4 : (slabs >= 4 ? 2 : 1)));
@@ -861,15 +862,11 @@ hipError_t launch_staged(int M, int N, int K, const float *A, int64_t lda, const
                   N, K, A, lda, B, ldb, C, ldc, epi, tiles_m, tiles_n);
 }
 
-// The product op(A).op(B) of one storage pair (AX, BX as in gemm_f32_kernel)
-// with epilogue `epi`, on the path and tiles of pick_tiles.
+// One launch of the product (see launch_product).
 template <bool AX, bool BX, class E>
-hipError_t launch_product(const Tiles &t, int M, int N, int K, const float *A, int64_t lda,
-                          const float *B, int64_t ldb, float *C, int64_t ldc, const E &epi,
-                          hipStream_t s) {
-    // Grids are at most 2^31 - 1 workgroups of the smallest tile (32 x 32);
-    // no product that fits in memory comes near that.
-    if ((int64_t)((M + 31) / 32) * ((N + 31) / 32) > INT32_MAX) return hipErrorInvalidValue;
+hipError_t launch_piece(const Tiles &t, int M, int N, int K, const float *A, int64_t lda,
+                        const float *B, int64_t ldb, float *C, int64_t ldc, const E &epi,
+                        hipStream_t s) {
     if (t.direct) {
         if constexpr (AX || BX)
             if (K % 4 != 0) return launch_tiles<AX, BX, true>(t, GG_ARGS);
@@ -885,6 +882,39 @@ hipError_t launch_product(const Tiles &t, int M, int N, int K, const float *A, i
 #undef GG_STAGED
 }
 #undef GG_ARGS
+
+// The product op(A).op(B) of one storage pair (AX, BX as in gemm_f32_kernel)
+// with epilogue `epi`, on the path and tiles of pick_tiles, in one launch where
+// that is possible: kernels count rows and columns in 32 bits, up to the end
+// of the last tile (at most 127 past the matrix), and a launch has fewer than
+// 2^32 threads.  Larger outputs are cut into rectangles, whose starts are
+// multiples of 128, so that the load path that t stands for serves each.
+template <bool AX, bool BX, class E>
+hipError_t launch_product(const Tiles &t, int M, int N, int K, const float *A, int64_t lda,
+                          const float *B, int64_t ldb, float *C, int64_t ldc, const E &epi,
+                          hipStream_t s) {
+    int bm = t.big ? 128 : 64, bn = 64, threads = THREADS;
+    if (t.direct) {
+        bm = t.quarter || (t.half && !t.tall && !t.t48) ? 32 : 64;
+        bn = t.quarter || (t.half && t.tall && !t.t48) ? 32 : t.t48 ? 48 : 64;
+        threads = t.quarter ? 64 * t.ksq : t.t48 ? 1024 : t.half ? 128 * t.ksh : 256 * t.ks;
+    }
+    int64_t rows = M > INT32_MAX - 127 ? 1 << 30 : M, cols = N > INT32_MAX - 127 ? 1 << 30 : N;
+    while (((rows + bm - 1) / bm) * ((cols + bn - 1) / bn) * threads > UINT32_MAX) {
+        int64_t &longer = rows >= cols ? rows : cols;
+        longer = ((longer + 1) / 2 + 127) & ~int64_t(127);
+    }
+    if (rows == M && cols == N) return launch_piece<AX, BX>(t, M, N, K, A, lda, B, ldb, C, ldc, epi, s);
+    for (int64_t m = 0; m < M; m += rows)
+        for (int64_t n = 0; n < N; n += cols) {
+            const hipError_t e = launch_piece<AX, BX>(
+                t, (int)(M - m < rows ? M - m : rows), (int)(N - n < cols ? N - n : cols), K,
+                A + (AX ? m * lda : m), lda, B + (BX ? n * ldb : n), ldb, C + m * ldc + n, ldc,
+                epi.from(m, n), s);
+            if (e != hipSuccess) return e;
+        }
+    return hipSuccess;
+}
 
 }  // namespace
 }  // namespace gg

@@ -26,6 +26,12 @@ struct Layer {
     int64_t ldz;
     int act;
 
+    // the epilogue of the rectangle at (m, n)
+    Layer from(int64_t m, int64_t n) const {
+        return {bias ? bias + n : nullptr, R ? R + m * ldr + n : nullptr, ldr,
+                Z ? Z + m * ldz + n : nullptr, ldz, act};
+    }
+
     // Bias and residuals of one column's NS sums, fetched before the K walk.
     template <int NS>
     struct Fetched {

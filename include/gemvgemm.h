@@ -26,9 +26,10 @@
  *    current device is a gfx950.  No exception or abort crosses this
  *    interface.  GG_ERR_LAUNCH reports the status of this call's own
  *    launch; an error left pending by an earlier HIP call is neither
- *    reported nor cleared.  (The one exception to "nothing was launched":
- *    a batch of more than 64 products takes several launches, and if a
- *    later one is rejected the earlier ones stay queued.)
+ *    reported nor cleared.  (The exceptions to "nothing was launched": a batch
+ *    of more than 64 products and an output too large for one grid take
+ *    several launches, and if a later one is rejected the earlier ones stay
+ *    queued.)
  *  - Results are reproducible bit for bit from run to run on the same shapes
  *    (fixed reduction trees, no floating-point atomics).  They agree with the
  *    exact sum to |c - c_exact| <= 1e-4 * sum_k |a_ik * b_kj| per element for

@@ -51,9 +51,12 @@ hipError_t hipLaunchKernel(const void *f, dim3 g, dim3 b, void **a, size_t, hipS
     } else if (has("column_sum")) {
         printf("%d %d\n", arg<int>(a, 0), arg<int>(a, 1));
     } else if (has("gemm_f32_") || has("linear_few")) {
-        // M N K, the distance of C, its leading dimension; tiles
-        printf("%d %d %d %lld %lld", arg<int>(a, 0), arg<int>(a, 1), arg<int>(a, 2),
-               from_out(arg<float *>(a, 7)) / 4, (long long)arg<int64_t>(a, 8));
+        // M N K, the distance of C, its leading dimension, the distances of
+        // both operands; tiles
+        printf("%d %d %d %lld %lld %lld %lld", arg<int>(a, 0), arg<int>(a, 1), arg<int>(a, 2),
+               from_out(arg<float *>(a, 7)) / 4, (long long)arg<int64_t>(a, 8),
+               (long long)(arg<const float *>(a, 3) - at<float>(1)),
+               (long long)(arg<const float *>(a, 5) - at<float>(2)));
         if (has("gemm_f32_")) printf(" %d %d", arg<int>(a, 10), arg<int>(a, 11));
         printf("\n");
     } else if (has("packed_")) {
@@ -76,6 +79,12 @@ int main(int argc, char **argv) {
         e = launch_linear_bwd(false, n(4), false, n(2), n(3), 1, at<float>(1), n(3), at<float>(2),
                               n(3), nullptr, 0, nullptr, 0, nullptr, 0, nullptr, 0, out, at<float>(3),
                               256, nullptr);
+    } else if (call == "gemm") {                // M N K, A as K x M, B as N x K
+        e = launch_gemm(!n(5), n(6), n(2), n(3), n(4), 1.f, at<float>(1), n(5) ? n(2) : n(4),
+                        at<float>(2), n(6) ? n(4) : n(3), 0.f, out, n(3), 256, nullptr);
+    } else if (call == "linear") {              // M N K, W as N x K
+        e = launch_linear(n(5), 0, n(2), n(3), n(4), at<float>(1), n(4), at<float>(2),
+                          n(5) ? n(4) : n(3), nullptr, nullptr, 0, nullptr, 0, out, n(3), 256, nullptr);
     } else if (call == "rows_of_chunk") {       // M chunk index -> first row, end
         const RowRange r = dz_rows(n(2), dz_chunk(n(2)), n(3));
         printf("%lld %lld\n", (long long)r.first, (long long)r.end);

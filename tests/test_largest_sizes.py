@@ -71,6 +71,53 @@ def test_chunks_of_the_element_pass(record, M, act):
     assert all(a < b for a, b in ends) and all(p[1] == q[0] for p, q in zip(ends, ends[1:]))
 
 
+def _rectangles(launches, M, N):
+    """The rectangles (row, column, rows, columns) that launches write, which
+    have to cover an M x N output with leading dimension N once."""
+    rects = []
+    for name, gx, gy, threads, a in launches:
+        m, n, off, ld = a[0], a[1], a[3], a[4]
+        assert ld == N and m > 0 and n > 0, (name, a)
+        rects.append((off // N, off % N, m, n))
+        assert rects[-1][0] + m <= M and rects[-1][1] + n <= N
+    assert sum(m * n for _, _, m, n in rects) == M * N
+    for i, (r, c, m, n) in enumerate(rects):
+        for r2, c2, m2, n2 in rects[:i]:
+            assert r >= r2 + m2 or r2 >= r + m or c >= c2 + n2 or c2 >= c + n
+    return rects
+
+
+LARGE = [(MOST, 1, 1), (MOST, 1, 200), (1, MOST, 1), (MOST - 127, 1, 1), (MOST - 126, 1, 4), (MOST, 30, 5),
+         (9, MOST, 1), (9, MOST, 64), (1 << 30, 65, 8), (190000, 200000, 128), (262145, 262143, 100),
+         (1 << 29, 64, 4), ((1 << 29) + 1, 64, 4), (64, 1 << 30, 7)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("ta,tb", [(0, 0), (0, 1), (1, 0), (1, 1)])
+def test_products_of_large_outputs(record, M, N, K, ta, tb):
+    launches = record("gemm", M, N, K, ta, tb)
+    for (r, c, m, n), (name, gx, _, _, a) in zip(_rectangles(launches, M, N), launches):
+        assert "gemm_f32_" in name and a[2] == K
+        assert m <= MOST - 127 and n <= MOST - 127              # rows of the last tile stay below 2^31
+        assert a[5] == (r if ta else r * K) and a[6] == (c * K if tb else c)
+        assert r % 128 == 0 and c % 128 == 0 and a[7] * a[8] == gx
+        assert a[7] >= -(-m // 128) and a[8] >= -(-n // 64)
+
+
+@pytest.mark.parametrize("M,N,K", [(346, 768, 768), (2048, 2048, 2048), (1 << 24, 64, 16)])
+def test_ordinary_products_take_one_launch(record, M, N, K):
+    assert len(record("gemm", M, N, K, 0, 0)) == 1
+    assert len(record("linear", M, N, K, 1)) == 1
+
+
+@pytest.mark.parametrize("M,N,K,tw", [(MOST, 1, 1, 0), (MOST, 2, 9, 1), (9, MOST, 3, 1), (9, MOST, 3, 0),
+                                      (200000, 190000, 128, 0)])
+def test_layers_of_large_outputs(record, M, N, K, tw):
+    launches = record("linear", M, N, K, tw)
+    for (r, c, m, n), (name, _, _, _, a) in zip(_rectangles(launches, M, N), launches):
+        assert m <= MOST - 127 and n <= MOST - 127 and a[5] == r * K and a[6] == (c * K if tw else c)
+
+
 @pytest.mark.gpu
 def test_bias_gradient_of_most_rows():
     """2^31 - 1 rows of one column, zeros but for ones at the border of the last
@@ -84,3 +131,47 @@ def test_bias_gradient_of_most_rows():
     del dY
     t.cuda.empty_cache()
     assert got == 6
+
+
+def _equal(Y, f, step=1 << 28):
+    """Whether the long vector Y is f(first, end) piece by piece."""
+    return all(bool((Y[i:i + step] == f(i, min(i + step, Y.numel()))).all()) for i in range(0, Y.numel(), step))
+
+
+def _pattern(i, j):
+    t = torch()
+    return (t.arange(i, j, device="cuda") % 251).float()
+
+
+@pytest.mark.gpu
+def test_layer_of_most_rows():
+    """2^31 - 1 rows through a 1 x 1 layer with bias and a residual updated in
+    place: small integers, exact."""
+    t = torch()
+    X = t.empty((MOST, 1), device="cuda")
+    for i in range(0, MOST, 1 << 28):
+        j = min(i + (1 << 28), MOST)
+        X[i:j, 0] = _pattern(i, j)
+    Y = t.full((MOST, 1), 3.0, device="cuda")
+    bd.linear_f32(X, t.full((1, 1), 2.0, device="cuda"), bias=t.ones(1, device="cuda"), residual=Y, Y=Y)
+    ok = _equal(Y[:, 0], lambda i, j: 2 * _pattern(i, j) + 4)
+    del X, Y
+    t.cuda.empty_cache()
+    assert ok
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tw", [0, 1])
+def test_layer_of_most_columns(tw):
+    """9 rows over 2^31 - 1 columns: the tile kernels."""
+    t = torch()
+    W = t.empty(MOST, device="cuda")
+    for i in range(0, MOST, 1 << 28):
+        j = min(i + (1 << 28), MOST)
+        W[i:j] = _pattern(i, j)
+    X = t.arange(1, 10, device="cuda").float()[:, None].contiguous()
+    Y = bd.linear_f32(X, W[:, None] if tw else W[None], trans_w=bool(tw))
+    ok = [_equal(Y[m], lambda i, j: _pattern(i, j) * (m + 1)) for m in range(9)]
+    del W, Y
+    t.cuda.empty_cache()
+    assert all(ok)
