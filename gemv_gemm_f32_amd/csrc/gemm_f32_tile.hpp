@@ -91,6 +91,15 @@ constexpr int xstride() { return BK + 4; }
 template <int TX>
 constexpr int kstride() { return TX + 8; }
 
+// Places along k near 2^31: whole and begun slabs of K, and min(k0 + k, last)
+// for a k inside the slab at k0, whose end may lie past 2^31 (last >= 0).
+template <int BK>
+__host__ __device__ __forceinline__ int slabs_of(int K) { return K / BK + (K % BK != 0); }
+__host__ __device__ __forceinline__ int clamp_k(int k0, int k, int last) {
+    const unsigned sum = (unsigned)k0 + (unsigned)k;
+    return (int)(sum < (unsigned)last ? sum : (unsigned)last);
+}
+
 template <int TX, int BK, bool XMAJOR>
 constexpr int tile_words() { return XMAJOR ? TX * xstride<BK>() : BK * kstride<TX>(); }
 
@@ -118,16 +127,16 @@ struct Operand {
             const int idx = tid + THREADS * p;
             if (XMAJOR) {
                 const int x = min(x0 + idx / (BK / 4), X - 1);
-                const int k = k0 + (idx % (BK / 4)) * 4;
+                const int k = (idx % (BK / 4)) * 4;
                 const float *row = P + (int64_t)x * ld;
                 if (VEC == 4) {
-                    r[p] = *reinterpret_cast<const v4f *>(row + min(k, K - 4));
+                    r[p] = *reinterpret_cast<const v4f *>(row + clamp_k(k0, k, K - 4));
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) r[p][c] = row[min(k + c, K - 1)];
+                    for (int c = 0; c < 4; ++c) r[p][c] = row[clamp_k(k0, k + c, K - 1)];
                 }
             } else {
-                const int k = min(k0 + idx / (TX / 4), K - 1);
+                const int k = clamp_k(k0, idx / (TX / 4), K - 1);
                 const int x = x0 + (idx % (TX / 4)) * 4;
                 const float *row = P + (int64_t)k * ld;
                 if (VEC == 4) {
@@ -141,7 +150,8 @@ struct Operand {
     }
 
     __device__ __forceinline__ void store(float *lds, int tid, int k0, int K) const {
-        const bool tail = k0 + BK > K;     // uniform: only the last slab
+        const int left = K - k0;
+        const bool tail = left < BK;       // uniform: only the last slab
 #pragma unroll
         for (int p = 0; p < NL; ++p) {
             const int idx = tid + THREADS * p;
@@ -150,12 +160,12 @@ struct Operand {
                 const int x = idx / (BK / 4), k = (idx % (BK / 4)) * 4;
                 if (tail) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = k0 + k + c < K ? v[c] : 0.f;
+                    for (int c = 0; c < 4; ++c) v[c] = k + c < left ? v[c] : 0.f;
                 }
                 *reinterpret_cast<v4f *>(lds + x * xstride<BK>() + k) = v;
             } else {
                 const int k = idx / (TX / 4), x = (idx % (TX / 4)) * 4;
-                if (tail && k0 + k >= K) v = v4f{0.f, 0.f, 0.f, 0.f};
+                if (tail && k >= left) v = v4f{0.f, 0.f, 0.f, 0.f};
                 *reinterpret_cast<v4f *>(lds + k * KS + x) = v;
             }
         }
@@ -238,7 +248,7 @@ __global__ __launch_bounds__(THREADS) void gemm_f32_kernel(
 #pragma unroll
         for (int j = 0; j < JB; ++j) epi.fetch(pre[i][j], col_of(j), M, N, row_of(i), all);
 
-    const int nk = (K + BK - 1) / BK;
+    const int nk = slabs_of<BK>(K);
     if (nk > 0) {
         la.load(A, lda, m0, 0, M, K, tid);
         lb.load(B, ldb, n0, 0, N, K, tid);

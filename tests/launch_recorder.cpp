@@ -11,6 +11,7 @@
 #include <map>
 #include <string>
 
+#include "gemm_f32_tile.hpp"
 #include "kernels.hpp"
 
 using namespace gg;
@@ -85,6 +86,12 @@ int main(int argc, char **argv) {
     } else if (call == "linear") {              // M N K, W as N x K
         e = launch_linear(n(5), 0, n(2), n(3), n(4), at<float>(1), n(4), at<float>(2),
                           n(5) ? n(4) : n(3), nullptr, nullptr, 0, nullptr, 0, out, n(3), 256, nullptr);
+    } else if (call == "k_walk") {              // K -> slabs; places in the last one
+        const int K = n(2), slabs = slabs_of<32>(K), k0 = (slabs - 1) * 32;
+        printf("%d\n", slabs);
+        for (int k = 0; k < 32; ++k) printf("%d ", clamp_k(k0, k, K - 1));
+        printf("\n");
+        e = hipSuccess;
     } else if (call == "rows_of_chunk") {       // M chunk index -> first row, end
         const RowRange r = dz_rows(n(2), dz_chunk(n(2)), n(3));
         printf("%lld %lld\n", (long long)r.first, (long long)r.end);

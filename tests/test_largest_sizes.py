@@ -104,6 +104,16 @@ def test_products_of_large_outputs(record, M, N, K, ta, tb):
         assert a[7] >= -(-m // 128) and a[8] >= -(-n // 64)
 
 
+@pytest.mark.parametrize("K", [1, 31, 32, 33, (1 << 30) + 5, MOST - 32, MOST - 31, MOST - 30, MOST - 1, MOST])
+def test_walk_along_k(record, K):
+    """The staged kernels' slabs of 32 columns: as many as K has, the last one's
+    places clamped to the last column.  (On the GPU one tile walks the longest
+    of them for over a minute, so that it is not run there.)"""
+    (slabs,), places = record("k_walk", K)
+    assert slabs == -(-K // 32)
+    assert places == [min((slabs - 1) * 32 + k, K - 1) for k in range(32)]
+
+
 @pytest.mark.parametrize("M,N,K", [(346, 768, 768), (2048, 2048, 2048), (1 << 24, 64, 16)])
 def test_ordinary_products_take_one_launch(record, M, N, K):
     assert len(record("gemm", M, N, K, 0, 0)) == 1
