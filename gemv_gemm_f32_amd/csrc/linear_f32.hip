@@ -231,19 +231,20 @@ template <int MB>
 hipError_t launch_few(bool trans_w, int M, int N, int K, const float *X, int64_t ldx,
                       const float *W, int64_t ldw, float *Y, int64_t ldy, const Layer &e,
                       int num_cus, hipStream_t s) {
-#define GG_FEW M, N, K, X, ldx, W, ldw, Y, ldy, e
-    if (!trans_w) {
-        const int64_t nb = ((int64_t)N + 31) / 32;
-        if (nb * 1024 > UINT32_MAX) return hipErrorInvalidValue;
-        return launch(linear_few_kn<MB, 16>, dim3((unsigned)nb), dim3(1024), s, GG_FEW);
-    }
-    if (N >= 8 * num_cus) {
-        const int64_t nb = ((int64_t)N + 3) / 4;
-        if (nb * 256 > UINT32_MAX) return hipErrorInvalidValue;
-        return launch(linear_few_nk<MB, 1, 4>, dim3((unsigned)nb), dim3(256), s, GG_FEW);
-    }
-    return launch(linear_few_nk<MB, 4, 1>, dim3((unsigned)N), dim3(256), s, GG_FEW);
+    // A launch has fewer than 2^32 threads: wider outputs take several.
+    constexpr int64_t MOST = 1 << 25;
+    for (int64_t n = 0; n < N; n += MOST) {
+        const int cols = (int)(N - n < MOST ? N - n : MOST);
+#define GG_FEW M, cols, K, X, ldx, W + (trans_w ? n * ldw : n), ldw, Y + n, ldy, e.from(0, n)
+        const hipError_t st =
+            !trans_w ? launch(linear_few_kn<MB, 16>, dim3((cols + 31) / 32), dim3(1024), s, GG_FEW)
+            : N >= 8 * num_cus
+                ? launch(linear_few_nk<MB, 1, 4>, dim3((cols + 3) / 4), dim3(256), s, GG_FEW)
+                : launch(linear_few_nk<MB, 4, 1>, dim3(cols), dim3(256), s, GG_FEW);
+        if (st != hipSuccess) return st;
 #undef GG_FEW
+    }
+    return hipSuccess;
 }
 
 }  // namespace

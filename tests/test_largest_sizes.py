@@ -104,6 +104,15 @@ def test_products_of_large_outputs(record, M, N, K, ta, tb):
         assert a[7] >= -(-m // 128) and a[8] >= -(-n // 64)
 
 
+@pytest.mark.parametrize("M,tw", [(1, 0), (3, 0), (4, 0), (1, 1), (2, 1), (8, 1)])
+@pytest.mark.parametrize("N", [1, 2047, 2048, 1 << 25, (1 << 25) + 1, (1 << 26) + 1, (1 << 27) + 1, MOST])
+def test_few_rows_over_many_columns(record, M, N, tw):
+    launches = record("linear", M, N, 3, tw)
+    assert len(launches) == -(-N // (1 << 25))
+    for (r, c, m, n), (name, _, _, _, a) in zip(_rectangles(launches, M, N), launches):
+        assert "linear_few" in name and m == M and a[5] == 0 and a[6] == (c * 3 if tw else c)
+
+
 @pytest.mark.parametrize("K", [1, 31, 32, 33, (1 << 30) + 5, MOST - 32, MOST - 31, MOST - 30, MOST - 1, MOST])
 def test_walk_along_k(record, K):
     """The staged kernels' slabs of 32 columns: as many as K has, the last one's
@@ -183,5 +192,26 @@ def test_layer_of_most_columns(tw):
     Y = bd.linear_f32(X, W[:, None] if tw else W[None], trans_w=bool(tw))
     ok = [_equal(Y[m], lambda i, j: _pattern(i, j) * (m + 1)) for m in range(9)]
     del W, Y
+    t.cuda.empty_cache()
+    assert all(ok)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tw", [0, 1])
+def test_two_rows_over_most_columns(tw):
+    """Bias, pre-activations and a residual updated in place past the columns
+    of one launch."""
+    t = torch()
+    W = t.empty(MOST, device="cuda")
+    for i in range(0, MOST, 1 << 28):
+        j = min(i + (1 << 28), MOST)
+        W[i:j] = _pattern(i, j)
+    X = t.tensor([[1.0], [2.0]], device="cuda")
+    Y = t.full((2, MOST), -5.0, device="cuda")
+    Z = t.empty((2, MOST), device="cuda")
+    bd.linear_f32(X, W[:, None] if tw else W[None], bias=W, residual=Y, Z=Z, Y=Y, act="relu", trans_w=bool(tw))
+    ok = [_equal(Z[m], lambda i, j: _pattern(i, j) * (m + 2)) and
+          _equal(Y[m], lambda i, j: _pattern(i, j) * (m + 2) - 5) for m in range(2)]
+    del W, Y, Z
     t.cuda.empty_cache()
     assert all(ok)
