@@ -450,11 +450,45 @@ __global__ __launch_bounds__(64 * NH * KW) void packed_rows_kernel(PackedLinear 
     }
 }
 
+// A launch has fewer than 2^32 threads: with `threads` for each bm x bn tile,
+// larger outputs are cut into rectangles (from multiples of 256, so that
+// blocks of 32 columns stay whole), and one(rectangle) launches each.
+template <class One>
+hipError_t in_parts(const PackedLinear &a, int bm, int bn, int threads, One one) {
+    int64_t rows = a.M, cols = a.N;
+    while (((rows + bm - 1) / bm) * ((cols + bn - 1) / bn) * threads > UINT32_MAX) {
+        int64_t &longer = rows >= cols ? rows : cols;
+        longer = ((longer + 1) / 2 + 255) & ~int64_t(255);
+    }
+    for (int64_t m = 0; m < a.M; m += rows)
+        for (int64_t n = 0; n < a.N; n += cols) {
+            PackedLinear p = a;
+            p.M = (int)(a.M - m < rows ? a.M - m : rows);
+            p.N = (int)(a.N - n < cols ? a.N - n : cols);
+            p.X += m * a.ldx;
+            p.XE += m * a.ldxe;
+            p.Q += n * a.ldq;
+            p.S += n * a.lds;
+            if (a.bias) p.bias += n;
+            if (a.R) p.R += m * a.ldr + n;
+            if (a.Y) p.Y += m * a.ldy + n;
+            if (a.Y8) {
+                p.Y8 += m * a.ldy8 + n;
+                p.YE += m * a.ldye + n / 32;
+            }
+            const hipError_t e = one(p);
+            if (e != hipSuccess) return e;
+        }
+    return hipSuccess;
+}
+
 template <int BITS, int NH, int KW>
 hipError_t launch_rows(const PackedLinear &a, hipStream_t s) {
-    const int64_t nb = ((int64_t)a.N + 16 * NH - 1) / (16 * NH);
-    if (nb * 64 * NH * KW > UINT32_MAX) return hipErrorInvalidValue;
-    return launch(packed_rows_kernel<BITS, NH, KW>, dim3((unsigned)nb), dim3(64 * NH * KW), s, a);
+    constexpr int COLS = 16 * NH, THREADS = 64 * NH * KW;
+    return in_parts(a, 16, COLS, THREADS, [s](const PackedLinear &p) {
+        const int64_t nb = ((int64_t)p.N + COLS - 1) / COLS;
+        return launch(packed_rows_kernel<BITS, NH, KW>, dim3((unsigned)nb), dim3(THREADS), s, p);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -659,7 +693,6 @@ __global__ __launch_bounds__(64 * KW, MW) void packed_block_kernel(PackedLinear 
 template <int KW, int BITS, int MW>
 hipError_t launch_block(const PackedLinear &a, hipStream_t s) {
     const int64_t tm = ((int64_t)a.M + 31) / 32, tn = ((int64_t)a.N + 31) / 32;
-    if (tm * tn * 64 * KW > UINT32_MAX) return hipErrorInvalidValue;
     return launch(packed_block_kernel<KW, BITS, MW>, dim3((unsigned)(tm * tn)), dim3(64 * KW), s, a, (int)tm);
 }
 
@@ -917,10 +950,11 @@ __global__ __launch_bounds__(64 * NW, MW) void packed_wide_kernel(PackedLinear a
 
 template <int BM, int NW, int BITS, int MW = 2>
 hipError_t launch_wide(const PackedLinear &a, hipStream_t s) {
-    const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + 32 * NW - 1) / (32 * NW);
-    if (tm * tn * 64 * NW > UINT32_MAX) return hipErrorInvalidValue;
-    return launch(packed_wide_kernel<BM, NW, BITS, MW>, dim3((unsigned)(tm * tn)), dim3(64 * NW), s, a,
-                  (int)tm);
+    return in_parts(a, BM, 32 * NW, 64 * NW, [s](const PackedLinear &p) {
+        const int64_t tm = ((int64_t)p.M + BM - 1) / BM, tn = ((int64_t)p.N + 32 * NW - 1) / (32 * NW);
+        return launch(packed_wide_kernel<BM, NW, BITS, MW>, dim3((unsigned)(tm * tn)), dim3(64 * NW), s, p,
+                      (int)tm);
+    });
 }
 
 template <int BITS>

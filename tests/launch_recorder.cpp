@@ -62,7 +62,13 @@ hipError_t hipLaunchKernel(const void *f, dim3 g, dim3 b, void **a, size_t, hipS
         printf("\n");
     } else if (has("packed_")) {
         const PackedLinear p = arg<PackedLinear>(a, 0);
-        printf("%d %d %d %lld %lld\n", p.M, p.N, p.K, from_out(p.Y) / 4, (long long)p.ldy);
+        printf("%d %d %d %lld %lld", p.M, p.N, p.K, from_out(p.Y) / 4, (long long)p.ldy);
+        printf(" %lld %lld %lld %lld", (long long)(p.X - at<uint8_t>(1)), (long long)(p.XE - at<uint8_t>(2)),
+               (long long)(p.Q - at<uint8_t>(3)), (long long)(p.S - at<uint16_t>(4)));
+        printf(" %lld %lld", p.Y8 ? (long long)(p.Y8 - at<uint8_t>(5)) : -1,
+               p.YE ? (long long)(p.YE - at<uint8_t>(6)) : -1);
+        printf(" %lld %lld\n", p.bias ? (long long)(p.bias - at<float>(7)) : -1,
+               p.R ? (long long)(p.R - at<float>(8)) : -1);
     } else {
         printf("\n");
     }
@@ -86,6 +92,15 @@ int main(int argc, char **argv) {
     } else if (call == "linear") {              // M N K, W as N x K
         e = launch_linear(n(5), 0, n(2), n(3), n(4), at<float>(1), n(4), at<float>(2),
                           n(5) ? n(4) : n(3), nullptr, nullptr, 0, nullptr, 0, out, n(3), 256, nullptr);
+    } else if (call == "packed") {              // bits M N K, to 8 bits as well
+        const int64_t N = n(4), K = n(5);
+        const int64_t ldq = (K * n(2) + 7) / 8;
+        const PackedLinear a{0, n(3), n(4), n(5), at<uint8_t>(1), at<uint8_t>(2), at<uint8_t>(3), at<uint16_t>(4),
+                             n(6) ? at<float>(7) : nullptr, n(6) ? at<float>(8) : nullptr, out,
+                             n(6) ? at<uint8_t>(5) : nullptr, n(6) ? at<uint8_t>(6) : nullptr,
+                             K, (K + 31) / 32, ldq, (K + 63) / 64, n(6) ? N : 0, N, n(6) ? N : 0,
+                             n(6) ? (N + 31) / 32 : 0};
+        e = launch_packed_linear(n(2), a, 256, nullptr);
     } else if (call == "k_walk") {              // K -> slabs; places in the last one
         const int K = n(2), slabs = slabs_of<32>(K), k0 = (slabs - 1) * 32;
         printf("%d\n", slabs);

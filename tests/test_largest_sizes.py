@@ -113,6 +113,21 @@ def test_few_rows_over_many_columns(record, M, N, tw):
         assert "linear_few" in name and m == M and a[5] == 0 and a[6] == (c * 3 if tw else c)
 
 
+@pytest.mark.parametrize("bits", [2, 4])
+@pytest.mark.parametrize("both", [0, 1])
+@pytest.mark.parametrize("M,N,K", [(1, MOST, 5), (16, MOST, 200), (17, MOST, 100), (1, 1 << 28, 1), (1, (1 << 28) + 1, 1),
+                                   (MOST, 1, 1), (MOST, 130, 300), ((1 << 30) + 1, 40, 64), (1 << 20, 1 << 17, 1536),
+                                   (500, 12288, 1536), (64, 4096, 4096), (1, 1536, 12288)])
+def test_packed_layers_of_large_outputs(record, M, N, K, both, bits):
+    launches = record("packed", bits, M, N, K, both)
+    if M * N < 1 << 28:
+        assert len(launches) == 1
+    for (r, c, m, n), (name, _, _, _, a) in zip(_rectangles(launches, M, N), launches):
+        assert "packed_" in name and a[2] == K and c % 32 == 0
+        assert a[5:9] == [r * K, r * -(-K // 32), c * -(-K * bits // 8), c * -(-K // 64)]
+        assert a[9:13] == ([r * N + c, r * -(-N // 32) + c // 32, c, r * N + c] if both else [-1] * 4)
+
+
 @pytest.mark.parametrize("K", [1, 31, 32, 33, (1 << 30) + 5, MOST - 32, MOST - 31, MOST - 30, MOST - 1, MOST])
 def test_walk_along_k(record, K):
     """The staged kernels' slabs of 32 columns: as many as K has, the last one's
@@ -215,3 +230,55 @@ def test_two_rows_over_most_columns(tw):
     del W, Y, Z
     t.cuda.empty_cache()
     assert all(ok)
+
+
+def _e4m3(q):
+    return q.view(torch().float8_e4m3fn).float()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [2, 4])
+def test_packed_token_of_most_columns(bits):
+    """One row of one column over 2^31 - 1 outputs, in fp32 and 8 bits: odd
+    halves, exact in both."""
+    t = torch()
+    Q = t.empty(MOST, dtype=t.uint8, device="cuda")
+    half = (1 << bits) - 1
+    for i in range(0, MOST, 1 << 28):
+        j = min(i + (1 << 28), MOST)
+        Q[i:j] = (_pattern(i, j).to(t.uint8) & half)
+    S = t.ones(MOST, dtype=t.float16, device="cuda")
+    X8 = t.full((1, 1), 0x38, dtype=t.uint8, device="cuda")                    # 1
+    XE = t.full((1, 1), 127, dtype=t.uint8, device="cuda")
+    f = bd.linear_q2_mx8 if bits == 2 else bd.linear_q4_mx8
+    Y, Y8, YE = f(X8, XE, Q[:, None], S[:, None], out="both")
+
+    def want(i, j):
+        return (_pattern(i, j).to(t.uint8) & half).float() - half / 2
+
+    def of_8_bits(i, j):
+        e = YE[0, i // 32:-(-j // 32)].float() - 127
+        return _e4m3(Y8[0, i:j]) * t.exp2(e).repeat_interleave(32)[:j - i]
+    ok = _equal(Y[0], want) and all(
+        bool((of_8_bits(i, min(i + (1 << 28), MOST)) == Y[0, i:i + (1 << 28)]).all()) for i in range(0, MOST, 1 << 28))
+    del Q, S, Y, Y8, YE
+    t.cuda.empty_cache()
+    assert ok
+
+
+@pytest.mark.gpu
+def test_packed_layer_of_most_rows():
+    """2^31 - 1 rows of one column, the residual updated in place."""
+    t = torch()
+    X8 = t.empty((MOST, 1), dtype=t.uint8, device="cuda")
+    for i in range(0, MOST, 1 << 28):
+        j = min(i + (1 << 28), MOST)
+        X8[i:j, 0] = (_pattern(i, j).to(t.uint8) & 7) + 0x38                  # 1, 1.125, ...
+    XE = t.full((MOST, 1), 127, dtype=t.uint8, device="cuda")
+    Y = t.full((MOST, 1), 2.0, device="cuda")
+    bd.linear_q4_mx8(X8, XE, t.full((1, 1), 15, dtype=t.uint8, device="cuda"),
+                     t.ones((1, 1), dtype=t.float16, device="cuda"), residual=Y, Y=Y)
+    ok = _equal(Y[:, 0], lambda i, j: 7.5 * _e4m3(X8[i:j, 0]) + 2)
+    del X8, XE, Y
+    t.cuda.empty_cache()
+    assert ok
