@@ -13,12 +13,17 @@
 // Element passes and epilogues are bound by memory only while an element costs
 // a few tens of instructions, so the exponential is the hardware's 2^x (its
 // argument's rounding makes a relative error of |t| 2^-23 in exp(t), at most
-// 2^-24 in p, where exp(t) counts for p (1 - p)), the quotient a product with
-// the hardware's reciprocal (1 step), and erf the rational form of Hastings
-// (Abramowitz and Stegun 7.1.26, absolute error 1.5e-7, half of that in p):
-// p is within 2^-22 of its value in all three.  With the library's erfc and
-// exp the slope of the erf form over 1024 x 4096 took 12.2 us against
-// 10.5, and the layer 1024 x 2304 x 768 41.2 against 39.1.
+// 2^-24 in p, where exp(t) counts for p (1 - p)) and the quotient a product with
+// the hardware's reciprocal (1 step): p is within 2^-22 of its value.
+//
+// The erf form is made of two least-maximum fits of its own (weighted by z and
+// by the tail's inverse, found by linear programming in 64 bits):
+//   |z| < 1.25:  p = 1/2 + z P(z^2), P of degree 5, within 2^-28.8
+//   beyond:      (1 - erf(|z| / sqrt 2)) / 2 = exp(-z^2 / 2) t Q(t) with
+//                t = 1 / (1 + 0.4 |z|), Q of degree 6, within 2^-24.3 relative
+// so p is within 2^-23 of its value and in the left tail, where p is small,
+// within (12 + 2 z^2) 2^-24 relative (to z = -13; 0 where exp(-z^2 / 2) falls
+// below 2^-126).
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -30,7 +35,6 @@ namespace gg {
 
 constexpr float GELU_2C = 1.5957691216057308f;        // 2 sqrt(2/pi)
 constexpr float GELU_2CA = 0.07135481627260025f;      // 2 sqrt(2/pi) * 0.044715
-constexpr float SQRT_HALF = 0.7071067811865476f;
 constexpr float INV_SQRT_2PI = 0.3989422804014327f;
 
 constexpr float LOG2E = 1.4426950408889634f;
@@ -44,15 +48,22 @@ __device__ __forceinline__ float logistic(float t) {
 
 // (1 + erf(z / sqrt 2)) / 2, and exp(-z^2 / 2) on the way
 __device__ __forceinline__ float normal_weight(float z, float &gauss) {
-    const float a = __builtin_fabsf(z) * SQRT_HALF;
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, a, 1.f));
-    float q = __builtin_fmaf(1.061405429f, t, -1.453152027f);
-    q = __builtin_fmaf(q, t, 1.421413741f);
-    q = __builtin_fmaf(q, t, -0.284496736f);
-    q = __builtin_fmaf(q, t, 0.254829592f);
-    gauss = exp_fast(-a * a);
-    const float tail = 0.5f * (q * t) * gauss;         // (1 - erf(a)) / 2
-    return z < 0.f ? tail : 1.f - tail;
+    const float a = __builtin_fabsf(z), zz = z * z;
+    gauss = __builtin_amdgcn_exp2f(-0.5f * LOG2E * zz);
+    float p = __builtin_fmaf(-6.6448406e-06f, zz, 1.10327375e-04f);
+    p = __builtin_fmaf(p, zz, -1.18270947e-03f);
+    p = __builtin_fmaf(p, zz, 9.97150037e-03f);
+    p = __builtin_fmaf(p, zz, -6.64899871e-02f);
+    p = __builtin_fmaf(p, zz, 0.398942262f);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.4f, a, 1.f));
+    float q = __builtin_fmaf(6.93908185e-02f, t, -0.189606979f);
+    q = __builtin_fmaf(q, t, 0.108559087f);
+    q = __builtin_fmaf(q, t, 5.38959317e-02f);
+    q = __builtin_fmaf(q, t, 0.139457434f);
+    q = __builtin_fmaf(q, t, 0.159035996f);
+    q = __builtin_fmaf(q, t, 0.159599349f);
+    const float tail = q * t * gauss;
+    return a < 1.25f ? __builtin_fmaf(z, p, 0.5f) : z < 0.f ? tail : 1.f - tail;
 }
 
 template <int ACT>

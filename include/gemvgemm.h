@@ -332,7 +332,7 @@ int gemv_q4_batched(int64_t count, int64_t M, int64_t K,
  * then updated in place.  Any other overlap of Y or Z with an input or with
  * each other gives GG_ERR_ALIAS.  With K = 0, Z is the bias.
  * Accuracy: Z as gemm_f32's result plus one rounding for the bias; the
- * activation adds at most 2^-19 |z|, the residual one rounding.  Non-finite inputs
+ * activation adds at most 2^-22 |z| and one rounding, the residual one more.  Non-finite inputs
  * follow IEEE arithmetic through the formulas above; an activation of minus
  * infinity is NaN except for ReLU's 0.
  */
