@@ -523,16 +523,18 @@ def linear_f32_bwd(dY, X, W, Z=None, act="none", trans_w=False, dX=None, dW=None
                    want=("dX", "dW", "db"), accumulate=False, workspace=None, stream=None):
     """Gradients (dX, dW, db) of linear_f32 from dY (M x N) and the kept
     pre-activation Z (not needed for act "none"); the residual's gradient is
-    dY itself.  Gradients not named in `want` are not computed and returned
+    dY itself.  X is needed for dW alone and W for dX; either may be None
+    otherwise.  Gradients not named in `want` are not computed and returned
     as None; outputs not given are allocated.  accumulate: dW and db, which
     must then be given, are added to."""
     torch = _torch()
     f32, dev = torch.float32, torch.cuda.current_device()
     M, N = _matrix(dY, "dY")
     wx, ww, wb = (n in want for n in ("dX", "dW", "db"))
-    K = _matrix(X, "X")[1] if X is not None else _matrix(W, "W")[1 if trans_w else 0]
     if (wx and W is None) or (ww and X is None):
         raise ValueError("dX needs W and dW needs X")
+    # db alone needs neither, and no K
+    K = _matrix(X, "X")[1] if X is not None else _matrix(W, "W")[1 if trans_w else 0] if W is not None else 0
     wshape = (N, K) if trans_w else (K, N)
     a = _activation(act)
     if a and Z is None:
