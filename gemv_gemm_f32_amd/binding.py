@@ -416,8 +416,8 @@ def _arg(t, shape, dtype, name, dev):
     shape and type on device number `dev`; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if getattr(t, "dtype", None) is not dtype:
+        raise _type_error(t, dtype, name)
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
     if t.get_device() != dev:
@@ -430,8 +430,14 @@ def _arg(t, shape, dtype, name, dev):
     return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] or 1
 
 
+def _type_error(t, dtype, name):
+    return TypeError("%s must be a torch tensor of %s, got %s" % (name, dtype, getattr(t, "dtype", type(t).__name__)))
+
+
 def _wide(t, rows, cols, dtype, name, dev):
     """As _arg for rows of at least `cols` entries."""
+    if getattr(t, "dtype", None) is not dtype:
+        raise _type_error(t, dtype, name)
     shape = t.shape
     if len(shape) != 2 or shape[1] < cols:
         raise ValueError("%s must be 2-D with at least %d columns" % (name, cols))
@@ -479,6 +485,8 @@ def _workspace(ws, need, dev, like, stream):
     torch = _torch()
     if ws is None:
         ws = _new((need,), torch.uint8, like, stream)
+    elif not isinstance(ws, torch.Tensor):
+        raise TypeError("the workspace must be a torch tensor")
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on the current GPU device")
     n = ws.numel() * ws.element_size()
@@ -581,7 +589,7 @@ def rmsnorm_f32(X, gamma=None, eps=1e-5, residual=None, S=None, Y=None, rstd=Non
 def _bytes(t):
     """A float8 tensor as its bytes; a uint8 tensor as it is."""
     torch = _torch()
-    if t is not None and t.dtype in (torch.float8_e4m3fn, torch.float8_e8m0fnu):
+    if getattr(t, "dtype", None) in (torch.float8_e4m3fn, torch.float8_e8m0fnu):
         return t.view(torch.uint8)
     return t
 
@@ -648,7 +656,7 @@ def _packed_linear(name, bits, X8, XE, Q, S, bias, act, residual, Y, Y8, YE, out
     X8, XE = _bytes(X8), _bytes(XE)
     M, K = _matrix(X8, "X8")
     N = _matrix(Q, "Q")[0]
-    if S.dtype is torch.int16:
+    if getattr(S, "dtype", None) is torch.int16:
         S = S.view(torch.float16)
     px, ldx = _arg(X8, (M, K), u8, "X8", dev)
     pe, ldxe = _arg(XE, (M, -(-K // 32)), u8, "XE", dev)
