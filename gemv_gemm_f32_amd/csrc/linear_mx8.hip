@@ -1,6 +1,6 @@
 // linear_mx8.hip -- Y = act(X8.W^T + b) + R with X8 in 8 bits (mx8.hpp) and W
 // as 2-bit or 4-bit codes with one binary16 scale per 64 columns, on gfx950's
-// block-scaled matrix instruction.
+// bf16 matrix instructions.
 //
 //   w(n, k) = (code - 7.5) s(n, k/64) = (2 code - 15) s/2     (4 bits)
 //   w(n, k) = (code - 1.5) s(n, k/64) = (2 code - 3) s/2      (2 bits)
@@ -9,7 +9,8 @@
 // e4m3 numbers times a power of two), so both operands are bf16 numbers
 // exactly and products are exact in fp32: v_mfma_f32_32x32x16_bf16 sums them in
 // fp32, group by group, and one fp32 multiply-add per sum and group applies
-// s/2.  Nothing is rounded but the sums.
+// s/2.  Nothing is rounded but the sums, and values of x below bf16's smallest
+// step, 2^-133 (in blocks whose power of two is 2^-125 or less), to that step.
 //
 // The 8-bit matrix instructions (f8f6f4 and fp8) would take both operands as
 // they are, twice as fast, but add products within parts of their k in an
@@ -705,9 +706,12 @@ hipError_t launch_block(const PackedLinear &a, hipStream_t s) {
 // matrix unit (4 x 4 x 32 cycles per wave and group), the vector unit (64
 // instructions of expansion, 64 multiply-adds) and LDS (16 KiB per wave) have
 // about equally much to do, so products and vector work are interleaved turn
-// by turn: 2048 x 4096 x 4096 takes 77 us at 2 bits and 79 at 4 (890 and 870
-// TFLOP/s, vector issue busy for two thirds of the time and the matrix unit for
-// half), 89 and 93 with a block's products before its vector work.  MW: waves
+// by turn: 2048 x 4096 x 4096 takes 73-77 us at 2 bits and 78-82 at 4 (890-940
+// and 840-880 TFLOP/s; at 4 bits vector issue is busy for 65% of the time and
+// the matrix unit for 44%), 89 and 93 with a block's products before its vector
+// work.  Four waves of 64 rows (three workgroups per CU) leave 168 registers, of
+// which 4 (2 bits) and 6 (4 bits) spill; 500 x 1536 x 12288 takes 31.5 and 34.5
+// us, a residual 2 and 2.5 more (vector issue 63 and 65%, matrix unit 29 and 25%).  MW: waves
 // per SIMD that the registers leave room for; a SIMD issues vector
 // instructions of one wave every 7 cycles, of two or more every 3 to 4.
 //

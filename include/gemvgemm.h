@@ -383,8 +383,9 @@ int64_t linear_f32_bwd_ws_size(int act, int64_t M, int64_t N);
  * S may be X itself or R itself (same pointer and leading dimension), which
  * updates a residual stream in place; any other overlap of an output with an
  * input or another output gives GG_ERR_ALIAS.  K = 0 writes nothing.
- * Squares and their sum are fp32: a row whose mean square leaves fp32's
- * range gives rstd = 0.  A row of zeros with eps = 0 gives NaN; a NaN or an
+ * Squares and their sum are fp32: a row whose mean square is past fp32's
+ * range gives rstd = 0, and one whose squares are all below it, with eps = 0,
+ * an infinite rstd.  A row of zeros with eps = 0 gives NaN; a NaN or an
  * infinity makes its own row's rstd NaN or 0, and no other row's.
  */
 int rmsnorm_f32(int64_t M, int64_t K, const float *X, int64_t ldx, const float *R, int64_t ldr,
@@ -442,7 +443,9 @@ int64_t rmsnorm_f32_bwd_ws_size(int64_t M, int64_t K);
  * Bits of codes for columns past K, scales past ceil(K/64) and bytes of X8
  * and XE past the row are never used.  Accuracy of the sums (before act and
  * R) as gemv_q4's, relative to sum_k |w(n,k) x(i,k)|: codes and 8-bit values
- * enter exactly, sums are fp32.  A NaN in a row of X makes that row of Y
+ * enter exactly (values below 2^-133, in blocks of a power of two of 2^-125 or
+ * less, rounded to a multiple of that), sums are fp32 and are formed of odd
+ * integers up to 15 times x before a scale is applied.  A NaN in a row of X makes that row of Y
  * NaN, a NaN scale its own column.
  */
 int linear_q4_mx8(int act, int64_t M, int64_t N, int64_t K,
