@@ -32,7 +32,11 @@ ENTRY_POINTS = ("gemm_f32", "gemm_f32_tn", "gemm_f32_nt", "gemm_f32_ex", "gemv_f
                 "gemv_q2_batched_ws_size", "gemv_q2_batched_noalloc", "gemv_q4",
                 "gemv_q4_batched", "linear_f32", "linear_f32_bwd", "linear_f32_bwd_ws_size",
                 "rmsnorm_f32", "rmsnorm_mx8", "rmsnorm_f32_bwd", "rmsnorm_f32_bwd_ws_size",
-                "linear_q2_mx8", "linear_q4_mx8", "gg_strerror")
+                "linear_q2_mx8", "linear_q4_mx8", "expert_groups", "expert_combine",
+                "expert_combine_bwd", "linear_f32_grouped", "linear_f32_grouped_bwd",
+                "linear_f32_grouped_bwd_ws_size", "linear_q2_mx8_grouped", "linear_q4_mx8_grouped",
+                "block_norm_f32", "block_norm_mx8", "block_norm_f32_bwd",
+                "block_norm_f32_bwd_ws_size", "gg_strerror")
 
 # enum gg_act by name
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu_tanh": 2, "gelu_erf": 3, "silu": 4}
@@ -116,6 +120,33 @@ def load(path: str = LIB_PATH):
         f.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp,
                       i64, vp, i64, vp, i64, vp]
         f.restype = i32
+    lib.expert_groups.argtypes = [i64, i64, i64, vp, i64, vp, vp, vp, i64, vp]
+    lib.expert_combine.argtypes = [i64, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.expert_combine_bwd.argtypes = [i64, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+                                       i64, vp, i64, vp]
+    lib.linear_f32_grouped.argtypes = [i32, i32, i64, i64, i64, i64, i64, vp, i64, vp, vp, vp, i64,
+                                       i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.linear_f32_grouped_bwd.argtypes = [i32, i32, i32, i64, i64, i64, i64, i64, vp, i64, vp, i64,
+                                           vp, i64, vp, vp, vp, i64, i64, vp, i64, vp, i64, i64, vp,
+                                           i64, vp, i64, vp]
+    for name in ("linear_q2_mx8_grouped", "linear_q4_mx8_grouped"):
+        f = getattr(lib, name)
+        f.argtypes = [i32, i64, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, i64, vp, i64,
+                      i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+        f.restype = i32
+    lib.block_norm_f32.argtypes = [i64, i64, vp, i64, vp, i64, vp, vp, i64, f32, vp, f32, vp, i64,
+                                   vp, i64, vp, vp, vp]
+    lib.block_norm_mx8.argtypes = [i64, i64, vp, i64, vp, i64, vp, vp, i64, f32, vp, f32, vp, i64,
+                                   vp, i64, vp, i64, vp]
+    lib.block_norm_f32_bwd.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, f32, vp,
+                                       vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp]
+    for name in ("expert_groups", "expert_combine", "expert_combine_bwd", "linear_f32_grouped",
+                 "linear_f32_grouped_bwd", "block_norm_f32", "block_norm_mx8", "block_norm_f32_bwd"):
+        getattr(lib, name).restype = i32
+    lib.linear_f32_grouped_bwd_ws_size.argtypes = [i32, i64, i64, i64]
+    lib.linear_f32_grouped_bwd_ws_size.restype = i64
+    lib.block_norm_f32_bwd_ws_size.argtypes = [i64, i64]
+    lib.block_norm_f32_bwd_ws_size.restype = i64
     lib.gg_strerror.argtypes = [ctypes.c_int]
     lib.gg_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -423,7 +454,7 @@ def _arg(t, shape, dtype, name, dev):
     if t.get_device() != dev:
         raise ValueError("%s must be on the current GPU device" % name)
     st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
+    if shape[-1] > 1 and st[-1] != 1 and t.numel():
         raise ValueError("%s must have a contiguous last dimension" % name)
     if len(shape) == 1:
         return t.data_ptr(), shape[0]
@@ -691,3 +722,349 @@ def linear_q4_mx8(X8, XE, Q, S, bias=None, act="none", residual=None, Y=None, Y8
     """As linear_q2_mx8 for gemv_q4's codes, Q (N x >= ceil(K/2))."""
     return _packed_linear("linear_q4_mx8", 4, X8, XE, Q, S, bias, act, residual, Y, Y8, YE, out,
                           stream)
+
+
+# ---------------------------------------------------- layers with experts --
+
+def _each(t, shape, dtype, name, dev):
+    """(address, leading dimension, stride) of a matrix per expert: a 3-D
+    tensor of this shape; (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    if getattr(t, "dtype", None) is not dtype:
+        raise _type_error(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current GPU device" % name)
+    st = t.stride()
+    if shape[2] > 1 and st[2] != 1 and t.numel():
+        raise ValueError("%s must have a contiguous last dimension" % name)
+    return t.data_ptr(), st[1] if shape[1] > 1 else shape[2] or 1, st[0] if shape[0] > 1 else 0
+
+
+def _three(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dim() != 3:
+        raise ValueError("%s must be 3-D" % name)
+    return tuple(t.shape)
+
+
+def _grouping(offsets, rows, X_rows, E, M, dev):
+    """(address of rows, address of offsets, M) of a layer on grouped rows; M
+    is given, or that of X without rows."""
+    i32 = _torch().int32
+    po, _ = _arg(offsets, (E + 1,), i32, "offsets", dev)
+    if po is None:
+        raise TypeError("offsets must be a torch tensor of int32")
+    if rows is None:
+        if M is not None and M != X_rows:
+            raise ValueError("without rows, X must have a row for each of the %d rows" % M)
+        return None, po, X_rows
+    if getattr(rows, "dtype", None) is not i32:
+        raise _type_error(rows, i32, "rows")
+    if M is None:
+        M = rows.numel()
+    pr, _ = _arg(rows, (M,), i32, "rows", dev)
+    return pr, po, M
+
+
+def expert_groups(ids, E, offsets=None, rows=None, pos=None, stream=None):
+    """(offsets, rows, pos) of the T x k expert numbers ids (int32): the pairs
+    (t, j) in the order of their experts.  offsets (E + 1,): group e is places
+    offsets[e] .. offsets[e + 1] - 1; rows (T*k,): the token at each place; pos
+    (T x k): each pair's place.  Pairs whose id is not in 0 .. E-1 come last
+    and have pos -1."""
+    torch = _torch()
+    i32, dev = torch.int32, torch.cuda.current_device()
+    T, k = _matrix(ids, "ids")
+    pi, ldi = _arg(ids, (T, k), i32, "ids", dev)
+    if not 0 <= E <= 1024:
+        raise ValueError("E must be in 0 .. 1024")
+    offsets, po, _ = _out(offsets, (E + 1,), i32, "offsets", dev, ids, stream)
+    rows, pr, _ = _out(rows, (T * k,), i32, "rows", dev, ids, stream)
+    pos, pp, ldp = _out(pos, (T, k), i32, "pos", dev, ids, stream)
+    _check(load().expert_groups(T, k, E, pi, ldi, po, pr, pp, ldp, _stream(stream, dev)), "expert_groups")
+    return offsets, rows, pos
+
+
+def expert_combine(Y, pos, weights=None, residual=None, out=None, stream=None):
+    """out_t = residual_t + sum_j weights_tj Y[pos_tj], fp32: Y (M x K) in
+    grouped order, pos (T x k) int32 as expert_groups returns it, weights (T x
+    k; ones when None), residual and out (T x K).  Entries of pos outside of Y
+    add nothing.  out may be the residual itself."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    M, K = _matrix(Y, "Y")
+    T, k = _matrix(pos, "pos")
+    py, ldy = _arg(Y, (M, K), f32, "Y", dev)
+    pp, ldp = _arg(pos, (T, k), torch.int32, "pos", dev)
+    pw, ldw = _arg(weights, (T, k), f32, "weights", dev)
+    pr, ldr = _arg(residual, (T, K), f32, "residual", dev)
+    out, po, ldo = _out(out, (T, K), f32, "out", dev, Y, stream)
+    _check(load().expert_combine(T, k, M, K, py, ldy, pp, ldp, pw, ldw, pr, ldr, po, ldo,
+                                 _stream(stream, dev)), "expert_combine")
+    return out
+
+
+def expert_combine_bwd(dO, pos, Y=None, weights=None, M=None, dY=None, dw=None, want=("dY", "dw"),
+                       stream=None):
+    """Gradients (dY, dw) of expert_combine from dO (T x K): dY (M x K) in
+    grouped order and dw (T x k).  Y is needed for dw; M, where neither Y nor
+    dY is given, is T*k.  Gradients not named in `want` are returned as None.
+    Rows of dY that no entry of pos names are not written; the residual's
+    gradient is dO itself."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    T, K = _matrix(dO, "dO")
+    k = _matrix(pos, "pos")[1]
+    wy, ww = "dY" in want, "dw" in want
+    if ww and Y is None:
+        raise ValueError("dw needs Y")
+    if M is None:
+        M = _matrix(Y, "Y")[0] if Y is not None else _matrix(dY, "dY")[0] if dY is not None else T * k
+    pd, ldd = _arg(dO, (T, K), f32, "dO", dev)
+    pp, ldp = _arg(pos, (T, k), torch.int32, "pos", dev)
+    py, ldy = _arg(Y, (M, K), f32, "Y", dev)
+    pw, ldw = _arg(weights, (T, k), f32, "weights", dev)
+    none = (None, None, 0)
+    dY, pdy, lddy = _out(dY, (M, K), f32, "dY", dev, dO, stream) if wy else none
+    dw, pdw, lddw = _out(dw, (T, k), f32, "dw", dev, dO, stream) if ww else none
+    _check(load().expert_combine_bwd(T, k, M, K, pd, ldd, py, ldy, pp, ldp, pw, ldw, pdy, lddy, pdw,
+                                     lddw, _stream(stream, dev)), "expert_combine_bwd")
+    return dY, dw
+
+
+def linear_f32_grouped(X, W, offsets, rows=None, bias=None, act="none", Z=None, Y=None, trans_w=False,
+                       stream=None):
+    """Y_i = act(X[rows_i].op(W_e) + bias_e), fp32, for the rows i of group e,
+    offsets[e] <= i < offsets[e + 1]: W (E x K x N, or E x N x K when trans_w),
+    offsets (E + 1,) and rows (M,) int32 as expert_groups returns them, bias (E
+    x N), Z (receives the pre-activation) and Y (M x N).  Without rows, X has
+    the M rows in grouped order.  Rows of Y outside of the groups are not
+    written."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    T, K = _matrix(X, "X")
+    wshape = _three(W, "W")
+    E, N = wshape[0], wshape[1] if trans_w else wshape[2]
+    px, ldx = _arg(X, (T, K), f32, "X", dev)
+    pr, po, M = _grouping(offsets, rows, T, E, None, dev)
+    pw, ldw, sw = _each(W, (E, N, K) if trans_w else (E, K, N), f32, "W", dev)
+    pb, ldb = _arg(bias, (E, N), f32, "bias", dev)
+    pz, ldz = _arg(Z, (M, N), f32, "Z", dev)
+    Y, py, ldy = _out(Y, (M, N), f32, "Y", dev, X, stream)
+    _check(load().linear_f32_grouped(int(bool(trans_w)), _activation(act), M, N, K, E, T, px, ldx, pr,
+                                     po, pw, ldw, sw, pb, ldb, pz, ldz, py, ldy, _stream(stream, dev)),
+           "linear_f32_grouped")
+    return Y
+
+
+def linear_f32_grouped_bwd_ws_size(act, M, N, E):
+    """Bytes of workspace linear_f32_grouped_bwd needs for an M x N output of E
+    groups."""
+    return _ws_size("linear_f32_grouped_bwd_ws_size", _activation(act), M, N, E)
+
+
+def linear_f32_grouped_bwd(dY, X, W, offsets, rows=None, Z=None, act="none", trans_w=False, dX=None,
+                           dW=None, db=None, want=("dX", "dW", "db"), accumulate=False, workspace=None,
+                           stream=None):
+    """Gradients (dX, dW, db) of linear_f32_grouped from dY (M x N) and the kept
+    pre-activation Z (not needed for act "none").  dX (M x K) is in grouped
+    order: expert_combine of it without weights is the tokens' gradient.  X is
+    needed for dW alone; W always (its shape is that of dW).  `want`,
+    accumulate and outputs as linear_f32_bwd."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    M, N = _matrix(dY, "dY")
+    wx, ww, wb = (n in want for n in ("dX", "dW", "db"))
+    E, r, c = _three(W, "W")
+    K = c if trans_w else r
+    if (r if trans_w else c) != N:
+        raise ValueError("W must have %d outputs" % N)
+    if ww and X is None:
+        raise ValueError("dW needs X")
+    a = _activation(act)
+    if a and Z is None:
+        raise ValueError("act %r needs Z" % act)
+    if accumulate and ((ww and dW is None) or (wb and db is None)):
+        raise ValueError("accumulate needs the gradients to add to")
+    T = _matrix(X, "X")[0] if X is not None else M if rows is None else 1
+    pd, lddy = _arg(dY, (M, N), f32, "dY", dev)
+    pz, ldz = _arg(Z if a else None, (M, N), f32, "Z", dev)
+    px, ldx = _arg(X, (T, K), f32, "X", dev)
+    pr, po, _ = _grouping(offsets, rows, T, E, M, dev)
+    pw, ldw, sw = _each(W, (E, r, c), f32, "W", dev)
+    none = (None, None, 0)
+    dX, pdx, lddx = _out(dX, (M, K), f32, "dX", dev, dY, stream) if wx else none
+    pdw = lddw = sdw = 0
+    if ww:
+        dW = _new((E, r, c), f32, dY, stream) if dW is None else dW
+        pdw, lddw, sdw = _each(dW, (E, r, c), f32, "dW", dev)
+    else:
+        dW = None
+    db, pdb, lddb = _out(db, (E, N), f32, "db", dev, dY, stream) if wb else none
+    need = _ws_size("linear_f32_grouped_bwd_ws_size", a, M, N, E)
+    keep, pws, nws = _workspace(workspace, need, dev, dY, stream)
+    _check(load().linear_f32_grouped_bwd(int(bool(trans_w)), a, int(bool(accumulate)), M, N, K, E, T, pd,
+                                         lddy, pz, ldz, px, ldx, pr, po, pw, ldw, sw, pdx, lddx, pdw,
+                                         lddw, sdw, pdb, lddb, pws, nws, _stream(stream, dev)),
+           "linear_f32_grouped_bwd")
+    return dX, dW, db
+
+
+def _packed_grouped(name, bits, X8, XE, Q, S, offsets, rows, bias, act, Y, Y8, YE, out, stream):
+    torch = _torch()
+    f32, u8, dev = torch.float32, torch.uint8, torch.cuda.current_device()
+    if out not in ("f32", "mx8", "both"):
+        raise ValueError("out must be f32, mx8 or both")
+    X8, XE = _bytes(X8), _bytes(XE)
+    T, K = _matrix(X8, "X8")
+    E, N, qc = _three(Q, "Q")
+    sc = _three(S, "S")[2]
+    if qc < -(-K * bits // 8) or sc < -(-K // 64):
+        raise ValueError("Q and S must have columns for %d inputs" % K)
+    if S.dtype is torch.int16:
+        S = S.view(torch.float16)
+    px, ldx = _arg(X8, (T, K), u8, "X8", dev)
+    pe, ldxe = _arg(XE, (T, -(-K // 32)), u8, "XE", dev)
+    pr, po, M = _grouping(offsets, rows, T, E, None, dev)
+    pq, ldq, sq = _each(Q, (E, N, qc), u8, "Q", dev)
+    ps, lds, ss = _each(S, (E, N, sc), torch.float16, "S", dev)
+    pb, ldb = _arg(bias, (E, N), f32, "bias", dev)
+    py = ldy = p8 = ldy8 = pye = ldye = 0
+    if out != "mx8":
+        Y, py, ldy = _out(Y, (M, N), f32, "Y", dev, X8, stream)
+    if out != "f32":
+        Y8, p8, ldy8 = _out(_bytes(Y8), (M, N), u8, "Y8", dev, X8, stream)
+        YE, pye, ldye = _out(_bytes(YE), (M, -(-N // 32)), u8, "YE", dev, X8, stream)
+    _check(getattr(load(), name)(_activation(act), M, N, K, E, T, px, ldx, pe, ldxe, pr, po, pq, ldq, sq,
+                                 ps, lds, ss, pb, ldb, py, ldy, p8, ldy8, pye, ldye,
+                                 _stream(stream, dev)), name)
+    return Y if out == "f32" else (Y8, YE) if out == "mx8" else (Y, Y8, YE)
+
+
+def linear_q2_mx8_grouped(X8, XE, Q, S, offsets, rows=None, bias=None, act="none", Y=None, Y8=None,
+                          YE=None, out="f32", stream=None):
+    """linear_q2_mx8 on rows grouped by expert: Y_i = act(X[rows_i].W_e^T +
+    bias_e) with Q (E x N x >= ceil(K/4)), S (E x N x >= ceil(K/64)), bias (E x
+    N), offsets and rows as linear_f32_grouped; `out` as linear_q2_mx8."""
+    return _packed_grouped("linear_q2_mx8_grouped", 2, X8, XE, Q, S, offsets, rows, bias, act, Y, Y8, YE,
+                           out, stream)
+
+
+def linear_q4_mx8_grouped(X8, XE, Q, S, offsets, rows=None, bias=None, act="none", Y=None, Y8=None,
+                          YE=None, out="f32", stream=None):
+    """As linear_q2_mx8_grouped for gemv_q4's codes, Q (E x N x >= ceil(K/2))."""
+    return _packed_grouped("linear_q4_mx8_grouped", 4, X8, XE, Q, S, offsets, rows, bias, act, Y, Y8, YE,
+                           out, stream)
+
+
+# ------------------------------------------------- the norms around a block --
+
+def _gate(gate, M, K, dev):
+    """(address, leading dimension) of a gate: 0 for one that serves all rows."""
+    if gate is None:
+        return None, 0
+    f32 = _torch().float32
+    if getattr(gate, "dtype", None) is not f32:
+        raise _type_error(gate, f32, "gate")
+    if gate.dim() == 1:
+        return _arg(gate, (K,), f32, "gate", dev)[0], 0
+    pg, ldg = _arg(gate, (M, K), f32, "gate", dev)
+    if ldg == 0:
+        raise ValueError("a gate that serves all rows must be a vector")
+    return pg, ldg
+
+
+def block_norm_f32(U, X, gamma_u=None, gamma_s=None, eps=1e-5, gate=None, alpha=1.0, S=None, Y=None,
+                   rstd_u=None, rstd_s=None, stream=None):
+    """(Y, S, rstd_u, rstd_s) with S = alpha * X + gate * norm(U) * gamma_u and Y
+    = norm(S) * gamma_s, fp32, where norm divides a row by the root of its mean
+    square plus eps: U, the block's output, and X, the residual stream (M x K);
+    gamma_u and gamma_s (K,), ones when None; gate (K,) for all rows, (M x K),
+    or None for ones.  S may be given as X itself, to update it in place."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    M, K = _matrix(U, "U")
+    pu, ldu = _arg(U, (M, K), f32, "U", dev)
+    px, ldx = _arg(X, (M, K), f32, "X", dev)
+    pgu, _ = _arg(gamma_u, (K,), f32, "gamma_u", dev)
+    pgs, _ = _arg(gamma_s, (K,), f32, "gamma_s", dev)
+    pg, ldg = _gate(gate, M, K, dev)
+    S, ps, lds = _out(S, (M, K), f32, "S", dev, U, stream)
+    Y, py, ldy = _out(Y, (M, K), f32, "Y", dev, U, stream)
+    rstd_u, pru, _ = _out(rstd_u, (M,), f32, "rstd_u", dev, U, stream)
+    rstd_s, prs, _ = _out(rstd_s, (M,), f32, "rstd_s", dev, U, stream)
+    _check(load().block_norm_f32(M, K, pu, ldu, px, ldx, pgu, pg, ldg, float(alpha), pgs, float(eps), ps,
+                                 lds, py, ldy, pru, prs, _stream(stream, dev)), "block_norm_f32")
+    return Y, S, rstd_u, rstd_s
+
+
+def block_norm_mx8(U, X, gamma_u=None, gamma_s=None, eps=1e-5, gate=None, alpha=1.0, S=None, Q=None,
+                   E=None, stream=None):
+    """(Q, E, S): block_norm_f32 with its output in 8 bits, as rmsnorm_mx8's."""
+    torch = _torch()
+    f32, u8, dev = torch.float32, torch.uint8, torch.cuda.current_device()
+    M, K = _matrix(U, "U")
+    pu, ldu = _arg(U, (M, K), f32, "U", dev)
+    px, ldx = _arg(X, (M, K), f32, "X", dev)
+    pgu, _ = _arg(gamma_u, (K,), f32, "gamma_u", dev)
+    pgs, _ = _arg(gamma_s, (K,), f32, "gamma_s", dev)
+    pg, ldg = _gate(gate, M, K, dev)
+    S, ps, lds = _out(S, (M, K), f32, "S", dev, U, stream)
+    Q, pq, ldq = _out(_bytes(Q), (M, K), u8, "Q", dev, U, stream)
+    E, pe, lde = _out(_bytes(E), (M, -(-K // 32)), u8, "E", dev, U, stream)
+    _check(load().block_norm_mx8(M, K, pu, ldu, px, ldx, pgu, pg, ldg, float(alpha), pgs, float(eps), ps,
+                                 lds, pq, ldq, pe, lde, _stream(stream, dev)), "block_norm_mx8")
+    return Q, E, S
+
+
+def block_norm_f32_bwd_ws_size(M, K):
+    """Bytes of workspace block_norm_f32_bwd needs for its sums over rows."""
+    return _ws_size("block_norm_f32_bwd_ws_size", M, K)
+
+
+def block_norm_f32_bwd(dY, U, S, gamma_u, gamma_s, rstd_u, rstd_s, gate=None, alpha=1.0, dS=None, dU=None,
+                       dX=None, dgamma_u=None, dgamma_s=None, dgate=None,
+                       want=("dU", "dX", "dgamma_u", "dgamma_s", "dgate"), accumulate=False,
+                       workspace=None, stream=None):
+    """Gradients (dU, dX, dgamma_u, dgamma_s, dgate) of block_norm_f32 from dY
+    (M x K), with the U that it was given and the S, rstd_u and rstd_s that it
+    returned.  dS: the gradient that reaches S past the norm; dX may be dS
+    itself.  dgate has the gate's shape (None without a gate).  Gradients not
+    named in `want` are returned as None.  accumulate: the gradients that are
+    sums over rows (vectors), which must then be given, are added to."""
+    torch = _torch()
+    f32, dev = torch.float32, torch.cuda.current_device()
+    M, K = _matrix(dY, "dY")
+    wu, wx, wgu, wgs, wg = (n in want for n in ("dU", "dX", "dgamma_u", "dgamma_s", "dgate"))
+    pd, lddy = _arg(dY, (M, K), f32, "dY", dev)
+    pu, ldu = _arg(U, (M, K), f32, "U", dev)
+    ps, lds = _arg(S, (M, K), f32, "S", dev)
+    pgu, _ = _arg(gamma_u, (K,), f32, "gamma_u", dev)
+    pgs, _ = _arg(gamma_s, (K,), f32, "gamma_s", dev)
+    pg, ldg = _gate(gate, M, K, dev)
+    wg = wg and gate is not None
+    shared = wg and ldg == 0
+    if accumulate and ((wgu and dgamma_u is None) or (wgs and dgamma_s is None) or
+                       (shared and dgate is None)):
+        raise ValueError("accumulate needs the gradients to add to")
+    pru, _ = _arg(rstd_u, (M,), f32, "rstd_u", dev)
+    prs, _ = _arg(rstd_s, (M,), f32, "rstd_s", dev)
+    pds, ldds = _arg(dS, (M, K), f32, "dS", dev)
+    none = (None, None, 0)
+    dU, pdu, lddu = _out(dU, (M, K), f32, "dU", dev, dY, stream) if wu else none
+    dX, pdx, lddx = _out(dX, (M, K), f32, "dX", dev, dY, stream) if wx else none
+    dgamma_u, pdgu, _ = _out(dgamma_u, (K,), f32, "dgamma_u", dev, dY, stream) if wgu else none
+    dgamma_s, pdgs, _ = _out(dgamma_s, (K,), f32, "dgamma_s", dev, dY, stream) if wgs else none
+    dgate, pdg, lddg = _out(dgate, tuple(gate.shape), f32, "dgate", dev, dY, stream) if wg else none
+    need = _ws_size("block_norm_f32_bwd_ws_size", M, K) if wgu or wgs or shared else 0
+    keep, pws, nws = _workspace(workspace, need, dev, dY, stream)
+    _check(load().block_norm_f32_bwd(int(bool(accumulate)), M, K, pd, lddy, pu, ldu, ps, lds, pgu, pg,
+                                     ldg, float(alpha), pgs, pru, prs, pds, ldds, pdu, lddu, pdx, lddx,
+                                     pdgu, pdgs, pdg, lddg, pws, nws, _stream(stream, dev)),
+           "block_norm_f32_bwd")
+    return dU, dX, dgamma_u, dgamma_s, dgate

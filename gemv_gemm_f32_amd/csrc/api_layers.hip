@@ -15,77 +15,6 @@ using namespace gg;
 
 namespace {
 
-bool bad_size(int64_t n) { return n < 0 || n > kMaxDim; }
-bool bad_act(int act) { return act < GG_ACT_NONE || act > GG_ACT_SILU; }
-
-// The operands of one call, checked as they are added: a pointer that is
-// null or misaligned, a short leading dimension or a range past the address
-// space makes the call invalid.  Absent operands are not added.
-class Operands {
-public:
-    // An input, or an output, of rows x cols elements of `elem` bytes at p.
-    Operands &in(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t elem = 4) {
-        return add(INPUT, p, rows, cols, ld, elem);
-    }
-    Operands &out(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t elem = 4) {
-        return add(OUTPUT, p, rows, cols, ld, elem);
-    }
-    // An input that the output `onto` may replace in place, and that output:
-    // the same pointer and leading dimension.
-    Operands &replaced(const void *p, int64_t rows, int64_t cols, int64_t ld) {
-        return add(REPLACED, p, rows, cols, ld, 4);
-    }
-    Operands &onto(const void *p, int64_t rows, int64_t cols, int64_t ld) {
-        return add(ONTO, p, rows, cols, ld, 4);
-    }
-    // a workspace of `need` bytes (floats in number), 16-byte aligned
-    Operands &workspace(const void *p, int64_t bytes, unsigned __int128 need) {
-        if (need == 0) return *this;
-        const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-        if (bytes < 0 || need > (unsigned __int128)bytes || bad_ptr(p, 16) || need > UINTPTR_MAX - b) {
-            bad_ = true;
-            return *this;
-        }
-        op_[n_++] = {{b, b + (uintptr_t)need}, OUTPUT, p, 0};
-        return *this;
-    }
-    // GG_OK, or why the call is refused.
-    int status() const {
-        if (bad_) return GG_ERR_INVALID_ARG;
-        for (int i = 0; i < n_; ++i) {
-            if (op_[i].kind != OUTPUT && op_[i].kind != ONTO) continue;
-            for (int j = 0; j < n_; ++j) {
-                if (i == j || !overlaps(op_[i].s, op_[j].s)) continue;
-                if (op_[i].kind != ONTO || op_[j].kind != REPLACED || op_[i].p != op_[j].p ||
-                    op_[i].ld != op_[j].ld)
-                    return GG_ERR_ALIAS;
-            }
-        }
-        return GG_OK;
-    }
-
-private:
-    enum Kind { INPUT, OUTPUT, REPLACED, ONTO };
-    Operands &add(Kind kind, const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
-        if (rows == 0 || cols == 0) return *this;
-        if (ld < cols || ld > kMaxDim || bad_ptr(p, elem) || wraps(p, rows, cols, ld, elem)) {
-            bad_ = true;
-            return *this;
-        }
-        op_[n_++] = {span(p, rows, cols, ld, elem), kind, p, ld};
-        return *this;
-    }
-    struct Op {
-        Span s;
-        Kind kind;
-        const void *p;
-        int64_t ld;
-    };
-    Op op_[12];          // no entry point has more
-    int n_ = 0;
-    bool bad_ = false;
-};
-
 int packed_linear(int bits, int act, int64_t M, int64_t N, int64_t K, const uint8_t *X8,
                   int64_t ldx, const uint8_t *XE, int64_t ldxe, const uint8_t *Q, int64_t ldq,
                   const uint16_t *S, int64_t lds, const float *bias, const float *R, int64_t ldr,

@@ -98,4 +98,102 @@ inline bool outputs_disjoint(std::vector<Iv> &iv) {
     return true;
 }
 
+inline bool bad_size(int64_t n) { return n < 0 || n > kMaxDim; }
+inline bool bad_act(int act) { return act < GG_ACT_NONE || act > GG_ACT_SILU; }
+
+// The operands of one call, checked as they are added: a pointer that is
+// null or misaligned, a short leading dimension or a range past the address
+// space makes the call invalid.  Absent operands are not added.
+class Operands {
+public:
+    // An input, or an output, of rows x cols elements of `elem` bytes at p.
+    Operands &in(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t elem = 4) {
+        return add(INPUT, p, rows, cols, ld, elem);
+    }
+    Operands &out(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t elem = 4) {
+        return add(OUTPUT, p, rows, cols, ld, elem);
+    }
+    // n matrices of rows x cols elements, `stride` elements apart.
+    Operands &in_each(const void *p, int64_t n, int64_t stride, int64_t rows, int64_t cols, int64_t ld,
+                      int64_t elem = 4) {
+        return add_each(INPUT, p, n, stride, rows, cols, ld, elem);
+    }
+    Operands &out_each(const void *p, int64_t n, int64_t stride, int64_t rows, int64_t cols, int64_t ld,
+                       int64_t elem = 4) {
+        return add_each(OUTPUT, p, n, stride, rows, cols, ld, elem);
+    }
+    // An input that the output `onto` may replace in place, and that output:
+    // the same pointer and leading dimension.
+    Operands &replaced(const void *p, int64_t rows, int64_t cols, int64_t ld) {
+        return add(REPLACED, p, rows, cols, ld, 4);
+    }
+    Operands &onto(const void *p, int64_t rows, int64_t cols, int64_t ld) {
+        return add(ONTO, p, rows, cols, ld, 4);
+    }
+    // a workspace of `need` bytes (floats in number), 16-byte aligned
+    Operands &workspace(const void *p, int64_t bytes, unsigned __int128 need) {
+        if (need == 0) return *this;
+        const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+        if (bytes < 0 || need > (unsigned __int128)bytes || bad_ptr(p, 16) || need > UINTPTR_MAX - b) {
+            bad_ = true;
+            return *this;
+        }
+        op_[n_++] = {{b, b + (uintptr_t)need}, OUTPUT, p, 0};
+        return *this;
+    }
+    // GG_OK, or why the call is refused.
+    int status() const {
+        if (bad_) return GG_ERR_INVALID_ARG;
+        for (int i = 0; i < n_; ++i) {
+            if (op_[i].kind != OUTPUT && op_[i].kind != ONTO) continue;
+            for (int j = 0; j < n_; ++j) {
+                if (i == j || !overlaps(op_[i].s, op_[j].s)) continue;
+                if (op_[i].kind != ONTO || op_[j].kind != REPLACED || op_[i].p != op_[j].p ||
+                    op_[i].ld != op_[j].ld)
+                    return GG_ERR_ALIAS;
+            }
+        }
+        return GG_OK;
+    }
+
+private:
+    enum Kind { INPUT, OUTPUT, REPLACED, ONTO };
+    Operands &add(Kind kind, const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
+        if (rows == 0 || cols == 0) return *this;
+        if (ld < cols || ld > kMaxDim || bad_ptr(p, elem) || wraps(p, rows, cols, ld, elem)) {
+            bad_ = true;
+            return *this;
+        }
+        op_[n_++] = {span(p, rows, cols, ld, elem), kind, p, ld};
+        return *this;
+    }
+    // Outputs must not overlap each other, and no stride is negative.
+    Operands &add_each(Kind kind, const void *p, int64_t n, int64_t stride, int64_t rows, int64_t cols,
+                       int64_t ld, int64_t elem) {
+        if (n == 0 || rows == 0 || cols == 0) return *this;
+        const int before = n_;
+        add(kind, p, rows, cols, ld, elem);
+        if (n_ == before || n == 1) return *this;
+        const unsigned __int128 one = extent_bytes(rows, cols, ld, elem);
+        if (stride < 0 || (kind == OUTPUT && (unsigned __int128)stride * (uint64_t)elem < one)) {
+            bad_ = true;
+            return *this;
+        }
+        const unsigned __int128 all = (unsigned __int128)(n - 1) * (uint64_t)stride * (uint64_t)elem + one;
+        const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+        if (all > (unsigned __int128)(UINTPTR_MAX - b)) bad_ = true;
+        else op_[before].s = {b, b + (uintptr_t)all};
+        return *this;
+    }
+    struct Op {
+        Span s;
+        Kind kind;
+        const void *p;
+        int64_t ld;
+    };
+    Op op_[20];          // no entry point has more
+    int n_ = 0;
+    bool bad_ = false;
+};
+
 }  // namespace gg

@@ -183,11 +183,8 @@ struct Operand {
     }
 };
 
-// Grid index -> (tile row, tile column).
-__device__ __forceinline__ void tile_of(int bid, int nwg, int tiles_m, int tiles_n,
-                                        int &tm, int &tn) {
-    int t = bid;
-    if ((nwg & 7) == 0) t = (bid & 7) * (nwg >> 3) + (bid >> 3);   // XCD runs
+// Place in the tile order -> (tile row, tile column).
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &tm, int &tn) {
     const int per_group = GROUP_M * tiles_n;
     const int group = t / per_group;
     const int first_m = group * GROUP_M;
@@ -195,6 +192,14 @@ __device__ __forceinline__ void tile_of(int bid, int nwg, int tiles_m, int tiles
     const int in_group = t - group * per_group;
     tm = first_m + in_group % gsize;
     tn = in_group / gsize;
+}
+
+// Grid index -> (tile row, tile column).
+__device__ __forceinline__ void tile_of(int bid, int nwg, int tiles_m, int tiles_n,
+                                        int &tm, int &tn) {
+    int t = bid;
+    if ((nwg & 7) == 0) t = (bid & 7) * (nwg >> 3) + (bid >> 3);   // XCD runs
+    tile_at(t, tiles_m, tiles_n, tm, tn);
 }
 
 // AX: A is stored M x K (x-major tiles); otherwise K x M.
@@ -359,13 +364,18 @@ struct DirectOperand {
     int kof[NI];         // k of this lane's chunk (x-major) or row (k-major) in the slab
 
     __device__ __forceinline__ void init(int64_t ld, int x0, int X, int lane, int wave) {
+        init(ld, x0, X, lane, wave, [&](int row) { return min(x0 + row, X - 1); });
+    }
+    // x_of(row): which x an x-major stage's row holds
+    template <class XOf>
+    __device__ __forceinline__ void init(int64_t ld, int x0, int X, int lane, int wave, XOf x_of) {
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
             const int blk = has(j, wave) ? WPG * j + wave : 0;
             if (XMAJOR) {
                 const int row = 8 * blk + lane / 8;
                 const int c = (lane % 8) ^ xswz(row);
-                voff[j] = (unsigned)(((int64_t)min(x0 + row, X - 1) * ld + 4 * c) * 4);
+                voff[j] = (unsigned)(((int64_t)x_of(row) * ld + 4 * c) * 4);
                 kof[j] = 4 * c;
             } else {
                 // the lane writes LDS chunk q of the stage (row q / CPR, slot
@@ -434,6 +444,39 @@ struct DirectOperand {
     }
 };
 
+// One operand of a whole matrix, as direct_tile takes it: start() and issue()
+// are given the slab they are for, and the slab that the same k-group takes
+// after it.
+template <class OP>
+struct Slabs {
+    OP op;
+    const float *P;
+    int ext;
+    int64_t ld;
+    __device__ __forceinline__ void start(int) {}
+    __device__ __forceinline__ void issue(char *stage, int k0, int, int wave) {
+        op.issue(stage, P, ext, ld, k0, wave);
+    }
+};
+
+// The tile of a workgroup: how its waves and its operands are laid out.
+template <int BM, int BN, bool AX, bool BX, int KS, int WPG, bool KT, int MF>
+struct TileShape {
+    static constexpr int WC = MF == 16 ? 1 : (WPG == 4 ? 2 : (WPG == 2 && BN >= BM ? 2 : 1));   // wave columns
+    static constexpr int WR = WPG / WC;                  // wave rows
+    static constexpr int WM = BM / WR, WN = BN / WC;
+    static constexpr int IB = WM / MF, JB = WN / MF;
+    static_assert(IB * MF == WM && JB * MF == WN && WR * WC == WPG, "tile must split into MF-blocks");
+    // 16 x 16 blocks: a k-major B tile 48 wide is staged 64 wide (the next
+    // 16 columns ride along unused) so that its rows keep the conflict-free
+    // rotation of 64-float rows
+    static constexpr int TB = (MF == 16 && !BX && BN == 48) ? 64 : BN;
+    using OA = DirectOperand<BM, AX, WPG, KT, MF>;
+    using OB = DirectOperand<TB, BX, WPG, KT, MF>;
+    static constexpr int STAGE = OA::STAGE + OB::STAGE;
+    static constexpr int THREADS = 64 * WPG * KS;
+};
+
 // KS groups of WPG waves split the k-slabs of one output tile: group g takes
 // slabs g, g + KS, g + 2 KS, ... through its own double-buffered stages.  At
 // the end groups 1 .. KS-1 hand their accumulators to group 0 through LDS,
@@ -443,23 +486,19 @@ struct DirectOperand {
 // 1 x 1 over the tile; with 16 x 16 blocks (MF = 16) they stack along M,
 // each wave holding a row of BN / 16 blocks (64 x 48 tiles: 16 x 48 per
 // wave, three independent accumulators).
-template <int BM, int BN, bool AX, bool BX, int KS, int WPG, bool KT, int MF, class E>
-__global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
-    int M, int N, int K, const float *__restrict__ A, int64_t lda,
-    const float *__restrict__ B, int64_t ldb, float *__restrict__ C, int64_t ldc, E epi,
-    int tiles_m, int tiles_n) {
+//
+// sa and sb fetch the operands' slabs (Slabs, or their like); the tile is the
+// one at (m0, n0) of the M x N output C.
+template <int BM, int BN, bool AX, bool BX, int KS, int WPG, bool KT, int MF, class SA, class SB,
+          class E>
+__device__ __forceinline__ void direct_tile(int M, int N, int K, SA &sa, SB &sb,
+                                            float *__restrict__ C, int64_t ldc, const E &epi,
+                                            int m0, int n0) {
+    using S = TileShape<BM, BN, AX, BX, KS, WPG, KT, MF>;
     constexpr int BK = 32;
-    constexpr int WC = MF == 16 ? 1 : (WPG == 4 ? 2 : (WPG == 2 && BN >= BM ? 2 : 1));   // wave columns
-    constexpr int WR = WPG / WC;                  // wave rows
-    constexpr int WM = BM / WR, WN = BN / WC;
-    constexpr int IB = WM / MF, JB = WN / MF;
-    static_assert(IB * MF == WM && JB * MF == WN && WR * WC == WPG, "tile must split into MF-blocks");
-    // 16 x 16 blocks: a k-major B tile 48 wide is staged 64 wide (the next
-    // 16 columns ride along unused) so that its rows keep the conflict-free
-    // rotation of 64-float rows
-    constexpr int TB = (MF == 16 && !BX && BN == 48) ? 64 : BN;
-    using OA = DirectOperand<BM, AX, WPG, KT, MF>;
-    using OB = DirectOperand<TB, BX, WPG, KT, MF>;
+    constexpr int WC = S::WC, WM = S::WM, WN = S::WN, IB = S::IB, JB = S::JB, STAGE = S::STAGE;
+    using OA = typename S::OA;
+    using OB = typename S::OB;
     using Acc = typename std::conditional<MF == 32, v16f, v4f>::type;
     constexpr int AR = MF == 32 ? 16 : 4;         // accumulator words per block
     constexpr int NG = MF == 32 ? 4 : 2;          // k-groups of 4 steps per slab
@@ -472,7 +511,6 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
     // 2048^3 took 129.2 us against 127.5 and 1024 x 768 x 3072 46.3 against
     // 44.8.
     constexpr bool LATE = WPG <= 2 || (KS == 4 && MF == 32);
-    constexpr int STAGE = OA::STAGE + OB::STAGE;
     constexpr int ACCW = IB * JB * AR;            // accumulator words per lane
     static_assert(KS == 1 || (KS - 1) * 64 * WPG * ACCW * 4 <= KS * 2 * STAGE,
                   "the hand-over of partial sums must fit in the stages");
@@ -482,16 +520,8 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int grp = wave / WPG, wq = wave % WPG;  // k-group, wave within the group
     const int h = lane >> 5;
-    int tm, tn;
-    tile_of(blockIdx.x, gridDim.x, tiles_m, tiles_n, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
     const int wm = (wq / WC) * WM, wn = (wq % WC) * WN;
 
-    OA oa;
-    OB ob;
-    oa.init(lda, m0, M, lane, wq);
-    ob.init(ldb, n0, N, lane, wq);
-    const int exta = OA::extent(lda, M, K), extb = OB::extent(ldb, N, K);
     char *const gsmem = smem + grp * 2 * STAGE;
     auto stage_a = [&](int b) { return gsmem + b * STAGE; };
     auto stage_b = [&](int b) { return gsmem + b * STAGE + OA::STAGE; };
@@ -540,12 +570,14 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
     const int rounds = (nk + KS - 1) / KS;        // the same for every group
     if (rounds > 0) {
         if (grp < nk) {
-            oa.issue(stage_a(0), A, exta, lda, grp * BK, wq);
-            ob.issue(stage_b(0), B, extb, ldb, grp * BK, wq);
+            sa.start(grp * BK);
+            sb.start(grp * BK);
+            sa.issue(stage_a(0), grp * BK, (grp + KS) * BK, wq);
+            sb.issue(stage_b(0), grp * BK, (grp + KS) * BK, wq);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             if (grp * BK + BK > K) {
-                oa.zero_tail(stage_a(0), grp * BK, K, wq, lane);
-                ob.zero_tail(stage_b(0), grp * BK, K, wq, lane);
+                sa.op.zero_tail(stage_a(0), grp * BK, K, wq, lane);
+                sb.op.zero_tail(stage_b(0), grp * BK, K, wq, lane);
             }
         }
         __syncthreads();
@@ -559,8 +591,8 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
         // slab kn goes to the stage last read in round r-1, whose reads all
         // finished before the previous barrier
         if (!LATE && more && kn < nk) {
-            oa.issue(stage_a(buf ^ 1), A, exta, lda, k1, wq);
-            ob.issue(stage_b(buf ^ 1), B, extb, ldb, k1, wq);
+            sa.issue(stage_a(buf ^ 1), k1, k1 + KS * BK, wq);
+            sb.issue(stage_b(buf ^ 1), k1, k1 + KS * BK, wq);
         }
         if (kt < nk) {
             const char *as = stage_a(buf), *bs = stage_b(buf);
@@ -613,8 +645,8 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 if (LATE && g == 0 && more && kn < nk) {
-                    oa.issue(stage_a(buf ^ 1), A, exta, lda, k1, wq);
-                    ob.issue(stage_b(buf ^ 1), B, extb, ldb, k1, wq);
+                    sa.issue(stage_a(buf ^ 1), k1, k1 + KS * BK, wq);
+                    sb.issue(stage_b(buf ^ 1), k1, k1 + KS * BK, wq);
                     __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
@@ -628,8 +660,8 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
             // wait for them, so wait here before publishing the slab
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             if (kn < nk && k1 + BK > K) {
-                oa.zero_tail(stage_a(buf ^ 1), k1, K, wq, lane);
-                ob.zero_tail(stage_b(buf ^ 1), k1, K, wq, lane);
+                sa.op.zero_tail(stage_a(buf ^ 1), k1, K, wq, lane);
+                sb.op.zero_tail(stage_b(buf ^ 1), k1, K, wq, lane);
             }
             // A k-group of one wave reads only the stages it fills itself:
             // its own wait above publishes the slab to it, and its reads of
@@ -725,6 +757,24 @@ __global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
         for (int j = 0; j < JB; ++j)
             if (col_of(j) < N)
                 epi.block(acc[i][j], pre[i][j], col_of(j), M, C, ldc, row_of(i), mine(i, j));
+}
+
+template <int BM, int BN, bool AX, bool BX, int KS, int WPG, bool KT, int MF, class E>
+__global__ __launch_bounds__(64 * WPG * KS) void gemm_f32_direct(
+    int M, int N, int K, const float *__restrict__ A, int64_t lda,
+    const float *__restrict__ B, int64_t ldb, float *__restrict__ C, int64_t ldc, E epi,
+    int tiles_m, int tiles_n) {
+    using S = TileShape<BM, BN, AX, BX, KS, WPG, KT, MF>;
+    const int lane = threadIdx.x & 63;
+    const int wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WPG;   // wave within the group
+    int tm, tn;
+    tile_of(blockIdx.x, gridDim.x, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    Slabs<typename S::OA> sa{{}, A, S::OA::extent(lda, M, K), lda};
+    Slabs<typename S::OB> sb{{}, B, S::OB::extent(ldb, N, K), ldb};
+    sa.op.init(lda, m0, M, lane, wq);
+    sb.op.init(ldb, n0, N, lane, wq);
+    direct_tile<BM, BN, AX, BX, KS, WPG, KT, MF>(M, N, K, sa, sb, C, ldc, epi, m0, n0);
 }
 
 template <bool AX, bool BX, int BM, int BN, int KS, int WPG, bool KT, int MF, class E>

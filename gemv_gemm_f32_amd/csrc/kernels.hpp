@@ -174,4 +174,109 @@ struct PackedLinear {
 };
 hipError_t launch_packed_linear(int bits, const PackedLinear &a, int num_cus, hipStream_t stream);
 
+// S = alpha X + gate * norm(U) gamma_u and its norm, to fp32 Y or to Q and E
+// (block_norm.hip).  gate: NULL for ones, a vector (ldg = 0) or a row per row;
+// gu, gs, ru and rs may be NULL; S may be X.
+struct BlockNorm {
+    int M, K;
+    const float *U, *X, *gu, *gate, *gs;
+    float *S, *Y, *ru, *rs;
+    uint8_t *Q, *E;
+    int64_t ldu, ldx, ldg, lds, ldy, ldq, lde;
+    float alpha, eps;
+};
+hipError_t launch_block_norm(const BlockNorm &a, hipStream_t stream);
+
+// Its gradients; each output may be NULL.  own: gate (and dgate) has a row per
+// row, else both are vectors.  ws holds block_norm_bwd_workspace_floats floats
+// and is NULL where no sum over rows is wanted.  dX may be dS.
+struct BlockNormBwd {
+    int M, K;
+    const float *dY, *U, *S, *gu, *gate, *gs, *ru, *rs, *dS;
+    float *dU, *dX, *dgu, *dgs, *dgate, *ws;
+    int64_t lddy, ldu, lds, ldg, ldds, lddu, lddx, lddg;
+    float alpha;
+    bool own, accumulate;
+};
+hipError_t launch_block_norm_bwd(const BlockNormBwd &a, hipStream_t stream);
+// Partial sums of both kinds: two rows of K per workgroup.
+constexpr int BLOCK_NORM_BWD_GROUPS = 1024;
+inline int64_t block_norm_bwd_workspace_floats(int64_t M, int64_t K) {
+    return 2 * (M < BLOCK_NORM_BWD_GROUPS ? M : BLOCK_NORM_BWD_GROUPS) * K;
+}
+
+// The T x k entries of ids in the order of their experts (experts.hip).
+constexpr int MAX_EXPERTS = 1024;
+struct ExpertGroups {
+    int T, k, E;
+    const int32_t *ids;
+    int32_t *offsets, *rows, *pos;
+    int64_t ldi, ldp;
+};
+hipError_t launch_expert_groups(const ExpertGroups &a, hipStream_t stream);
+
+// out_t = R_t + sum_j w_tj Y[pos_tj] over entries with 0 <= pos < M.  R and w
+// may be NULL; out may be R.
+struct ExpertCombine {
+    int T, k, M, K;
+    const float *Y, *w, *R;
+    const int32_t *pos;
+    float *out;
+    int64_t ldy, ldw, ldp, ldr, ldo;
+};
+hipError_t launch_expert_combine(const ExpertCombine &a, hipStream_t stream);
+
+// dY[pos_tj] = w_tj dO_t, dw_tj = dO_t . Y[pos_tj] (0 where pos has no row).
+struct ExpertCombineBwd {
+    int T, k, M, K;
+    const float *dO, *Y, *w;
+    const int32_t *pos;
+    float *dY, *dw;
+    int64_t ldo, ldy, ldw, ldp, lddy, lddw;
+};
+hipError_t launch_expert_combine_bwd(const ExpertCombineBwd &a, hipStream_t stream);
+
+// Y_i = act(X[rows_i].op(W_e) + b_e) for the rows i of group e, fp32
+// (groups.hpp): M rows in E groups; W, bias and their like have a matrix or a
+// row per group.  rows (T rows of X to pick from), bias and Z may be NULL.
+struct LinearGrouped {
+    bool trans_w;
+    int act, M, N, K, E, T;
+    const float *X, *W, *bias;
+    const int32_t *rows, *offsets;
+    float *Z, *Y;
+    int64_t ldx, ldw, stridew, ldb, ldz, ldy;
+};
+hipError_t launch_linear_grouped(const LinearGrouped &a, int num_cus, hipStream_t stream);
+
+// Its gradients; each of dX, dW and db may be NULL.  ws holds
+// linear_grouped_bwd_workspace_floats floats.
+struct LinearGroupedBwd {
+    bool trans_w, accumulate;
+    int act, M, N, K, E, T;
+    const float *dY, *Z, *X, *W;
+    const int32_t *rows, *offsets;
+    float *dX, *dW, *db, *ws;
+    int64_t lddy, ldz, ldx, ldw, stridew, lddx, lddw, stridedw, lddb;
+};
+hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hipStream_t stream);
+// Tiles of rows of its element pass at most, and its workspace: dZ, where the
+// activation is not the identity, and a row of column sums per tile.
+int64_t grouped_dz_tiles(int64_t M, int64_t E);
+inline unsigned __int128 linear_grouped_bwd_workspace_floats(bool identity, int64_t M, int64_t N, int64_t E) {
+    return (identity ? 0 : (unsigned __int128)M * dz_stride(N)) + (unsigned __int128)grouped_dz_tiles(M, E) * N;
+}
+
+// The packed layers on rows grouped by expert (groups.hpp): layer.M rows in E
+// groups, layer's Q, S and bias those of the first expert, the others'
+// strideq bytes, strides halves and ldb floats apart.  rows (T rows of X to
+// pick from) may be NULL; layer.R is.
+struct PackedGrouped {
+    PackedLinear layer;
+    const int32_t *rows, *offsets;
+    int E, T;
+    int64_t strideq, strides, ldb;
+};
+hipError_t launch_packed_grouped(int bits, const PackedGrouped &a, int num_cus, hipStream_t stream);
+
 }  // namespace gg

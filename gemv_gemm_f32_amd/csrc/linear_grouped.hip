@@ -1,0 +1,395 @@
+// linear_grouped.hip -- the fp32 dense layer on rows grouped by expert, and its
+// gradients:
+//
+//   Z_i = X[rows_i] . op(W_e) + b_e,  Y = act(Z)     (i in group e)
+//   dZ = dY * act'(Z)
+//   dX_i = dZ_i . op(W_e)^T,  dW_e = X_e^T . dZ_e (or its transpose),
+//   db_e = sum of dZ_e's rows
+//
+// The tiles are those of gemm_f32_tile.hpp (bound by the fp32 matrix unit), in
+// one launch for all experts: tiles never span two groups (groups.hpp), and
+// the operands' addresses are those of the tile's expert.  Offsets within an
+// operand are 32 bits wide and counted from the tile (or, along k, from the
+// slab), so only the rows that `rows` picks have to lie within 2 GiB.
+//
+// X is read through `rows` on its way into LDS, where each lane computes its
+// own address in any case; a copy of X in grouped order is never made.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+
+#include "gemm_f32_tile.hpp"
+#include "groups.hpp"
+#include "kernels.hpp"
+#include "linear_few.hpp"
+
+namespace gg {
+namespace {
+
+// An operand's slabs from an address that moves along k; offsets within a
+// slab are 32 bits.
+template <class OP, bool XMAJOR>
+struct NearSlabs {
+    OP op;
+    const float *P;      // x-major: the tile's first row; k-major: its first column
+    int64_t ld, X, K;    // x-major: rows from P on; k-major: columns
+    __device__ __forceinline__ void start(int) {}
+    __device__ __forceinline__ void issue(char *stage, int k0, int, int wave) {
+        const float *p = P + (XMAJOR ? (int64_t)k0 : k0 * ld);
+        const int64_t words = XMAJOR ? (X - 1) * ld + K - k0 : (min(K - k0, (int64_t)32) - 1) * ld + X;
+        op.issue(stage, p, (int)(words * 4), 0, 0, wave);
+    }
+};
+
+// A k-major operand whose row k is row rows[k] of P.  The next slab's row
+// numbers are fetched with each slab, so that no load waits for them.
+template <class OP>
+struct PickedSlabs {
+    OP op;
+    const float *P;
+    int64_t ld, X;
+    const int32_t *rows;
+    int K, T;
+    unsigned column[OP::NI];   // bytes
+    int next[OP::NI];
+
+    __device__ __forceinline__ void init(int X, int lane, int wave) {
+        op.init(0, 0, X, lane, wave);
+#pragma unroll
+        for (int j = 0; j < OP::NI; ++j) column[j] = op.voff[j];
+    }
+    __device__ __forceinline__ void start(int k0) {
+#pragma unroll
+        for (int j = 0; j < OP::NI; ++j)
+            next[j] = rows[min((unsigned)k0 + op.kof[j], (unsigned)K - 1)];
+    }
+    __device__ __forceinline__ void issue(char *stage, int, int k_next, int wave) {
+#pragma unroll
+        for (int j = 0; j < OP::NI; ++j)
+            op.voff[j] = column[j] + (unsigned)((int64_t)min((unsigned)next[j], (unsigned)T - 1) * ld * 4);
+        op.issue(stage, P, (int)(((int64_t)(T - 1) * ld + X) * 4), 0, 0, wave);
+        start(k_next);
+    }
+};
+
+// C = acc, or C += acc.
+struct Store {
+    bool accumulate;
+
+    template <int N>
+    struct Fetched {};
+    template <int N, class Row, class Mine>
+    __device__ __forceinline__ void fetch(Fetched<N> &, int, int, int, Row, Mine) const {}
+    template <int NS, class Acc, class Row, class Mine>
+    __device__ __forceinline__ void block(const Acc &acc, const Fetched<NS> &, int col, int M,
+                                          float *C, int64_t ldc, Row row, Mine mine) const {
+#pragma unroll
+        for (int r = 0; r < NS; ++r) {
+            if (!mine(r) || row(r) >= M) continue;
+            float *c = C + (int64_t)row(r) * ldc + col;
+            *c = accumulate ? *c + acc[r] : acc[r];
+        }
+    }
+};
+
+// The epilogue of a group's tile at (row, n) of the output, with the group's
+// bias `bias` floats on.
+__device__ __forceinline__ Store at_tile(const Store &s, int64_t, int64_t, int64_t) { return s; }
+__device__ __forceinline__ Layer at_tile(const Layer &l, int64_t bias, int64_t row, int64_t n) {
+    return {l.bias ? l.bias + bias + n : nullptr, nullptr, 0,
+            l.Z ? l.Z + row * l.ldz + n : nullptr, l.ldz, l.act};
+}
+
+// Rows of a grouped product: C_i = A[rows_i] . B_e.
+struct GroupedRows {
+    Groups g;
+    int N, K, T;                   // T: rows of A where rows picks them
+    const float *A, *B;
+    const int32_t *rows;           // NULL: A_i
+    float *C;
+    int64_t lda, ldb, strideb, ldc, ldbias;
+};
+
+template <int BM, int BN, bool BX, int KS, int WPG, class E>
+__global__ __launch_bounds__(64 * WPG * KS) void grouped_rows_kernel(GroupedRows a, E epi, int most) {
+    using S = TileShape<BM, BN, true, BX, KS, WPG, true, 32>;
+    const int tiles_n = (a.N + BN - 1) / BN;
+    const int tiles_m = min(tiles_before<BM>(a.g, a.g.E), most);
+    const int64_t bid = group_number(), n = (int64_t)tiles_m * tiles_n;
+    if (bid >= n) return;
+    const int lane = threadIdx.x & 63;
+    const int wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WPG;
+    int tm, tn;
+    tile_at(xcd_run((int)bid, (int)n), tiles_m, tiles_n, tm, tn);
+    const GroupTile t = tile_of_groups<BM>(a.g, tm);
+    const int n0 = tn * BN, left = min(t.left, BM), cols = a.N - n0;
+
+    NearSlabs<typename S::OA, true> sa{{}, a.A, a.lda, left, a.K};
+    if (a.rows) {
+        const int32_t *rows = a.rows + t.row;
+        sa.X = a.T;
+        sa.op.init(a.lda, 0, left, lane, wq, [&](int row) {
+            return (int)min((unsigned)rows[min(row, left - 1)], (unsigned)a.T - 1);
+        });
+    } else {
+        sa.P += t.row * a.lda;
+        sa.op.init(a.lda, 0, left, lane, wq);
+    }
+    NearSlabs<typename S::OB, BX> sb{{}, a.B + t.e * a.strideb + (BX ? n0 * a.ldb : n0), a.ldb,
+                                     BX ? min(cols, BN) : cols, a.K};
+    sb.op.init(a.ldb, 0, cols, lane, wq);
+    direct_tile<BM, BN, true, BX, KS, WPG, true, 32>(left, cols, a.K, sa, sb, a.C + t.row * a.ldc + n0,
+                                                     a.ldc, at_tile(epi, t.e * a.ldbias, t.row, n0), 0, 0);
+}
+
+// The same on few rows per group: tiles of MB rows, as linear_f32.hip's kernels
+// for few rows.
+template <int MB, bool BX, int KW, int ROWS>
+__global__ __launch_bounds__(64 * KW * ROWS) void grouped_few_kernel(GroupedRows a, Layer epi, int most) {
+    constexpr int COLS = BX ? ROWS : 32;
+    const int tiles_n = (a.N + COLS - 1) / COLS;
+    const int tiles_m = min(tiles_before<MB>(a.g, a.g.E), most);
+    const int64_t bid = group_number();
+    if (bid >= (int64_t)tiles_m * tiles_n) return;
+    const GroupTile t = tile_of_groups<MB>(a.g, (int)(bid / tiles_n));
+    const int64_t n0 = bid % tiles_n * COLS;
+    const int left = min(t.left, MB);
+    const int32_t *rows = a.rows ? a.rows + t.row : nullptr;
+    const float *A = a.rows ? a.A : a.A + t.row * a.lda;
+    const auto x = [&](int m) {
+        return A + (rows ? (int64_t)min((unsigned)rows[m], (unsigned)a.T - 1) : (int64_t)m) * a.lda;
+    };
+    const float *W = a.B + t.e * a.strideb;
+    const Layer e = at_tile(epi, t.e * a.ldbias, t.row, 0);
+    float *Y = a.C + t.row * a.ldc;
+    if constexpr (BX) few_nk<MB, KW, ROWS>(left, a.N, a.K, x, W, a.ldb, Y, a.ldc, e, n0);
+    else few_kn<MB, KW>(left, a.N, a.K, x, W, a.ldb, Y, a.ldc, e, n0);
+}
+
+// dW_e = A_e^T . B_e over the rows of group e, A and B stored row by row; PICK:
+// which of them is read through `rows`.
+enum Pick { NEITHER, PICK_A, PICK_B };
+struct GroupedWeights {
+    Groups g;
+    int M, N, T;                   // output M x N
+    const float *A, *B;
+    const int32_t *rows;
+    float *C;
+    int64_t lda, ldb, ldc, stridec;
+};
+
+template <int BM, int BN, int KS, int WPG, Pick PICK>
+__global__ __launch_bounds__(64 * WPG * KS) void grouped_weights_kernel(GroupedWeights a, Store epi) {
+    using S = TileShape<BM, BN, false, false, KS, WPG, false, 32>;
+    const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN, per = tiles_m * tiles_n;
+    const int64_t bid = group_number(), n = (int64_t)per * a.g.E;
+    if (bid >= n) return;
+    const int place = xcd_run((int)bid, (int)n), e = place / per;
+    int first, count;
+    group_rows(a.g, e, first, count);
+    first = __builtin_amdgcn_readfirstlane(first);
+    count = __builtin_amdgcn_readfirstlane(count);
+    if (count == 0 && epi.accumulate) return;
+    const int lane = threadIdx.x & 63;
+    const int wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WPG;
+    int tm, tn;
+    tile_at(place % per, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    float *C = a.C + e * a.stridec + m0 * a.ldc + n0;
+    const auto near = [&](auto op, const float *P, int64_t ld, int X) {
+        NearSlabs<decltype(op), false> s{op, P + first * ld, ld, X, count};
+        s.op.init(ld, 0, X, lane, wq);
+        return s;
+    };
+    const auto picked = [&](auto op, const float *P, int64_t ld, int X) {
+        PickedSlabs<decltype(op)> s;
+        s.op = op, s.P = P, s.ld = ld, s.X = X, s.rows = a.rows + first, s.K = count, s.T = a.T;
+        s.init(X, lane, wq);
+        return s;
+    };
+    const auto product = [&](auto sa, auto sb) {
+        direct_tile<BM, BN, false, false, KS, WPG, false, 32>(a.M - m0, a.N - n0, count, sa, sb, C, a.ldc, epi, 0, 0);
+    };
+    const typename S::OA oa{};
+    const typename S::OB ob{};
+    if constexpr (PICK == PICK_A) product(picked(oa, a.A + m0, a.lda, a.M - m0), near(ob, a.B + n0, a.ldb, a.N - n0));
+    else if constexpr (PICK == PICK_B) product(near(oa, a.A + m0, a.lda, a.M - m0), picked(ob, a.B + n0, a.ldb, a.N - n0));
+    else product(near(oa, a.A + m0, a.lda, a.M - m0), near(ob, a.B + n0, a.ldb, a.N - n0));
+}
+
+// ---------------------------------------------------------------------------
+// dZ = dY * act'(Z) and the column sums of each tile of DZ_ROWS rows, as the
+// dense layer's element pass (linear_bwd.hip): 64 columns per workgroup, 16
+// lanes of 4 columns by 16 rows at a time.
+constexpr int DZ_ROWS = 128;
+
+__global__ __launch_bounds__(256) void grouped_dz_kernel(Groups g, int act, int N, const float *dY,
+                                                         int64_t lddy, const float *Z, int64_t ldz,
+                                                         float *dZ, int64_t lddz, float *partial, int most) {
+    __shared__ v4f red[256];
+    const int tiles_n = (N + 63) / 64;
+    const int tiles = min(tiles_before<DZ_ROWS>(g, g.E), most);
+    const int64_t bid = group_number();
+    if (bid >= (int64_t)tiles * tiles_n) return;
+    const int tm = (int)(bid / tiles_n);
+    const GroupTile t = tile_of_groups<DZ_ROWS>(g, tm);
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int64_t col = bid % tiles_n * 64 + 4 * tx;
+    const int live = (int)min(max(N - col, (int64_t)0), (int64_t)4);   // columns of this thread that exist
+    const int64_t end = (int64_t)t.row + min(t.left, DZ_ROWS);
+    v4f sum = {0.f, 0.f, 0.f, 0.f};
+    with_act(act, [&](auto a) {
+        constexpr int ACT = decltype(a)::value;
+#pragma unroll 4
+        for (int64_t r = t.row + ty; r < end; r += 16) {
+            const float *pd = dY + r * lddy + col;
+            const float *pz = Z + r * ldz + col;
+            v4f d = {0.f, 0.f, 0.f, 0.f}, z = d;
+            if (live == 4) {
+                d = *reinterpret_cast<const v4f_any *>(pd);
+                if (ACT != GG_ACT_NONE) z = *reinterpret_cast<const v4f_any *>(pz);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    if (c >= live) continue;
+                    d[c] = pd[c];
+                    if (ACT != GG_ACT_NONE) z[c] = pz[c];
+                }
+            }
+            if constexpr (ACT != GG_ACT_NONE) {
+                float *po = dZ + r * lddz + col;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) d[c] *= act_slope<ACT>(z[c]);
+                if (live == 4) {
+                    *reinterpret_cast<v4f_any *>(po) = d;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 3; ++c)
+                        if (c < live) po[c] = d[c];
+                }
+            }
+            sum += d;
+        }
+    });
+    if (partial == nullptr) return;                   // uniform
+    red[threadIdx.x] = sum;
+    __syncthreads();
+    if (ty == 0) {
+#pragma unroll
+        for (int y = 1; y < 16; ++y) sum += red[y * 16 + tx];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (c < live) partial[(int64_t)tm * N + col + c] = sum[c];
+    }
+}
+
+// db_e: the sums of its group's tiles, 8 interleaved runs of tiles per column,
+// then the runs in order.
+__global__ __launch_bounds__(512) void grouped_bias_kernel(Groups g, int N, const float *partial, bool accumulate,
+                                                           float *db, int64_t lddb, int most) {
+    __shared__ float red[8][64];
+    const int64_t blocks = ((int64_t)N + 63) / 64, bid = group_number();
+    if (bid >= blocks * g.E) return;
+    const int e = (int)(bid / blocks);
+    const int from = min(tiles_before<DZ_ROWS>(g, e), most);
+    int first, count;
+    group_rows(g, e, first, count);
+    const int end = min(from + tiles_in<DZ_ROWS>(count), most);
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    const int64_t col = bid % blocks * 64 + tx;
+    float sum = 0.f;
+    if (col < N)
+#pragma unroll 4
+        for (int i = from + ty; i < end; i += 8) sum += partial[(int64_t)i * N + col];
+    red[ty][tx] = sum;
+    __syncthreads();
+    if (ty > 0 || col >= N) return;
+#pragma unroll
+    for (int y = 1; y < 8; ++y) sum += red[y][tx];
+    float *to = db + e * lddb + col;
+    *to = accumulate ? *to + sum : sum;
+}
+
+// ---------------------------------------------------------------------------
+
+template <int BM, int BN, bool BX, int KS, int WPG, class E>
+hipError_t rows_tiles(const GroupedRows &a, const E &epi, hipStream_t s) {
+    const int64_t most = tiles_most(a.g.M, a.g.E, BM), n = most * (((int64_t)a.N + BN - 1) / BN);
+    if (n > INT_MAX) return hipErrorInvalidConfiguration;
+    return launch(grouped_rows_kernel<BM, BN, BX, KS, WPG, E>, grid_of(n), dim3(64 * WPG * KS), s, a, epi, (int)most);
+}
+
+template <int MB, bool BX, int KW, int ROWS>
+hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
+    constexpr int COLS = BX ? ROWS : 32;
+    const int64_t most = tiles_most(a.g.M, a.g.E, MB), n = most * (((int64_t)a.N + COLS - 1) / COLS);
+    if (n > INT_MAX) return hipErrorInvalidConfiguration;
+    return launch(grouped_few_kernel<MB, BX, KW, ROWS>, grid_of(n), dim3(64 * KW * ROWS), s, a, epi, (int)most);
+}
+
+template <bool BX, class E>
+hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStream_t s) {
+    const int64_t per_group = a.g.M / a.g.E;
+    if (per_group < 32) return rows_tiles<32, 64, BX, 4, 2>(a, epi, s);
+    return rows_tiles<64, 64, BX, 2, 4>(a, epi, s);
+}
+
+template <Pick PICK>
+hipError_t weights_product(const GroupedWeights &a, const Store &epi, hipStream_t s) {
+    constexpr int BM = 64, BN = 64, KS = 2, WPG = 4;
+    const int64_t n = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
+    if (n > INT_MAX / a.g.E) return hipErrorInvalidConfiguration;
+    return launch(grouped_weights_kernel<BM, BN, KS, WPG, PICK>, grid_of(n * a.g.E), dim3(64 * WPG * KS), s, a, epi);
+}
+
+}  // namespace
+
+int64_t grouped_dz_tiles(int64_t M, int64_t E) { return tiles_most(M, E, DZ_ROWS); }
+
+hipError_t launch_linear_grouped(const LinearGrouped &a, int num_cus, hipStream_t s) {
+    const GroupedRows r{{a.offsets, a.E, a.M}, a.N, a.K, a.T, a.X, a.W, a.rows, a.Y,
+                        a.ldx, a.ldw, a.stridew, a.ldy, a.ldb};
+    const Layer e{a.bias, nullptr, 0, a.Z, a.ldz, a.act};
+    return a.trans_w ? rows_product<true>(r, e, num_cus, s) : rows_product<false>(r, e, num_cus, s);
+}
+
+hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hipStream_t s) {
+    const Groups g{a.offsets, a.E, a.M};
+    hipError_t e = hipSuccess;
+    const float *dZ = a.dY;
+    int64_t lddz = a.lddy;
+    if (a.N > 0 && (a.act != GG_ACT_NONE || a.db != nullptr)) {
+        const int64_t most = grouped_dz_tiles(a.M, a.E), cols = ((int64_t)a.N + 63) / 64;
+        float *out = a.ws, *partial = a.ws;
+        if (a.act != GG_ACT_NONE) {
+            lddz = dz_stride(a.N);
+            partial = a.ws + (int64_t)a.M * lddz;
+            dZ = out;
+        }
+        if (most * cols > INT_MAX || cols * a.E > INT_MAX) return hipErrorInvalidConfiguration;
+        if (most > 0)
+            e = launch(grouped_dz_kernel, grid_of(most * cols), dim3(256), s, g, a.act, a.N, a.dY, a.lddy, a.Z, a.ldz,
+                       out, lddz, a.db ? partial : nullptr, (int)most);
+        if (e != hipSuccess) return e;
+        if (a.db)
+            e = launch(grouped_bias_kernel, grid_of(cols * a.E), dim3(512), s, g, a.N, partial, a.accumulate, a.db,
+                       a.lddb, (int)most);
+        if (e != hipSuccess) return e;
+    }
+    if (a.dX) {
+        const GroupedRows r{g, a.K, a.N, 0, dZ, a.W, nullptr, a.dX, lddz, a.ldw, a.stridew, a.lddx, 0};
+        e = a.trans_w ? rows_product<false>(r, Store{false}, num_cus, s)
+                      : rows_product<true>(r, Store{false}, num_cus, s);
+        if (e != hipSuccess) return e;
+    }
+    if (a.dW) {
+        GroupedWeights w{g, a.K, a.N, a.T, a.X, dZ, a.rows, a.dW, a.ldx, lddz, a.lddw, a.stridedw};
+        if (a.trans_w) w = {g, a.N, a.K, a.T, dZ, a.X, a.rows, a.dW, lddz, a.ldx, a.lddw, a.stridedw};
+        const Store st{a.accumulate};
+        e = !a.rows ? weights_product<NEITHER>(w, st, s)
+            : a.trans_w ? weights_product<PICK_B>(w, st, s) : weights_product<PICK_A>(w, st, s);
+    }
+    return e;
+}
+
+}  // namespace gg

@@ -47,4 +47,19 @@ __device__ __forceinline__ float wave64_sum(float v) {
     return lo + hi;
 }
 
+// Inclusive sums over the lanes of a wave, in lane order: within each 16-lane
+// row by shifts, then across rows by broadcasts of their last lanes.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int dpp_add(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave64_scan(int v) {
+    v = dpp_add<0x111>(v);             // row_shr:1, 2, 4, 8
+    v = dpp_add<0x112>(v);
+    v = dpp_add<0x114>(v);
+    v = dpp_add<0x118>(v);
+    v = dpp_add<0x142, 0xA>(v);        // row_bcast:15 into rows 1 and 3
+    return dpp_add<0x143, 0xC>(v);     // row_bcast:31 into rows 2 and 3
+}
+
 }  // namespace gg

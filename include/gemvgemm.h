@@ -460,6 +460,183 @@ int linear_q2_mx8(int act, int64_t M, int64_t N, int64_t K,
                   const float *bias, const float *R, int64_t ldr, float *Y, int64_t ldy,
                   uint8_t *Y8, int64_t ldy8, uint8_t *YE, int64_t ldye, gg_stream_t stream);
 
+/*
+ * ---- Layers with experts ------------------------------------------------
+ *
+ * A token is sent to k of E experts.  expert_groups puts the T x k (token,
+ * expert) pairs in the order of their experts; the grouped layers then take M
+ * rows in E groups, group e being rows offsets[e] .. offsets[e + 1] - 1, and
+ * expert_combine brings the results back to their tokens.
+ *   offsets: E + 1 ints in DEVICE memory, not decreasing, from 0 up to at most M.
+ *   rows: DEVICE ints or NULL.  With rows, row i of the grouped order is row
+ *   rows[i] of X, which has T rows (no copy of X in grouped order is needed);
+ *   with NULL it is row i of X, which has M rows, and T does not matter.
+ * Sizes of groups are known to the device alone: nothing waits for them, a
+ * call may be captured into a graph, and its replays follow what offsets and
+ * rows hold at the time.  A group may be empty.  Rows of outputs before
+ * offsets[0] and from offsets[E] on are left as they were, and such rows of
+ * inputs are not used.  Offsets out of order or out of range and row numbers
+ * out of range give wrong results in the rows they concern, but nothing
+ * outside the operands is ever read or written.  E is at most 1,024.
+ */
+
+/*
+ * The order of (token, expert) pairs by expert, from ids[t*ldi + j] (T x k):
+ *   offsets[e]       number of pairs whose expert is below e (E + 1 ints)
+ *   pos[t*ldp + j]   place of pair (t, j) in the order: by expert, and within an
+ *                    expert by t, then j; -1 for a pair without an expert
+ *   rows[i]          the token t of the pair at place i (T*k ints)
+ * Pairs whose id is not in 0 .. E-1 (padding) have no expert: they come last,
+ * behind offsets[E].  T*k must be below 2^31.  The three outputs must be
+ * disjoint from each other and from ids.
+ */
+int expert_groups(int64_t T, int64_t k, int64_t E, const int32_t *ids, int64_t ldi,
+                  int32_t *offsets, int32_t *rows, int32_t *pos, int64_t ldp, gg_stream_t stream);
+
+/*
+ * out_t = R_t + sum_j w_tj Y[pos_tj], fp32, added in the order of j.
+ *   Y: M x K (the grouped order);  pos, weights: T x k;  R, out: T x K.
+ *   weights NULL: ones (the sum of the gradients that reach a token through its
+ *   experts).  R NULL: nothing added.  out may be R itself (same pointer and
+ *   leading dimension).  Entries of pos that are not in 0 .. M-1 add nothing.
+ */
+int expert_combine(int64_t T, int64_t k, int64_t M, int64_t K, const float *Y, int64_t ldy,
+                   const int32_t *pos, int64_t ldp, const float *weights, int64_t ldw,
+                   const float *R, int64_t ldr, float *out, int64_t ldo, gg_stream_t stream);
+
+/*
+ * Gradients of expert_combine from dO (T x K):
+ *   dY[pos_tj] = w_tj dO_t (M x K),  dw_tj = dO_t . Y[pos_tj] (T x k)
+ * R's gradient is dO itself.  dY and dw may each be NULL (not wanted); Y is read
+ * for dw only.  Entries of pos must differ, as expert_groups makes them; those
+ * not in 0 .. M-1 write no row and get dw = 0, and rows of dY that no entry
+ * names are left as they were.
+ */
+int expert_combine_bwd(int64_t T, int64_t k, int64_t M, int64_t K, const float *dO, int64_t lddo,
+                       const float *Y, int64_t ldy, const int32_t *pos, int64_t ldp,
+                       const float *weights, int64_t ldw, float *dY, int64_t lddy, float *dw,
+                       int64_t lddw, gg_stream_t stream);
+
+/*
+ * Dense layer on rows grouped by expert, fp32:
+ *   Y_i = act(Z_i),  Z_i = X[rows_i] . op(W_e) + b_e   for i in group e
+ *   W: E matrices as linear_f32 takes them (trans_w, ldw), stridew floats
+ *   apart;  bias: E x N with ldb, or NULL;  Z and Y: M x N, Z may be NULL.
+ * Limits: leading dimensions of X and W up to 2^22; with rows, the T rows of X
+ * within 2 GiB (else GG_ERR_INVALID_ARG); and fewer than 2^31 tiles of 32 x 32
+ * ((M / 32 + E) * ceil(N / 32)).  Accuracy and non-finite inputs as linear_f32;
+ * results do not depend on the sizes of other groups.
+ */
+int linear_f32_grouped(int trans_w, int act, int64_t M, int64_t N, int64_t K, int64_t E, int64_t T,
+                       const float *X, int64_t ldx, const int32_t *rows, const int32_t *offsets,
+                       const float *W, int64_t ldw, int64_t stridew, const float *bias, int64_t ldb,
+                       float *Z, int64_t ldz, float *Y, int64_t ldy, gg_stream_t stream);
+
+/*
+ * Gradients of linear_f32_grouped from dY[M x N], with dZ = dY * act'(Z):
+ *   dX_i = dZ_i . op(W_e)^T   (M x K, in grouped order: the gradient of a token
+ *                              is expert_combine of dX without weights)
+ *   dW_e = X_e^T . dZ_e or its transpose, as W (lddw, stridedw);  db: E x N
+ * where X_e are the rows rows_i of group e.  Gradients of an empty group are
+ * zeros.  accumulate, absent outputs and the workspace as linear_f32_bwd, with
+ * linear_f32_grouped_bwd_ws_size bytes; limits as above, for dY, N and for the
+ * tiles of dX and of dW too.
+ */
+int linear_f32_grouped_bwd(int trans_w, int act, int accumulate, int64_t M, int64_t N, int64_t K,
+                           int64_t E, int64_t T, const float *dY, int64_t lddy, const float *Z,
+                           int64_t ldz, const float *X, int64_t ldx, const int32_t *rows,
+                           const int32_t *offsets, const float *W, int64_t ldw, int64_t stridew,
+                           float *dX, int64_t lddx, float *dW, int64_t lddw, int64_t stridedw,
+                           float *db, int64_t lddb, void *workspace, int64_t workspace_bytes,
+                           gg_stream_t stream);
+
+/*
+ * Bytes of workspace linear_f32_grouped_bwd needs, or GG_ERR_INVALID_ARG for an
+ * unknown activation, a negative or oversized size, or a result past 2^62.
+ */
+int64_t linear_f32_grouped_bwd_ws_size(int act, int64_t M, int64_t N, int64_t E);
+
+/*
+ * Packed layers (linear_q4_mx8, linear_q2_mx8) on rows grouped by expert:
+ *   Y_i = act(X[rows_i] . W_e^T + b_e)   for i in group e
+ * X8, XE: T rows (M without rows);  Q, S: E matrices as there, strideq bytes
+ * and strides halves apart;  bias: E x N with ldb, or NULL;  Y, or Y8 and YE, or
+ * all three: M rows.  One token through k experts is M = k rows.  The number of
+ * tiles is limited as in linear_f32_grouped; accuracy as linear_q4_mx8.
+ */
+int linear_q4_mx8_grouped(int act, int64_t M, int64_t N, int64_t K, int64_t E, int64_t T,
+                          const uint8_t *X8, int64_t ldx, const uint8_t *XE, int64_t ldxe,
+                          const int32_t *rows, const int32_t *offsets,
+                          const uint8_t *Q, int64_t ldq, int64_t strideq,
+                          const uint16_t *S, int64_t lds, int64_t strides,
+                          const float *bias, int64_t ldb, float *Y, int64_t ldy,
+                          uint8_t *Y8, int64_t ldy8, uint8_t *YE, int64_t ldye, gg_stream_t stream);
+
+int linear_q2_mx8_grouped(int act, int64_t M, int64_t N, int64_t K, int64_t E, int64_t T,
+                          const uint8_t *X8, int64_t ldx, const uint8_t *XE, int64_t ldxe,
+                          const int32_t *rows, const int32_t *offsets,
+                          const uint8_t *Q, int64_t ldq, int64_t strideq,
+                          const uint16_t *S, int64_t lds, int64_t strides,
+                          const float *bias, int64_t ldb, float *Y, int64_t ldy,
+                          uint8_t *Y8, int64_t ldy8, uint8_t *YE, int64_t ldye, gg_stream_t stream);
+
+/*
+ * The norm behind a block and the norm before the next one, with the block's
+ * gate and the residual's scale between them, in one pass over the rows:
+ *   V = U rstd_u gamma_u,        rstd_u,i = 1 / sqrt((1/K) sum_k U_ik^2 + eps)
+ *   S = alpha X + gate V
+ *   Y = S rstd_s gamma_s,        rstd_s,i = 1 / sqrt((1/K) sum_k S_ik^2 + eps)
+ *   U (the block's output), X (the residual stream), S, Y: M x K;  gamma_u,
+ *   gamma_s: K floats or NULL (ones);  rstd_u, rstd_s: M floats or NULL (not
+ *   kept; block_norm_f32_bwd takes both).
+ *   gate: NULL (ones), K floats for all rows (ldgate = 0), or M x K with a
+ *   leading dimension.  alpha: finite.  eps: finite and not negative.
+ * S may be X itself (same pointer and leading dimension), which updates the
+ * residual stream in place; any other overlap of an output with an input or
+ * another output gives GG_ERR_ALIAS.  K = 0 writes nothing.  Squares beyond
+ * fp32's range, rows of zeros and non-finite rows as rmsnorm_f32, for either
+ * norm.
+ */
+int block_norm_f32(int64_t M, int64_t K, const float *U, int64_t ldu, const float *X, int64_t ldx,
+                   const float *gamma_u, const float *gate, int64_t ldgate, float alpha,
+                   const float *gamma_s, float eps, float *S, int64_t lds, float *Y, int64_t ldy,
+                   float *rstd_u, float *rstd_s, gg_stream_t stream);
+
+/* The same with Y in 8 bits, Q and E as rmsnorm_mx8 writes them. */
+int block_norm_mx8(int64_t M, int64_t K, const float *U, int64_t ldu, const float *X, int64_t ldx,
+                   const float *gamma_u, const float *gate, int64_t ldgate, float alpha,
+                   const float *gamma_s, float eps, float *S, int64_t lds, uint8_t *Q, int64_t ldq,
+                   uint8_t *E, int64_t lde, gg_stream_t stream);
+
+/*
+ * Gradients of block_norm_f32 from dY[M x K], with xs = S rstd_s, xu = U rstd_u:
+ *   G  = rstd_s (gamma_s dY - xs (1/K) sum_k gamma_s,k dY_ik xs_ik) + dS
+ *   dX = alpha G,  dgamma_s = sum over rows of dY xs
+ *   H  = gate G,   dgamma_u = sum over rows of H xu
+ *   dU = rstd_u (gamma_u H - xu (1/K) sum_k gamma_u,k H_ik xu_ik)
+ *   dgate = gamma_u xu G: its sum over rows (K floats) where one gate serves
+ *           all rows (ldgate = 0), else M x K with lddgate
+ *   dS (M x K) is the gradient that reaches S past the norm, NULL for none; dX
+ *   may be dS itself (same pointer and leading dimension).  S, rstd_u and rstd_s
+ *   are those that the forward pass kept.  Every output may be NULL (not
+ *   wanted); dgate needs a gate.  accumulate == 1: the sums over rows (K floats)
+ *   are added to what they hold; everything else is overwritten.
+ *   workspace: at least block_norm_f32_bwd_ws_size(M, K) bytes, 16-byte
+ *   aligned, as for linear_f32_bwd; needed only where a sum over rows is
+ *   wanted.
+ */
+int block_norm_f32_bwd(int accumulate, int64_t M, int64_t K, const float *dY, int64_t lddy,
+                       const float *U, int64_t ldu, const float *S, int64_t lds, const float *gamma_u,
+                       const float *gate, int64_t ldgate, float alpha, const float *gamma_s,
+                       const float *rstd_u, const float *rstd_s, const float *dS, int64_t ldds,
+                       float *dU, int64_t lddu, float *dX, int64_t lddx, float *dgamma_u,
+                       float *dgamma_s, float *dgate, int64_t lddgate, void *workspace,
+                       int64_t workspace_bytes, gg_stream_t stream);
+
+/* Bytes of workspace block_norm_f32_bwd needs for its sums over rows, or
+ * GG_ERR_INVALID_ARG for a negative or oversized size. */
+int64_t block_norm_f32_bwd_ws_size(int64_t M, int64_t K);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *gg_strerror(int status);
 
