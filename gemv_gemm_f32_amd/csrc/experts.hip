@@ -13,113 +13,199 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef v4f v4f_any __attribute__((aligned(4)));   // rows may start at any float
 
 // ---------------------------------------------------------------------------
-// Grouping is a counting sort that keeps the order of equal keys.  One
-// workgroup does it all: entries are few (a training batch has some 10^5), so
-// what counts is the launch, the barriers and each wave's walk, and no second
-// launch or exchange between workgroups.  Each of W waves takes a run of entries,
-// counts its experts in an LDS row of its own (integers: their order does not
-// matter), the rows are scanned over waves and experts, and the wave walks its
-// run again, 64 entries at a time in order: entries of one expert find each
-// other by a ballot per bit of the key, and their rank is the number of
-// earlier lanes among them.  Entries without an expert have the key E and come
-// last.
-template <int W>
-__global__ __launch_bounds__(64 * W) void expert_groups_kernel(ExpertGroups a, int bits) {
-    constexpr int THREADS = 64 * W;
-    __shared__ int count[W * (MAX_EXPERTS + 1)];      // W rows of E + 1
-    __shared__ int wave_total[W];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int bins = a.E + 1;
-    for (int i = tid; i < W * bins; i += THREADS) count[i] = 0;
-    __syncthreads();
-
+// Grouping is a counting sort that keeps the order of equal keys.  A wave takes
+// a run of entries, counts its experts in an LDS row of its own (integers:
+// their order does not matter), the rows are scanned over waves and experts, and
+// the wave walks its run again, 64 entries at a time in order: entries of one
+// expert find each other by a ballot per bit of the key, and their rank is the
+// number of earlier lanes among them.  Entries without an expert have the key E
+// and come last.
+//
+// Few entries are one workgroup's work, in one launch.  More are bound by the
+// scattered stores of rows, a cache line per lane, and are spread over
+// workgroups: one launch counts each workgroup's experts into rows (all of which
+// the last launch writes), a second finds the places, and a third writes rows.
+// (8,192 tokens, 8 of 128 experts: 64.8 us in one workgroup of 16 waves, 14.1 in
+// 64; 1,024 tokens, 8 of 64: one workgroup.)
+struct Entries {
+    const ExpertGroups &a;
+    unsigned k;
     // fewer than 2^31 entries, so that sums of places fit 32 bits
-    const unsigned k = a.k, n = (unsigned)a.T * k;
-    const unsigned per = ((n + W - 1) / W + 63) / 64 * 64;
-    const unsigned first = min(per * wave, n), end = min(first + per, n);
-    int *mine = count + wave * bins;
-    const auto key_of = [&](unsigned i) {
+    __device__ __forceinline__ explicit Entries(const ExpertGroups &g) : a(g), k(g.k) {}
+    __device__ __forceinline__ unsigned number() const { return (unsigned)a.T * k; }
+    __device__ __forceinline__ int key(unsigned i) const {
         const int e = a.ids[a.ldi == a.k ? (int64_t)i : i / k * a.ldi + i % k];
         return e >= 0 && e < a.E ? e : a.E;
-    };
-    constexpr int U = 8;                              // loads in flight
-    for (unsigned base = first; base < end; base += 64 * U) {
-        int key[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) key[u] = key_of(min(base + 64 * u + lane, end - 1));
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (base + 64 * u + lane < end) atomicAdd(mine + key[u], 1);
     }
-    __syncthreads();
-
-    // counts to places: over the waves of one expert, then over experts, a
-    // round of THREADS bins at a time
-    int before = 0;
-    for (int b0 = 0; b0 < bins; b0 += THREADS) {
-        const int b = b0 + tid;
-        int total = 0;
-        if (b < bins)
+    __device__ __forceinline__ int32_t &pos(unsigned i) const {
+        return a.pos[a.ldp == a.k ? (int64_t)i : i / k * a.ldp + i % k];
+    }
+    static constexpr int U = 8;                       // loads in flight
+    // adds a run's counts to bin[0 .. E] in LDS
+    __device__ __forceinline__ void count(int *bin, unsigned first, unsigned end) const {
+        const unsigned lane = threadIdx.x & 63;
+        for (unsigned base = first; base < end; base += 64 * U) {
+            int e[U];
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const int c = count[w * bins + b];
-                count[w * bins + b] = total;
-                total += c;
-            }
-        int incl = total;                             // inclusive over the wave
+            for (int u = 0; u < U; ++u) e[u] = key(min(base + 64 * u + lane, end - 1));
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(incl, d);
-            if (lane >= d) incl += o;
+            for (int u = 0; u < U; ++u)
+                if (base + 64 * u + lane < end) atomicAdd(bin + e[u], 1);
         }
+    }
+    // store(i, key, place) for a run whose experts' next places are in `next`, an
+    // LDS row of the wave's own
+    template <class Store>
+    __device__ __forceinline__ void place(int *next, unsigned first, unsigned end, int bits, Store store) const {
+        const unsigned lane = threadIdx.x & 63;
+        for (unsigned base = first; base < end; base += 64 * U) {
+            int e[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) e[u] = key(min(base + 64 * u + lane, end - 1));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (base + 64 * u >= end) break;      // uniform
+                const unsigned i = base + 64 * u + lane;
+                const bool there = i < end;
+                uint64_t same = __ballot(there);
+                for (int bit = 0; bit < bits; ++bit) {
+                    const uint64_t set = __ballot(e[u] >> bit & 1);
+                    same &= e[u] >> bit & 1 ? set : ~set;
+                }
+                if (there) store(i, e[u], next[e[u]] + __popcll(same & ((1ull << lane) - 1)));
+                // the last of the equal lanes moves the expert's place on, after
+                // all have read it: LDS takes a wave's accesses in order
+                in_order();
+                if (there && (same >> lane) == 1) next[e[u]] += __popcll(same);
+                in_order();
+            }
+        }
+    }
+    static __device__ __forceinline__ void in_order() {
+#if defined(__HIP_DEVICE_COMPILE__)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#endif
+    }
+};
+
+// Sums of value(b) over the bins before b, for all bins: out(b, sum), by the
+// W waves of a workgroup, a round of their threads at a time.
+template <int W, class Value, class Out>
+__device__ __forceinline__ void scan_bins(int bins, Value value, Out out) {
+    __shared__ int wave_total[W];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int before = 0;
+    for (int b0 = 0; b0 < bins; b0 += 64 * W) {
+        const int b = b0 + (int)threadIdx.x, v = b < bins ? value(b) : 0, incl = wave64_scan(v);
         if (lane == 63) wave_total[wave] = incl;
         __syncthreads();
-        int start = before + incl - total;
+        int start = before + incl - v;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             if (w < wave) start += wave_total[w];
             before += wave_total[w];
         }
-        if (b < bins) {
-#pragma unroll
-            for (int w = 0; w < W; ++w) count[w * bins + b] += start;
-            a.offsets[b] = start;                     // bin E starts where the last group ends
-        }
+        if (b < bins) out(b, start);
         __syncthreads();
     }
+}
 
-    for (unsigned base = first; base < end; base += 64 * U) {
-        int key[U];
+template <int W>
+__global__ __launch_bounds__(64 * W) void expert_groups_kernel(ExpertGroups a, int bits) {
+    __shared__ int count[W * (MAX_EXPERTS + 1)];      // W rows of E + 1
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int bins = a.E + 1;
+    for (int i = threadIdx.x; i < W * bins; i += 64 * W) count[i] = 0;
+    __syncthreads();
+    const Entries all(a);
+    const unsigned n = all.number(), per = ((n + W - 1) / W + 63) / 64 * 64;
+    const unsigned first = min(per * wave, n), end = min(first + per, n);
+    int *mine = count + wave * bins;
+    all.count(mine, first, end);
+    __syncthreads();
+    // counts to places: over the waves of one expert, then over experts
+    const auto over_waves = [&](int b) {
+        int total = 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) key[u] = key_of(min(base + 64 * u + lane, end - 1));
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const unsigned i = base + 64 * u + lane;
-            const bool there = i < end;
-            uint64_t same = __ballot(there);
-            for (int bit = 0; bit < bits; ++bit) {
-                const uint64_t set = __ballot(key[u] >> bit & 1);
-                same &= key[u] >> bit & 1 ? set : ~set;
-            }
-            if (there) {
-                const int rank = __popcll(same & ((1ull << lane) - 1));
-                const int at = mine[key[u]] + rank;
-                a.rows[at] = (int)(i / k);
-                a.pos[i / k * a.ldp + i % k] = key[u] < a.E ? at : -1;
-            }
-            // the last of the equal lanes moves the expert's place on, after
-            // all have read it: LDS takes a wave's accesses in order
-#if defined(__HIP_DEVICE_COMPILE__)
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-#endif
-            if (there && (same >> lane) == 1) mine[key[u]] += __popcll(same);
-#if defined(__HIP_DEVICE_COMPILE__)
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-#endif
+        for (int w = 0; w < W; ++w) {
+            const int c = count[w * bins + b];
+            count[w * bins + b] = total;
+            total += c;
         }
+        return total;
+    };
+    scan_bins<W>(bins, over_waves, [&](int b, int start) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) count[w * bins + b] += start;
+        a.offsets[b] = start;                         // bin E starts where the last group ends
+    });
+    all.place(mine, first, end, bits, [&](unsigned i, int e, int at) {
+        a.rows[at] = (int)(i / all.k);
+        all.pos(i) = e < a.E ? at : -1;
+    });
+}
+
+// The same over workgroups of PW waves, each with `per` entries, a multiple of
+// 64 PW.
+constexpr int PW = 4;
+
+__global__ __launch_bounds__(64 * PW) void expert_count_kernel(ExpertGroups a, unsigned per) {
+    __shared__ int count[MAX_EXPERTS + 1];
+    for (int b = threadIdx.x; b <= a.E; b += 64 * PW) count[b] = 0;
+    __syncthreads();
+    const Entries all(a);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned first = min(per * blockIdx.x + per / PW * wave, all.number());
+    all.count(count, first, min(first + per / PW, all.number()));
+    __syncthreads();
+    for (int b = threadIdx.x; b <= a.E; b += 64 * PW) a.rows[(int64_t)blockIdx.x * (a.E + 1) + b] = count[b];
+}
+
+__global__ __launch_bounds__(64 * PW) void expert_place_kernel(ExpertGroups a, unsigned per, int bits) {
+    __shared__ int count[PW * (MAX_EXPERTS + 1)], earlier[MAX_EXPERTS + 1];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int bins = a.E + 1;
+    for (int i = threadIdx.x; i < PW * bins; i += 64 * PW) count[i] = 0;
+    __syncthreads();
+    const Entries all(a);
+    const unsigned first = min(per * blockIdx.x + per / PW * wave, all.number());
+    const unsigned end = min(first + per / PW, all.number());
+    int *mine = count + wave * bins;
+    all.count(mine, first, end);
+    // all entries of an expert, and those of earlier workgroups
+    const auto over_groups = [&](int b) {
+        int total = 0, before = 0;
+#pragma unroll 8
+        for (int g = 0; g < (int)gridDim.x; ++g) {
+            const int c = a.rows[(int64_t)g * bins + b];
+            total += c;
+            before += g < (int)blockIdx.x ? c : 0;
+        }
+        earlier[b] = before;
+        return total;
+    };
+    scan_bins<PW>(bins, over_groups, [&](int b, int start) {
+        if (blockIdx.x == 0) a.offsets[b] = start;
+        int at = start + earlier[b];                  // this thread's own value
+#pragma unroll
+        for (int w = 0; w < PW; ++w) {
+            const int c = count[w * bins + b];
+            count[w * bins + b] = at;
+            at += c;
+        }
+    });
+    // no place is -1, so that its complement marks an entry without an expert
+    all.place(mine, first, end, bits, [&](unsigned i, int e, int at) { all.pos(i) = e < a.E ? at : ~at; });
+}
+
+__global__ __launch_bounds__(256) void expert_rows_kernel(ExpertGroups a) {
+    const Entries all(a);
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all.number(); i += (uint64_t)gridDim.x * 256) {
+        const int at = all.pos((unsigned)i);
+        a.rows[at < 0 ? ~at : at] = (int)((unsigned)i / all.k);
+        if (at < 0) all.pos((unsigned)i) = -1;
     }
 }
 
@@ -259,10 +345,21 @@ inline unsigned groups(int64_t n) { return (unsigned)(n < MAX_GROUPS ? n : MAX_G
 hipError_t launch_expert_groups(const ExpertGroups &a, hipStream_t s) {
     int bits = 0;
     while (a.E >> bits) ++bits;                       // keys up to E
+    const int64_t n = (int64_t)a.T * a.k;
     // one wave needs no barriers: the better choice for the few entries of
     // generated tokens
-    if ((int64_t)a.T * a.k <= 512) return launch(expert_groups_kernel<1>, dim3(1), dim3(64), s, a, bits);
-    return launch(expert_groups_kernel<16>, dim3(1), dim3(1024), s, a, bits);
+    if (n <= 512) return launch(expert_groups_kernel<1>, dim3(1), dim3(64), s, a, bits);
+    // workgroups of at least 1,024 entries, as many as their counts fit into rows
+    const int64_t room = n / (a.E + 1), most = n / 1024;
+    const int64_t groups = room < most ? (room < 256 ? room : 256) : (most < 256 ? most : 256);
+    if (groups < 8) return launch(expert_groups_kernel<16>, dim3(1), dim3(1024), s, a, bits);
+    const unsigned per = (unsigned)(((n + groups - 1) / groups + 64 * PW - 1) / (64 * PW) * (64 * PW));
+    const unsigned grid = (unsigned)((n + per - 1) / per);
+    hipError_t e = launch(expert_count_kernel, dim3(grid), dim3(64 * PW), s, a, per);
+    if (e == hipSuccess) e = launch(expert_place_kernel, dim3(grid), dim3(64 * PW), s, a, per, bits);
+    if (e == hipSuccess)
+        e = launch(expert_rows_kernel, dim3((unsigned)(n < (1 << 20) ? (n + 255) / 256 : 4096)), dim3(256), s, a);
+    return e;
 }
 
 hipError_t launch_expert_combine(const ExpertCombine &a, hipStream_t s) {

@@ -184,7 +184,9 @@ __global__ __launch_bounds__(64 * WPG * KS) void grouped_weights_kernel(GroupedW
     const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN, per = tiles_m * tiles_n;
     const int64_t bid = group_number(), n = (int64_t)per * a.g.E;
     if (bid >= n) return;
-    const int place = xcd_run((int)bid, (int)n), e = place / per;
+    // every XCD takes a part of each expert: groups differ in size, so that an
+    // expert per XCD would leave most of them waiting for the largest
+    const int e = (int)(bid / per), place = xcd_run((int)(bid % per), per);
     int first, count;
     group_rows(a.g, e, first, count);
     first = __builtin_amdgcn_readfirstlane(first);
@@ -193,7 +195,7 @@ __global__ __launch_bounds__(64 * WPG * KS) void grouped_weights_kernel(GroupedW
     const int lane = threadIdx.x & 63;
     const int wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WPG;
     int tm, tn;
-    tile_at(place % per, tiles_m, tiles_n, tm, tn);
+    tile_at(place, tiles_m, tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     float *C = a.C + e * a.stridec + m0 * a.ldc + n0;
     const auto near = [&](auto op, const float *P, int64_t ld, int X) {
@@ -327,19 +329,88 @@ hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
     return launch(grouped_few_kernel<MB, BX, KW, ROWS>, grid_of(n), dim3(64 * KW * ROWS), s, a, epi, (int)most);
 }
 
+// The tile of a product of grouped rows.  How many tiles there will be is only
+// guessed here (groups of like size): one per group that can hold a row, or a
+// half-empty one per group beside the full ones.  Tiles of 32 rows throughout:
+// a group leaves 16 rows of its last tile empty on average, with 64 rows 32, and
+// the last round of tiles is shorter (1,536 to 8,192 rows of 8 groups, 2048 x
+// 1024: 3 to 10% less time than in 64 x 64).  The k-groups by how many tiles a
+// CU holds at once (us, K = 768, groups of like size):
+//
+//   rows, groups, N    32 x 64 in 1   in 2   in 4   32 x 32 in 8
+//     64,  8,  768         21.1       14.4   13.3       10.2
+//    192,  8,  768         20.9       14.3   13.2       17.1
+//    256,  8, 2304         32.9       22.7   25.8       32.5
+//    768,  8, 2304         35.7       43.1   46.0       59.6
+//   1536, 32,  768         35.2       37.6   45.7       53.1
+//
+// One 32 x 32 tile in 8 k-groups, or one 32 x 64 in 4, fills a CU's LDS; 3 in 2
+// k-groups and 6 in 1 do.  Longer grids ran in 2 as fast as in 1 or faster up to
+// 14 tiles per CU (4,096 rows of 8 groups, 2048 x 1024: 170 against 167; 2,048:
+// 91 against 94; 8,192: 317 against 307).
 template <bool BX, class E>
 hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStream_t s) {
-    const int64_t per_group = a.g.M / a.g.E;
-    if (per_group < 32) return rows_tiles<32, 64, BX, 4, 2>(a, epi, s);
-    return rows_tiles<64, 64, BX, 2, 4>(a, epi, s);
+    const int64_t M = a.g.M, some = M < a.g.E ? M : a.g.E, full = M / 32 + a.g.E / 2;
+    const int64_t rows = some > full ? some : full, cus = num_cus;
+    const int64_t quarters = rows * (((int64_t)a.N + 31) / 32), tiles = rows * (((int64_t)a.N + 63) / 64);
+    const int slabs = slabs_of<32>(a.K);              // a k-group should have one at least
+    if (slabs >= 8 && quarters <= cus) return rows_tiles<32, 32, BX, 8, 1>(a, epi, s);
+    if (slabs >= 8 && tiles <= cus) return rows_tiles<32, 64, BX, 4, 2>(a, epi, s);
+    if (slabs >= 4 && (tiles <= 3 * cus || (4 * tiles > 17 * cus && tiles < 14 * cus)))
+        return rows_tiles<32, 64, BX, 2, 2>(a, epi, s);
+    return rows_tiles<32, 64, BX, 1, 2>(a, epi, s);
 }
 
+// Up to 16 rows, where groups have one or two at most: a kernel that reads each
+// group's matrix once, without tiles (us, 8 groups of N x K = 2304 x 768 /
+// 768 x 2304, against the best tile):
+//   W stored K x N   2 rows 6.9 / 9.4 against 9.7 / 16.3, 4 rows 8.1 / - against
+//                    10.1, 8 rows 9.6 / 9.9 against 9.9 / 16.7, 16 rows 12.0 / 14.5
+//                    against 13.3 / 17.1, 32 rows 19.6 / 21.7 against 14.7 / 17.5
+//   W stored N x K   2 rows 6.7 / 7.1 against 9.1 / 15.3, 8 rows 10.0 / 8.2 against
+//                    9.5 / 15.3, 16 rows 14.4 / 11.0 against 12.7 / 15.4
+// K x N: 16 waves per 32 columns where that is a workgroup per CU at most, else
+// 8 (2 rows, 2304 x 768: 6.9 against 7.3; 4 rows 10.3 against 8.1).
+inline bool few_rows(const GroupedRows &a, bool nk) {
+    const int64_t M = a.g.M, E = a.g.E;
+    return M <= 16 && (M <= E || (M <= 2 * E && (!nk || a.N <= 2048)));
+}
+
+template <bool BX>
+hipError_t few_product(const GroupedRows &a, const Layer &epi, int num_cus, hipStream_t s) {
+    if constexpr (BX) {
+        return few_tiles<2, true, 1, 4>(a, epi, s);
+    } else {
+        const int64_t M = a.g.M, slabs = ((int64_t)a.N + 31) / 32;
+        const bool wide = M * slabs <= num_cus;
+        if (M <= a.g.E) return wide ? few_tiles<1, false, 16, 1>(a, epi, s) : few_tiles<1, false, 8, 1>(a, epi, s);
+        return wide ? few_tiles<2, false, 16, 1>(a, epi, s) : few_tiles<2, false, 8, 1>(a, epi, s);
+    }
+}
+
+template <bool BX>
+hipError_t layer_product(const GroupedRows &a, const Layer &epi, int num_cus, hipStream_t s) {
+    return few_rows(a, BX) ? few_product<BX>(a, epi, num_cus, s) : rows_product<BX>(a, epi, num_cus, s);
+}
+
+template <int KS, Pick PICK>
+hipError_t weights_tiles(const GroupedWeights &a, const Store &epi, int64_t n, hipStream_t s) {
+    return launch(grouped_weights_kernel<64, 64, KS, 4, PICK>, grid_of(n), dim3(256 * KS), s, a, epi);
+}
+
+// 64 x 64 tiles; their k-groups by the rows per group, which is how far a tile
+// walks, and by tiles per CU (us in 1 / 2 / 4 k-groups, 8 groups unless said):
+//   rows   768 x 768       1024 x 1024      2048 x 1024
+//   2048   50 / 62 / 58    74 / 77 / 79     107 / 112 / 141
+//   4096   92 / 94 / 82    132 / 123 / 114  204 / 181 / 212
+//   6144   140 / 124 / 107 175 / 168 / 147  278 / 251 / 277
+//   4096 rows of 32 groups, 1024 x 1024: 115 / 144 / 194
 template <Pick PICK>
-hipError_t weights_product(const GroupedWeights &a, const Store &epi, hipStream_t s) {
-    constexpr int BM = 64, BN = 64, KS = 2, WPG = 4;
-    const int64_t n = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
-    if (n > INT_MAX / a.g.E) return hipErrorInvalidConfiguration;
-    return launch(grouped_weights_kernel<BM, BN, KS, WPG, PICK>, grid_of(n * a.g.E), dim3(64 * WPG * KS), s, a, epi);
+hipError_t weights_product(const GroupedWeights &a, const Store &epi, int num_cus, hipStream_t s) {
+    const int64_t per = (((int64_t)a.M + 63) / 64) * (((int64_t)a.N + 63) / 64), n = per * a.g.E;
+    if (per > INT_MAX / a.g.E) return hipErrorInvalidConfiguration;
+    if (a.g.M / a.g.E < 320) return weights_tiles<1, PICK>(a, epi, n, s);
+    return n <= 8 * (int64_t)num_cus ? weights_tiles<4, PICK>(a, epi, n, s) : weights_tiles<2, PICK>(a, epi, n, s);
 }
 
 }  // namespace
@@ -350,7 +421,7 @@ hipError_t launch_linear_grouped(const LinearGrouped &a, int num_cus, hipStream_
     const GroupedRows r{{a.offsets, a.E, a.M}, a.N, a.K, a.T, a.X, a.W, a.rows, a.Y,
                         a.ldx, a.ldw, a.stridew, a.ldy, a.ldb};
     const Layer e{a.bias, nullptr, 0, a.Z, a.ldz, a.act};
-    return a.trans_w ? rows_product<true>(r, e, num_cus, s) : rows_product<false>(r, e, num_cus, s);
+    return a.trans_w ? layer_product<true>(r, e, num_cus, s) : layer_product<false>(r, e, num_cus, s);
 }
 
 hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hipStream_t s) {
@@ -386,8 +457,8 @@ hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hip
         GroupedWeights w{g, a.K, a.N, a.T, a.X, dZ, a.rows, a.dW, a.ldx, lddz, a.lddw, a.stridedw};
         if (a.trans_w) w = {g, a.N, a.K, a.T, dZ, a.X, a.rows, a.dW, lddz, a.ldx, a.lddw, a.stridedw};
         const Store st{a.accumulate};
-        e = !a.rows ? weights_product<NEITHER>(w, st, s)
-            : a.trans_w ? weights_product<PICK_B>(w, st, s) : weights_product<PICK_A>(w, st, s);
+        e = !a.rows ? weights_product<NEITHER>(w, st, num_cus, s)
+            : a.trans_w ? weights_product<PICK_B>(w, st, num_cus, s) : weights_product<PICK_A>(w, st, num_cus, s);
     }
     return e;
 }
