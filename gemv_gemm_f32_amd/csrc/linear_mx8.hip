@@ -33,8 +33,10 @@ __global__ __launch_bounds__(64 * KW, MW) void packed_block_kernel(PackedLinear 
 
 template <int BM, int NW, int BITS, int MW = 2>
 __global__ __launch_bounds__(64 * NW, MW) void packed_wide_kernel(PackedLinear a, int tiles_m) {
+    __shared__ __attribute__((aligned(16))) char smem[wide_bytes<BM, NW>()];
     const int tb = tile_number();
-    packed_wide<BM, NW, BITS>(a, (int64_t)(tb % tiles_m) * BM, (int64_t)(tb / tiles_m) * 32 * NW, SameRow{});
+    packed_wide<BM, NW, BITS>(a, (int64_t)(tb % tiles_m) * BM, (int64_t)(tb / tiles_m) * 32 * NW, SameRow{},
+                              smem);
 }
 
 // A launch has fewer than 2^32 threads: with `threads` for each bm x bn tile,

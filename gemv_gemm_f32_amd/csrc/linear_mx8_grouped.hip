@@ -73,10 +73,20 @@ __global__ __launch_bounds__(64 * KW, MW) void packed_block_grouped(PackedGroupe
 
 template <int BM, int NW, int BITS, int MW>
 __global__ __launch_bounds__(64 * NW, MW) void packed_wide_grouped(PackedGrouped a, int most) {
+    __shared__ __attribute__((aligned(16))) char smem[wide_bytes<BM, NW>()];
     GroupTile t;
     int64_t n0;
     if (!find_tile<BM>(a, 32 * NW, most, t, n0)) return;
-    packed_wide<BM, NW, BITS>(layer_of<BM>(a, t), 0, n0, PickedRow(a, t));
+    const PackedLinear p = layer_of<BM>(a, t);
+    const PickedRow x(a, t);
+    // what a group's last tile needs no more than half of runs as one of half
+    // the rows
+    if constexpr (BM == 64 && NW == 4)
+        if (t.left <= 32) {
+            packed_wide<32, NW, BITS>(p, 0, n0, x, smem);
+            return;
+        }
+    packed_wide<BM, NW, BITS>(p, 0, n0, x, smem);
 }
 
 template <class Kernel>
@@ -101,14 +111,44 @@ hipError_t launch_wide(const PackedGrouped &a, hipStream_t s) {
     return launch_tiles(packed_wide_grouped<BM, NW, BITS, MW>, a, BM, 32 * NW, 64 * NW, s);
 }
 
+// The shape by what the groups' sizes are likely to be (rows / groups each) and by
+// how many tiles that makes (2 bits, us):
+//  - up to 8 rows per group in at most 16 tiles of 16 x 16 per CU: the kernel of
+//    few rows. 8 rows of 64 groups, 1536 x 1536: 7.5, in 32 x 128 tiles 12.5; 64 of
+//    16, 2048 x 4096: 22.0 / 26.9; but 8 of 64, 12288 x 1536: 25.1 / 23.7, and 128
+//    of 64, 1536 x 1536: 18.5 / 17.2.  Its runs of k: 4 for up to 4 tiles per CU (8
+//    rows of 64 groups: 7.5, 8.0 in 2, 8.5 in 1, 8.2 in 8), more for long rows where
+//    there is a tile per CU (2 rows, 1536 x 12288: 11.2 in 16, 12.4 in 4), else 1 (64
+//    rows of 16 groups, 2048 x 4096: 22.0 / 22.9 in 4; 32 of 64: 11.2 / 11.8), or 2
+//    with an output in 8 bits.
+//  - long rows and up to 6 cells of 32 x 32 per CU: a wave per run of k in each (400
+//    rows of 16 groups, 2048 x 4096: 28.6, 33.6 in 32 x 128, 36.3 in 64 x 128).
+//  - less than 16 rows per group: 32 x 128 (128 rows of 16 groups, 12288 x 1536:
+//    39.0, in 64 x 128 45.1).
+//  - 128 x 256 for large groups and products (4,096 rows of 8 groups, 4096 x 4096:
+//    201 / 217 at 4 bits, 210 / 234 in 64 x 128).
+//  - else 64 x 128, a last tile of up to 32 rows as 32 x 128 (1,000 rows of 16 groups,
+//    12288 x 1536: 80.6, all in 64 x 128 89.2, all in 32 x 128 87.7).
 template <int BITS>
 hipError_t launch_bits(const PackedGrouped &a, int num_cus, hipStream_t s) {
-    const int64_t per_group = a.layer.M / a.E;
-    if (per_group <= 8) {
-        if (a.layer.Y8) return launch_rows<BITS, 2, 4>(a, s);
-        return launch_rows<BITS, 1, 4>(a, s);
+    const int64_t M = a.layer.M, E = a.E, N = a.layer.N, cus = num_cus;
+    const auto tiles = [&](int bm, int bn) {
+        const int64_t some = M < E ? M : E, full = M / bm + E / 2;
+        return (some > full ? some : full) * ((N + bn - 1) / bn);
+    };
+    const bool lengthy = a.layer.K >= 4096;
+    const int64_t sixteens = tiles(16, 16);
+    if (M <= 8 * E && sixteens <= 16 * cus) {
+        if (a.layer.Y8) {
+            if (sixteens > 4 * cus) return launch_rows<BITS, 2, 2>(a, s);
+            return lengthy && sixteens <= cus ? launch_rows<BITS, 2, 8>(a, s) : launch_rows<BITS, 2, 4>(a, s);
+        }
+        if (sixteens > 4 * cus) return launch_rows<BITS, 1, 1>(a, s);
+        return lengthy && sixteens <= cus ? launch_rows<BITS, 1, 16>(a, s) : launch_rows<BITS, 1, 4>(a, s);
     }
-    if (per_group <= 32) return launch_block<4, BITS, 3>(a, s);
+    if (a.layer.K >= 2048 && tiles(32, 32) <= 6 * cus) return launch_block<4, BITS, 3>(a, s);
+    if (M < 16 * E) return launch_wide<32, 4, BITS, 3>(a, s);
+    if (M >= 256 * E && tiles(128, 256) >= 2 * cus) return launch_wide<128, 8, BITS, 2>(a, s);
     return launch_wide<64, 4, BITS, 3>(a, s);
 }
 

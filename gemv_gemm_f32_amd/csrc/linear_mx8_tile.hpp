@@ -674,14 +674,21 @@ __device__ __forceinline__ void packed_block(const PackedLinear &a, int64_t m0, 
 // bank twice, and every place within a stage is one address and a constant.
 constexpr int SPAN = 128, SPANB = 2 * SPAN + 16;      // columns of x in a stage, bytes of a row
 
+//
+// smem: wide_bytes<BM, NW>() of LDS, 16-byte aligned, the caller's, so that one
+// kernel may run tiles of several shapes.
+template <int BM, int NW>
+constexpr int wide_bytes() {
+    return 3 * BM * SPANB > BM * 32 * NW * 4 ? 3 * BM * SPANB : BM * 32 * NW * 4;
+}
+
 template <int BM, int NW, int BITS, class XOf>
-__device__ __forceinline__ void packed_wide(const PackedLinear &a, int64_t m0, int64_t n0, XOf x_of) {
+__device__ __forceinline__ void packed_wide(const PackedLinear &a, int64_t m0, int64_t n0, XOf x_of,
+                                            char *smem) {
     constexpr int THREADS = 64 * NW, BN = 32 * NW, IB = BM / 32;
     constexpr int XC = BM * (SPAN / 16) / THREADS;    // units of 16 columns of x per thread
     static_assert(XC * THREADS == BM * (SPAN / 16), "loads must split evenly");
-    constexpr int STAGE = BM * SPANB, TILE = BM * BN * 4;
-    constexpr int SMEM = 3 * STAGE > TILE ? 3 * STAGE : TILE;
-    __shared__ __attribute__((aligned(16))) char smem[SMEM];
+    constexpr int STAGE = BM * SPANB;
 
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
