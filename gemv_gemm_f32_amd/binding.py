@@ -447,7 +447,13 @@ def _arg(t, shape, dtype, name, dev):
     shape and type on device number `dev`; (None, 0) for None."""
     if t is None:
         return None, 0
-    if getattr(t, "dtype", None) is not dtype:
+    try:
+        # what nearly every call passes
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr(), shape[-1] or 1
+    except AttributeError:
+        raise _type_error(t, dtype, name) from None
+    if t.dtype is not dtype:
         raise _type_error(t, dtype, name)
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
@@ -487,9 +493,9 @@ def _out(t, shape, dtype, name, dev, like, stream):
 def _new(shape, dtype, like, stream):
     """A new tensor that belongs to the stream the call runs on, so that its
     memory is neither taken from nor given back to work of another stream."""
-    torch = _torch()
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(*shape) if like.dtype is dtype else like.new_empty(*shape, dtype=dtype)
+    torch = _torch()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
@@ -497,12 +503,12 @@ def _new(shape, dtype, like, stream):
 
 
 def _matrix(t, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("%s must be 2-D" % name)
-    return tuple(t.shape)
+    return shape
 
 
 def _activation(act):
@@ -619,8 +625,11 @@ def rmsnorm_f32(X, gamma=None, eps=1e-5, residual=None, S=None, Y=None, rstd=Non
 
 def _bytes(t):
     """A float8 tensor as its bytes; a uint8 tensor as it is."""
+    if t is None:
+        return None
     torch = _torch()
-    if getattr(t, "dtype", None) in (torch.float8_e4m3fn, torch.float8_e8m0fnu):
+    dtype = getattr(t, "dtype", None)
+    if dtype is not torch.uint8 and (dtype is torch.float8_e4m3fn or dtype is torch.float8_e8m0fnu):
         return t.view(torch.uint8)
     return t
 
@@ -726,47 +735,39 @@ def linear_q4_mx8(X8, XE, Q, S, bias=None, act="none", residual=None, Y=None, Y8
 
 # ---------------------------------------------------- layers with experts --
 
-def _each(t, shape, dtype, name, dev):
-    """(address, leading dimension, stride) of a matrix per expert: a 3-D
-    tensor of this shape; (None, 0, 0) for None."""
-    if t is None:
-        return None, 0, 0
+def _each(t, dtype, name, dev):
+    """(shape, address, leading dimension, stride) of a matrix per expert, a
+    3-D tensor."""
     if getattr(t, "dtype", None) is not dtype:
         raise _type_error(t, dtype, name)
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError("%s must be 3-D" % name)
     if t.get_device() != dev:
         raise ValueError("%s must be on the current GPU device" % name)
+    e, r, c = shape
+    if t.is_contiguous():
+        return shape, t.data_ptr(), c or 1, r * c
     st = t.stride()
-    if shape[2] > 1 and st[2] != 1 and t.numel():
+    if c > 1 and st[2] != 1 and t.numel():
         raise ValueError("%s must have a contiguous last dimension" % name)
-    return t.data_ptr(), st[1] if shape[1] > 1 else shape[2] or 1, st[0] if shape[0] > 1 else 0
-
-
-def _three(t, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch tensor" % name)
-    if t.dim() != 3:
-        raise ValueError("%s must be 3-D" % name)
-    return tuple(t.shape)
+    return shape, t.data_ptr(), st[1] if r > 1 else c or 1, st[0] if e > 1 else 0
 
 
 def _grouping(offsets, rows, X_rows, E, M, dev):
     """(address of rows, address of offsets, M) of a layer on grouped rows; M
     is given, or that of X without rows."""
     i32 = _torch().int32
-    po, _ = _arg(offsets, (E + 1,), i32, "offsets", dev)
-    if po is None:
+    if offsets is None:
         raise TypeError("offsets must be a torch tensor of int32")
+    po, _ = _arg(offsets, (E + 1,), i32, "offsets", dev)
     if rows is None:
         if M is not None and M != X_rows:
             raise ValueError("without rows, X must have a row for each of the %d rows" % M)
         return None, po, X_rows
-    if getattr(rows, "dtype", None) is not i32:
-        raise _type_error(rows, i32, "rows")
     if M is None:
-        M = rows.numel()
+        shape = getattr(rows, "shape", None)
+        M = shape[0] if shape else 0
     pr, _ = _arg(rows, (M,), i32, "rows", dev)
     return pr, po, M
 
@@ -848,11 +849,12 @@ def linear_f32_grouped(X, W, offsets, rows=None, bias=None, act="none", Z=None, 
     torch = _torch()
     f32, dev = torch.float32, torch.cuda.current_device()
     T, K = _matrix(X, "X")
-    wshape = _three(W, "W")
-    E, N = wshape[0], wshape[1] if trans_w else wshape[2]
+    (E, r, c), pw, ldw, sw = _each(W, f32, "W", dev)
+    N = r if trans_w else c
+    if (c if trans_w else r) != K:
+        raise ValueError("W must have %d inputs" % K)
     px, ldx = _arg(X, (T, K), f32, "X", dev)
     pr, po, M = _grouping(offsets, rows, T, E, None, dev)
-    pw, ldw, sw = _each(W, (E, N, K) if trans_w else (E, K, N), f32, "W", dev)
     pb, ldb = _arg(bias, (E, N), f32, "bias", dev)
     pz, ldz = _arg(Z, (M, N), f32, "Z", dev)
     Y, py, ldy = _out(Y, (M, N), f32, "Y", dev, X, stream)
@@ -880,7 +882,7 @@ def linear_f32_grouped_bwd(dY, X, W, offsets, rows=None, Z=None, act="none", tra
     f32, dev = torch.float32, torch.cuda.current_device()
     M, N = _matrix(dY, "dY")
     wx, ww, wb = (n in want for n in ("dX", "dW", "db"))
-    E, r, c = _three(W, "W")
+    (E, r, c), pw, ldw, sw = _each(W, f32, "W", dev)
     K = c if trans_w else r
     if (r if trans_w else c) != N:
         raise ValueError("W must have %d outputs" % N)
@@ -896,13 +898,15 @@ def linear_f32_grouped_bwd(dY, X, W, offsets, rows=None, Z=None, act="none", tra
     pz, ldz = _arg(Z if a else None, (M, N), f32, "Z", dev)
     px, ldx = _arg(X, (T, K), f32, "X", dev)
     pr, po, _ = _grouping(offsets, rows, T, E, M, dev)
-    pw, ldw, sw = _each(W, (E, r, c), f32, "W", dev)
     none = (None, None, 0)
     dX, pdx, lddx = _out(dX, (M, K), f32, "dX", dev, dY, stream) if wx else none
     pdw = lddw = sdw = 0
     if ww:
-        dW = _new((E, r, c), f32, dY, stream) if dW is None else dW
-        pdw, lddw, sdw = _each(dW, (E, r, c), f32, "dW", dev)
+        if dW is None:
+            dW = _new((E, r, c), f32, dY, stream)
+        shape, pdw, lddw, sdw = _each(dW, f32, "dW", dev)
+        if shape != (E, r, c):
+            raise ValueError("dW must have the shape of W")
     else:
         dW = None
     db, pdb, lddb = _out(db, (E, N), f32, "db", dev, dY, stream) if wb else none
@@ -922,17 +926,17 @@ def _packed_grouped(name, bits, X8, XE, Q, S, offsets, rows, bias, act, Y, Y8, Y
         raise ValueError("out must be f32, mx8 or both")
     X8, XE = _bytes(X8), _bytes(XE)
     T, K = _matrix(X8, "X8")
-    E, N, qc = _three(Q, "Q")
-    sc = _three(S, "S")[2]
+    if getattr(S, "dtype", None) is torch.int16:
+        S = S.view(torch.float16)
+    (E, N, qc), pq, ldq, sq = _each(Q, u8, "Q", dev)
+    (se, sn, sc), ps, lds, ss = _each(S, torch.float16, "S", dev)
+    if se != E or sn != N:
+        raise ValueError("Q and S must have the same number of experts and rows")
     if qc < -(-K * bits // 8) or sc < -(-K // 64):
         raise ValueError("Q and S must have columns for %d inputs" % K)
-    if S.dtype is torch.int16:
-        S = S.view(torch.float16)
     px, ldx = _arg(X8, (T, K), u8, "X8", dev)
     pe, ldxe = _arg(XE, (T, -(-K // 32)), u8, "XE", dev)
     pr, po, M = _grouping(offsets, rows, T, E, None, dev)
-    pq, ldq, sq = _each(Q, (E, N, qc), u8, "Q", dev)
-    ps, lds, ss = _each(S, (E, N, sc), torch.float16, "S", dev)
     pb, ldb = _arg(bias, (E, N), f32, "bias", dev)
     py = ldy = p8 = ldy8 = pye = ldye = 0
     if out != "mx8":
