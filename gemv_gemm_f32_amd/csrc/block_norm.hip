@@ -179,24 +179,49 @@ __global__ __launch_bounds__(1024) void block_norm_long_kernel(BlockNorm a) {
 }
 
 // One workgroup per row of the workspace (sums of dgamma_s, then q); its
-// T-thread teams take rows in turn.
+// T-thread teams take rows in turn.  With more than two chunks per thread the
+// column sums lie in LDS, each touched by its own thread alone, and vectors are
+// read again for each row: registers hold the row and no more.
 template <int T, int NV, Fit F>
 __global__ __launch_bounds__(group_threads<T>()) void block_norm_bwd_kernel(BlockNormBwd a) {
     constexpr int THREADS = group_threads<T>(), ROWS = THREADS / T;
-    constexpr bool ODD = F != WHOLE;
+    constexpr bool ODD = F != WHOLE, FULL = NV > 2;
+    static_assert(!FULL || ROWS == 1, "one team where the sums lie in LDS");
     __shared__ float red[2][16];
     __shared__ float part[ROWS > 1 ? THREADS * 4 : 1];
+    __shared__ v4f sums[FULL ? 2 * NV * T : 1];
     const int t = threadIdx.x % T;
     const float invk = 1.f / (float)a.K;
-    v4f gu[NV], gs[NV], gt[NV], qs[NV], qu[NV];
+    constexpr int HELD = FULL ? 1 : NV;
+    v4f gu[HELD], gs[HELD], gt[NV], qs[HELD], qu[HELD];
+    const auto zero = v4f{0.f, 0.f, 0.f, 0.f};
+    const auto column = [&](int j) { return (int64_t)(t + T * j) * 4; };
+    if constexpr (FULL) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int64_t col = (int64_t)(t + T * j) * 4;
-        gu[j] = factor<F>(a.gu, col, a.K);
-        gs[j] = factor<F>(a.gs, col, a.K);
-        gt[j] = factor<F>(a.own ? nullptr : a.gate, col, a.K);
-        qs[j] = qu[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < 2 * NV; ++j) sums[j * T + t] = zero;
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            gu[j] = factor<F>(a.gu, column(j), a.K);
+            gs[j] = factor<F>(a.gs, column(j), a.K);
+            gt[j] = factor<F>(a.own ? nullptr : a.gate, column(j), a.K);
+            qs[j] = qu[j] = zero;
+        }
     }
+    // chunk j of a vector, and of a column sum, to which w times x is added
+    const auto vec = [&](const v4f (&held)[HELD], const float *from, int j) {
+        if constexpr (FULL) return factor<F>(from, column(j), a.K);
+        else return held[j];
+    };
+    const auto add = [&](v4f (&held)[HELD], int which, int j, const v4f &w, const v4f &x) {
+        v4f q;
+        if constexpr (FULL) q = sums[(which * NV + j) * T + t];
+        else q = held[j];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) q[c] = __builtin_fmaf(w[c], x[c], q[c]);
+        if constexpr (FULL) sums[(which * NV + j) * T + t] = q;
+        else held[j] = q;
+    };
     for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.M; base += (int64_t)gridDim.x * ROWS) {
         const int64_t want = base + threadIdx.x / T;
         const bool live = want < a.M;                 // uniform per team
@@ -206,51 +231,59 @@ __global__ __launch_bounds__(group_threads<T>()) void block_norm_bwd_kernel(Bloc
         v4f d[NV], s[NV], u[NV], in[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = (int64_t)(t + T * j) * 4;
+            const int64_t col = column(j);
             d[j] = take<F>(a.dY + row * a.lddy, col, a.K);
             s[j] = take<F>(a.S + row * a.lds, col, a.K);
             u[j] = take<F>(a.U + row * a.ldu, col, a.K);
-            in[j] = v4f{0.f, 0.f, 0.f, 0.f};
+            in[j] = zero;
             if (a.dS) in[j] = take<F>(a.dS + row * a.ldds, col, a.K);
-            if (a.own) gt[j] = take<F>(a.gate + row * a.ldg, col, a.K);
+            if (a.own && !FULL) gt[j] = take<F>(a.gate + row * a.ldg, col, a.K);
         }
         if (!live) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) d[j] = s[j] = u[j] = in[j] = v4f{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < NV; ++j) d[j] = s[j] = u[j] = in[j] = zero;
         }
         float dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const v4f g = vec(gs, a.gs, j);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[j][c] *= rs;
+            add(qs, 0, j, d[j], s[j]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                s[j][c] *= rs;
-                qs[j][c] = __builtin_fmaf(d[j][c], s[j][c], qs[j][c]);
-                d[j][c] *= gs[j][c];
+                d[j][c] *= g[c];
                 dot = __builtin_fmaf(d[j][c], s[j][c], dot);
             }
+        }
         dot = row_sum<T>(dot, red, 0) * invk;
         float dot_u = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const v4f g = vec(gu, a.gu, j);
+            if constexpr (FULL) gt[j] = factor<F>(a.gate ? a.gate + row * a.ldg : nullptr, column(j), a.K);
+            v4f dv;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 d[j][c] = __builtin_fmaf(__builtin_fmaf(-s[j][c], dot, d[j][c]), rs, in[j][c]);   // dS
                 u[j][c] *= ru;
-                const float dv = d[j][c] * gt[j][c];
-                qu[j][c] = __builtin_fmaf(a.own ? dv : d[j][c], u[j][c], qu[j][c]);
-                s[j][c] = dv * gu[j][c];                                                          // h
+                dv[c] = d[j][c] * gt[j][c];
+                s[j][c] = dv[c] * g[c];                                                           // h
                 dot_u = __builtin_fmaf(s[j][c], u[j][c], dot_u);
             }
+            add(qu, 1, j, a.own ? dv : d[j], u[j]);
+        }
         if (a.dU) dot_u = row_sum<T>(dot_u, red, 1) * invk;    // uniform
         else if (T > 64) __syncthreads();                      // red[0] is used again
         if (!live) continue;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = (int64_t)(t + T * j) * 4;
+            const int64_t col = column(j);
             v4f o;
             if (a.dgate && a.own) {
+                const v4f g = vec(gu, a.gu, j);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) o[c] = d[j][c] * u[j][c] * gu[j][c];
+                for (int c = 0; c < 4; ++c) o[c] = d[j][c] * u[j][c] * g[c];
                 put<ODD>(a.dgate + row * a.lddg, col, a.K, o);
             }
             if (a.dX) {
@@ -270,8 +303,9 @@ __global__ __launch_bounds__(group_threads<T>()) void block_norm_bwd_kernel(Bloc
     float *out = a.ws + (int64_t)blockIdx.x * 2 * a.K;
 #pragma unroll
     for (int j = 0; j < 2 * NV; ++j) {
-        v4f q = j < NV ? qs[j % NV] : qu[j % NV];
-        const int64_t col = (int64_t)(t + T * (j % NV)) * 4;
+        v4f q;
+        if constexpr (FULL) q = sums[j * T + t];
+        else q = j < NV ? qs[j % NV] : qu[j % NV];
         if constexpr (ROWS > 1) {
             __syncthreads();
 #pragma unroll
@@ -283,7 +317,7 @@ __global__ __launch_bounds__(group_threads<T>()) void block_norm_bwd_kernel(Bloc
 #pragma unroll
                 for (int c = 0; c < 4; ++c) q[c] += part[(w * T + t) * 4 + c];
         }
-        put<ODD>(out + (j < NV ? 0 : a.K), col, a.K, q);
+        put<ODD>(out + (j < NV ? 0 : a.K), column(j % NV), a.K, q);
     }
 }
 
@@ -421,21 +455,49 @@ hipError_t norm(const BlockNorm &a, hipStream_t s) {
                : launch(block_norm_kernel<T, NV, F, false>, grid, dim3(group_threads<T>()), s, a);
 }
 
+// Threads and chunks per row (16 bytes per chunk) by the row's length: as few idle
+// threads as there can be, and no more than two chunks, whose loads are all in
+// flight at once (us, fp32 / 8 bits: 65536 x 256 46 / 41, on two chunks 51 / 50; 32768
+// x 768 81 / 75 on 256 threads, 85 / 82 on a wave with four chunks, 104 / 112 on 256
+// threads with two; 8192 x 4096 115 / 93 on 512, 136 / 146 on 1,024 threads; 1024 x
+// 16384 66 / 53 read twice, 57 / 65 on four chunks of 1,024 threads).
 template <Fit F>
 hipError_t norm_of(const BlockNorm &a, hipStream_t s) {
+    if (a.K <= 256) return norm<64, 1, F>(a, s);
     if (a.K <= 512) return norm<64, 2, F>(a, s);
+    if (a.K <= 1024) return norm<256, 1, F>(a, s);
     if (a.K <= 2048) return norm<256, 2, F>(a, s);
+    if (a.K <= 4096) return norm<512, 2, F>(a, s);
     if (a.K <= 8192) return norm<1024, 2, F>(a, s);
     const dim3 grid((unsigned)(a.M < MAX_GROUPS ? a.M : MAX_GROUPS));
     return a.Q ? launch(block_norm_long_kernel<F, true>, grid, dim3(1024), s, a)
                : launch(block_norm_long_kernel<F, false>, grid, dim3(1024), s, a);
 }
 
+// The same for the gradients, and how many workgroups (rows of the workspace)
+// they take: two per CU, one of 1,024 threads (16384 x 2048: 153 us on 512, 159 on
+// 768, 162 on 1,024; 4096 x 8192: 161 on 256, 170 on 512, 182 on 1,024).  Up to
+// 16,384 columns rows are read once (2048 x 12288: 145 us, in three passes 245).
+template <int T, int NV, Fit F>
+hipError_t norm_bwd(const BlockNormBwd &a, int &groups, hipStream_t s) {
+    constexpr int ROWS = group_threads<T>() / T;
+    const int64_t rows = ((int64_t)a.M + ROWS - 1) / ROWS;
+    const int most = T == 1024 ? BLOCK_NORM_BWD_GROUPS / 2 : BLOCK_NORM_BWD_GROUPS;
+    groups = (int)(rows < most ? rows : most);
+    return launch(block_norm_bwd_kernel<T, NV, F>, dim3(groups), dim3(group_threads<T>()), s, a);
+}
+
 template <Fit F>
-hipError_t norm_bwd_of(const BlockNormBwd &a, int groups, hipStream_t s) {
-    if (a.K <= 512) return launch(block_norm_bwd_kernel<64, 2, F>, dim3(groups), dim3(WG), s, a);
-    if (a.K <= 2048) return launch(block_norm_bwd_kernel<256, 2, F>, dim3(groups), dim3(WG), s, a);
-    if (a.K <= 8192) return launch(block_norm_bwd_kernel<1024, 2, F>, dim3(groups), dim3(1024), s, a);
+hipError_t norm_bwd_of(const BlockNormBwd &a, int &groups, hipStream_t s) {
+    if (a.K <= 256) return norm_bwd<64, 1, F>(a, groups, s);
+    if (a.K <= 512) return norm_bwd<64, 2, F>(a, groups, s);
+    if (a.K <= 1024) return norm_bwd<256, 1, F>(a, groups, s);
+    if (a.K <= 2048) return norm_bwd<256, 2, F>(a, groups, s);
+    if (a.K <= 4096) return norm_bwd<512, 2, F>(a, groups, s);
+    if (a.K <= 8192) return norm_bwd<1024, 2, F>(a, groups, s);
+    if (a.K <= 12288) return norm_bwd<1024, 3, F>(a, groups, s);
+    if (a.K <= 16384) return norm_bwd<1024, 4, F>(a, groups, s);
+    groups = a.M < BLOCK_NORM_BWD_GROUPS ? a.M : BLOCK_NORM_BWD_GROUPS;
     return launch(block_norm_bwd_long_kernel<F>, dim3(groups), dim3(1024), s, a);
 }
 
@@ -447,14 +509,10 @@ hipError_t launch_block_norm(const BlockNorm &a, hipStream_t s) {
 }
 
 hipError_t launch_block_norm_bwd(const BlockNormBwd &a, hipStream_t s) {
-    // a workgroup per row of the workspace; up to 512 columns it takes 4 rows
-    // at a time
-    const int64_t rows = a.K <= 512 ? ((int64_t)a.M + 3) / 4 : a.M;
-    const int groups = (int)(rows < BLOCK_NORM_BWD_GROUPS ? rows : BLOCK_NORM_BWD_GROUPS);
+    int groups = 0;
     if (a.M > 0) {
-        const hipError_t e =
-            a.K < 4 ? launch(block_norm_bwd_kernel<64, 1, TINY>, dim3(groups), dim3(WG), s, a)
-            : a.K % 4 ? norm_bwd_of<CUT>(a, groups, s) : norm_bwd_of<WHOLE>(a, groups, s);
+        const hipError_t e = a.K < 4    ? norm_bwd<64, 1, TINY>(a, groups, s)
+                             : a.K % 4 ? norm_bwd_of<CUT>(a, groups, s) : norm_bwd_of<WHOLE>(a, groups, s);
         if (e != hipSuccess) return e;
     }
     if (a.ws == nullptr && a.M > 0) return hipSuccess;

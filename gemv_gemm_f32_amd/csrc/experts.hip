@@ -271,7 +271,8 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(ExpertCombine a, in
 
 // Gradients: W waves take a token, a wave every W-th span of 256 columns, and
 // up to J of its entries at a time, whose products with dO stay in registers
-// until the row's end.
+// until the row's end.  Rows are loaded whether an entry has one or not (then
+// row 0), so that no load waits for a branch.
 template <int W, int J>
 __global__ __launch_bounds__(256) void expert_combine_bwd_kernel(ExpertCombineBwd a) {
     constexpr int TOKENS = 4 / W;
@@ -279,6 +280,7 @@ __global__ __launch_bounds__(256) void expert_combine_bwd_kernel(ExpertCombineBw
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sub = wave / W, part = wave % W;
+    const bool read = a.dw && a.M > 0;
     for (int64_t base = (int64_t)blockIdx.x * TOKENS; base < a.T; base += (int64_t)gridDim.x * TOKENS) {
         const bool live = base + sub < a.T;
         const int64_t t = live ? base + sub : a.T - 1;
@@ -290,27 +292,29 @@ __global__ __launch_bounds__(256) void expert_combine_bwd_kernel(ExpertCombineBw
             for (int i = 0; i < J; ++i) {
                 const int j = min(j0 + i, a.k - 1);
                 p[i] = a.pos[t * a.ldp + j];
-                if (j0 + i >= a.k || p[i] >= a.M || !live) p[i] = -1;
                 f[i] = a.w ? a.w[t * a.ldw + j] : 1.f;
+            }
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+                if (j0 + i >= a.k || p[i] >= a.M || !live) p[i] = -1;
                 dot[i] = 0.f;
             }
+#pragma unroll 2
             for (int64_t col = part * 256 + 4 * lane; col < a.K; col += W * 256) {
                 const v4f d = get(dO, col, a.K);
                 v4f y[J];
-                if (a.dw)
+                if (read)
 #pragma unroll
-                    for (int i = 0; i < J; ++i)
-                        if (p[i] >= 0) y[i] = get(a.Y + (int64_t)p[i] * a.ldy, col, a.K);
+                    for (int i = 0; i < J; ++i) y[i] = get(a.Y + (int64_t)max(p[i], 0) * a.ldy, col, a.K);
 #pragma unroll
                 for (int i = 0; i < J; ++i) {
-                    if (p[i] < 0) continue;           // uniform
                     v4f o;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         o[c] = f[i] * d[c];
-                        if (a.dw) dot[i] = __builtin_fmaf(d[c], y[i][c], dot[i]);
+                        if (read) dot[i] = __builtin_fmaf(d[c], y[i][c], dot[i]);
                     }
-                    if (a.dY) put(a.dY + (int64_t)p[i] * a.lddy, col, a.K, o);
+                    if (a.dY && p[i] >= 0) put(a.dY + (int64_t)p[i] * a.lddy, col, a.K, o);
                 }
             }
             if (a.dw == nullptr) continue;            // uniform
@@ -332,7 +336,7 @@ __global__ __launch_bounds__(256) void expert_combine_bwd_kernel(ExpertCombineBw
             if (live && part == 0 && lane == 0)
 #pragma unroll
                 for (int i = 0; i < J; ++i)
-                    if (j0 + i < a.k) a.dw[t * a.lddw + j0 + i] = dot[i];
+                    if (j0 + i < a.k) a.dw[t * a.lddw + j0 + i] = p[i] < 0 ? 0.f : dot[i];
         }
     }
 }
@@ -370,9 +374,21 @@ hipError_t launch_expert_combine(const ExpertCombine &a, hipStream_t s) {
     return launch(expert_combine_kernel<1>, dim3(groups((narrow * a.T + 3) / 4)), dim3(256), s, a, (int)narrow);
 }
 
+template <int W>
+hipError_t combine_bwd(const ExpertCombineBwd &a, hipStream_t s) {
+    const dim3 grid(groups(((int64_t)a.T + 4 / W - 1) / (4 / W)));
+    if (a.k == 1) return launch(expert_combine_bwd_kernel<W, 1>, grid, dim3(256), s, a);
+    if (a.k == 2) return launch(expert_combine_bwd_kernel<W, 2>, grid, dim3(256), s, a);
+    if (a.k <= 4) return launch(expert_combine_bwd_kernel<W, 4>, grid, dim3(256), s, a);
+    return launch(expert_combine_bwd_kernel<W, 8>, grid, dim3(256), s, a);
+}
+
 hipError_t launch_expert_combine_bwd(const ExpertCombineBwd &a, hipStream_t s) {
-    if (a.K > 256) return launch(expert_combine_bwd_kernel<4, 4>, dim3(groups(a.T)), dim3(256), s, a);
-    return launch(expert_combine_bwd_kernel<1, 4>, dim3(groups(((int64_t)a.T + 3) / 4)), dim3(256), s, a);
+    // four waves per token where each has a span, or where tokens are few (us, in
+    // one wave / in four: 8192 tokens, 2 entries, 2048 columns 70 / 62; 8192, 8, 512
+    // 58 / 88; 2048, 2, 768 6.5 / 7.8; 346, 2, 768 4.5 / 4.0; 1, 8, 1536 12.6 / 7.3)
+    if (a.K >= 1024 || (a.K > 256 && a.T < 1024)) return combine_bwd<4>(a, s);
+    return combine_bwd<1>(a, s);
 }
 
 }  // namespace gg

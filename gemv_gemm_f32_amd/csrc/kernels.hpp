@@ -200,7 +200,7 @@ struct BlockNormBwd {
 };
 hipError_t launch_block_norm_bwd(const BlockNormBwd &a, hipStream_t stream);
 // Partial sums of both kinds: two rows of K per workgroup.
-constexpr int BLOCK_NORM_BWD_GROUPS = 1024;
+constexpr int BLOCK_NORM_BWD_GROUPS = 512;
 inline int64_t block_norm_bwd_workspace_floats(int64_t M, int64_t K) {
     return 2 * (M < BLOCK_NORM_BWD_GROUPS ? M : BLOCK_NORM_BWD_GROUPS) * K;
 }

@@ -133,7 +133,7 @@ def block_norm_bwd(dY, U_, S, gu, gs, ru, rs, gate, alpha, dS):
     edot = (eh * a(xu)).mean(1, keepdims=True) + n * a(h * xu).mean(1, keepdims=True)
     dU = ru * (h - xu * dot)
     eU = ru * (eh + a(xu) * edot + 4 * U * (a(h) + a(xu * dot))) + U * a(dU)
-    rows = -(-M // 1024) + 100
+    rows = -(-M // 256) + 100
 
     def over_rows(t, et):
         return t.sum(0), (rows * U * a(t).sum(0) + et.sum(0)) * 1.01 + 1e-40

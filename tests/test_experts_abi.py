@@ -239,7 +239,7 @@ def test_norm_bwd_alias_and_passes():
     passes_checks(lambda: nbwd(gate=Z, dgt=O))
     passes_checks(lambda: nbwd(M=0, dy=None, u=None, s=None, ru=None, rs=None, ws=None, wsb=0))
     f = lib.block_norm_f32_bwd_ws_size
-    assert f(8, 96) == 8 * 96 * 8 and f(0, 96) == 0 and f(1 << 20, 96) == 1024 * 96 * 8
+    assert f(8, 96) == 8 * 96 * 8 and f(0, 96) == 0 and f(1 << 20, 96) == 512 * 96 * 8
     assert f(-1, 96) == BAD and f(8, 1 << 31) == BAD
 
 
