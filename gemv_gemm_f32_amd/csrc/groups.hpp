@@ -55,29 +55,58 @@ __device__ __forceinline__ int tiles_before(const Groups &g, int upto) {
     return sum;
 }
 
-// Tile number t of all (t below their number): its group, the tile's first
-// row and how many of the group's rows there are from there on.
+// Tile number t of all: its group, the tile's first row and how many of the
+// group's rows there are from there on.
 struct GroupTile {
     int e, row, left;
 };
+
+// Tiles of all groups, at most `most`, and then one of them.  Up to 64 groups'
+// offsets are read once, by the constructor.
 template <int BM>
-__device__ __forceinline__ GroupTile tile_of_groups(const Groups &g, int t) {
-    const int lane = threadIdx.x & 63;
-    for (int c = 0; c < g.E; c += 64) {
-        int first, count;
-        group_rows(g, c + lane, first, count);
-        const int n = tiles_in<BM>(count), incl = wave64_scan(n);
-        const uint64_t past = __ballot(incl > t);
-        if (past) {
-            const int l = __ffsll((unsigned long long)past) - 1;
-            const int skip = (t - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l))) * BM;
-            return {c + l, __builtin_amdgcn_readlane(first, l) + skip,
-                    __builtin_amdgcn_readlane(count, l) - skip};
+struct GroupTiles {
+    const Groups &g;
+    int first, count, incl, number;
+    __device__ __forceinline__ GroupTiles(const Groups &groups, int most) : g(groups) {
+        round(0);
+        number = __builtin_amdgcn_readlane(incl, 63);
+        for (int c = 64; c < g.E; c += 64) {
+            round(c);
+            number += __builtin_amdgcn_readlane(incl, 63);
         }
-        t -= __builtin_amdgcn_readlane(incl, 63);
+        number = __builtin_amdgcn_readfirstlane(min(number, most));
     }
-    return {0, 0, 0};
-}
+    // t below number
+    __device__ __forceinline__ GroupTile operator[](int t) {
+        if (g.E <= 64) return within(0, t);
+        for (int c = 0;; c += 64) {
+            round(c);
+            const int here = __builtin_amdgcn_readlane(incl, 63);
+            if (t < here || c + 64 >= g.E) return within(c, t);
+            t -= here;
+        }
+    }
+
+private:
+    // a lane per group from c on: its rows, and tiles up to its end
+    __device__ __forceinline__ void round(int c) {
+        group_rows(g, c + (int)(threadIdx.x & 63), first, count);
+        incl = wave64_scan(tiles_in<BM>(count));
+    }
+    // (The same in every lane, and made so: addresses that the compiler takes for
+    // a lane's own cost each load a loop over the lanes: 10 to 15% of the fp32
+    // products.)
+    __device__ __forceinline__ GroupTile within(int c, int t) const {
+        const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(incl > t)) - 1);
+        const int rows = __builtin_amdgcn_readlane(count, l);
+        const int skip = (t - (__builtin_amdgcn_readlane(incl, l) - tiles_in<BM>(rows))) * BM;
+        // Offsets that are not in order can make the sum pass 32 bits.
+        if (skip < 0 || skip >= rows) return {0, 0, 1};
+        return {__builtin_amdgcn_readfirstlane(c + l),
+                __builtin_amdgcn_readfirstlane(__builtin_amdgcn_readlane(first, l) + skip),
+                __builtin_amdgcn_readfirstlane(rows - skip)};
+    }
+};
 
 // Workgroups in a grid of up to 65,535 x 2^20, and one's number.
 __device__ __forceinline__ int64_t group_number() {

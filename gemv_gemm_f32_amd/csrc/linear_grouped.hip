@@ -110,18 +110,18 @@ struct GroupedRows {
     int64_t lda, ldb, strideb, ldc, ldbias;
 };
 
-template <int BM, int BN, bool BX, int KS, int WPG, class E>
+template <int BM, int BN, bool BX, int KS, int WPG, bool KT, class E>
 __global__ __launch_bounds__(64 * WPG * KS) void grouped_rows_kernel(GroupedRows a, E epi, int most) {
-    using S = TileShape<BM, BN, true, BX, KS, WPG, true, 32>;
+    using S = TileShape<BM, BN, true, BX, KS, WPG, KT, 32>;
     const int tiles_n = (a.N + BN - 1) / BN;
-    const int tiles_m = min(tiles_before<BM>(a.g, a.g.E), most);
-    const int64_t bid = group_number(), n = (int64_t)tiles_m * tiles_n;
+    GroupTiles<BM> tiles(a.g, most);
+    const int64_t bid = group_number(), n = (int64_t)tiles.number * tiles_n;
     if (bid >= n) return;
     const int lane = threadIdx.x & 63;
     const int wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WPG;
     int tm, tn;
-    tile_at(xcd_run((int)bid, (int)n), tiles_m, tiles_n, tm, tn);
-    const GroupTile t = tile_of_groups<BM>(a.g, tm);
+    tile_at(xcd_run((int)bid, (int)n), tiles.number, tiles_n, tm, tn);
+    const GroupTile t = tiles[tm];
     const int n0 = tn * BN, left = min(t.left, BM), cols = a.N - n0;
 
     NearSlabs<typename S::OA, true> sa{{}, a.A, a.lda, left, a.K};
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(64 * WPG * KS) void grouped_rows_kernel(GroupedRows
     NearSlabs<typename S::OB, BX> sb{{}, a.B + t.e * a.strideb + (BX ? n0 * a.ldb : n0), a.ldb,
                                      BX ? min(cols, BN) : cols, a.K};
     sb.op.init(a.ldb, 0, cols, lane, wq);
-    direct_tile<BM, BN, true, BX, KS, WPG, true, 32>(left, cols, a.K, sa, sb, a.C + t.row * a.ldc + n0,
+    direct_tile<BM, BN, true, BX, KS, WPG, KT, 32>(left, cols, a.K, sa, sb, a.C + t.row * a.ldc + n0,
                                                      a.ldc, at_tile(epi, t.e * a.ldbias, t.row, n0), 0, 0);
 }
 
@@ -148,10 +148,10 @@ template <int MB, bool BX, int KW, int ROWS>
 __global__ __launch_bounds__(64 * KW * ROWS) void grouped_few_kernel(GroupedRows a, Layer epi, int most) {
     constexpr int COLS = BX ? ROWS : 32;
     const int tiles_n = (a.N + COLS - 1) / COLS;
-    const int tiles_m = min(tiles_before<MB>(a.g, a.g.E), most);
+    GroupTiles<MB> tiles(a.g, most);
     const int64_t bid = group_number();
-    if (bid >= (int64_t)tiles_m * tiles_n) return;
-    const GroupTile t = tile_of_groups<MB>(a.g, (int)(bid / tiles_n));
+    if (bid >= (int64_t)tiles.number * tiles_n) return;
+    const GroupTile t = tiles[(int)(bid / tiles_n)];
     const int64_t n0 = bid % tiles_n * COLS;
     const int left = min(t.left, MB);
     const int32_t *rows = a.rows ? a.rows + t.row : nullptr;
@@ -230,11 +230,11 @@ __global__ __launch_bounds__(256) void grouped_dz_kernel(Groups g, int act, int 
                                                          float *dZ, int64_t lddz, float *partial, int most) {
     __shared__ v4f red[256];
     const int tiles_n = (N + 63) / 64;
-    const int tiles = min(tiles_before<DZ_ROWS>(g, g.E), most);
+    GroupTiles<DZ_ROWS> tiles(g, most);
     const int64_t bid = group_number();
-    if (bid >= (int64_t)tiles * tiles_n) return;
+    if (bid >= (int64_t)tiles.number * tiles_n) return;
     const int tm = (int)(bid / tiles_n);
-    const GroupTile t = tile_of_groups<DZ_ROWS>(g, tm);
+    const GroupTile t = tiles[tm];
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     const int64_t col = bid % tiles_n * 64 + 4 * tx;
     const int live = (int)min(max(N - col, (int64_t)0), (int64_t)4);   // columns of this thread that exist
@@ -318,7 +318,10 @@ template <int BM, int BN, bool BX, int KS, int WPG, class E>
 hipError_t rows_tiles(const GroupedRows &a, const E &epi, hipStream_t s) {
     const int64_t most = tiles_most(a.g.M, a.g.E, BM), n = most * (((int64_t)a.N + BN - 1) / BN);
     if (n > INT_MAX) return hipErrorInvalidConfiguration;
-    return launch(grouped_rows_kernel<BM, BN, BX, KS, WPG, E>, grid_of(n), dim3(64 * WPG * KS), s, a, epi, (int)most);
+    // (K a multiple of 4 apart: 8192 x 2048 x 1024 3.6% faster without the code for
+    // chunks that K cuts)
+    return a.K % 4 ? launch(grouped_rows_kernel<BM, BN, BX, KS, WPG, true, E>, grid_of(n), dim3(64 * WPG * KS), s, a, epi, (int)most)
+                   : launch(grouped_rows_kernel<BM, BN, BX, KS, WPG, false, E>, grid_of(n), dim3(64 * WPG * KS), s, a, epi, (int)most);
 }
 
 template <int MB, bool BX, int KW, int ROWS>
@@ -333,9 +336,11 @@ hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
 // guessed here (groups of like size): one per group that can hold a row, or a
 // half-empty one per group beside the full ones.  Tiles of 32 rows throughout:
 // a group leaves 16 rows of its last tile empty on average, with 64 rows 32, and
-// the last round of tiles is shorter (1,536 to 8,192 rows of 8 groups, 2048 x
-// 1024: 3 to 10% less time than in 64 x 64).  The k-groups by how many tiles a
-// CU holds at once (us, K = 768, groups of like size):
+// the last round of tiles is shorter.  (2048 x 1024, us in 32 x 64 against 64 x
+// 64, both in 2 k-groups, for groups of like, not the same size: 2,048 rows of 8
+// groups 83 / 89, 4,096 153 / 157, 8,192 of 8 293 / 295, of 64 351 / 378, of one
+// 286 / 279.)  The k-groups by how many tiles a CU holds at once (us, K = 768,
+// groups of like size):
 //
 //   rows, groups, N    32 x 64 in 1   in 2   in 4   32 x 32 in 8
 //     64,  8,  768         21.1       14.4   13.3       10.2
@@ -345,9 +350,9 @@ hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
 //   1536, 32,  768         35.2       37.6   45.7       53.1
 //
 // One 32 x 32 tile in 8 k-groups, or one 32 x 64 in 4, fills a CU's LDS; 3 in 2
-// k-groups and 6 in 1 do.  Longer grids ran in 2 as fast as in 1 or faster up to
-// 14 tiles per CU (4,096 rows of 8 groups, 2048 x 1024: 170 against 167; 2,048:
-// 91 against 94; 8,192: 317 against 307).
+// k-groups and 6 in 1 do.  Longer grids run in 2 as fast as in 1 or faster (2048
+// x 1024: 2,048 rows of 8 groups 83 against 89, 4,096 153 against 158, 8,192 293
+// against 292, 16,384 569 against 559; 8,192 rows, 1024 x 2048: 284 against 298).
 template <bool BX, class E>
 hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStream_t s) {
     const int64_t M = a.g.M, some = M < a.g.E ? M : a.g.E, full = M / 32 + a.g.E / 2;
@@ -356,8 +361,7 @@ hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStre
     const int slabs = slabs_of<32>(a.K);              // a k-group should have one at least
     if (slabs >= 8 && quarters <= cus) return rows_tiles<32, 32, BX, 8, 1>(a, epi, s);
     if (slabs >= 8 && tiles <= cus) return rows_tiles<32, 64, BX, 4, 2>(a, epi, s);
-    if (slabs >= 4 && (tiles <= 3 * cus || (4 * tiles > 17 * cus && tiles < 14 * cus)))
-        return rows_tiles<32, 64, BX, 2, 2>(a, epi, s);
+    if (slabs >= 4 && (tiles <= 3 * cus || 4 * tiles > 17 * cus)) return rows_tiles<32, 64, BX, 2, 2>(a, epi, s);
     return rows_tiles<32, 64, BX, 1, 2>(a, epi, s);
 }
 

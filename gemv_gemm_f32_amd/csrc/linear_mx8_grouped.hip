@@ -46,12 +46,13 @@ struct PickedRow {
 template <int BM>
 __device__ __forceinline__ bool find_tile(const PackedGrouped &a, int bn, int most, GroupTile &t, int64_t &n0) {
     const Groups g{a.offsets, a.E, a.layer.M};
-    const int tiles_m = min(tiles_before<BM>(g, g.E), most), tiles_n = (a.layer.N + bn - 1) / bn;
-    const int64_t bid = group_number(), n = (int64_t)tiles_m * tiles_n;
+    GroupTiles<BM> tiles(g, most);
+    const int tiles_n = (a.layer.N + bn - 1) / bn;
+    const int64_t bid = group_number(), n = (int64_t)tiles.number * tiles_n;
     if (bid >= n) return false;
     const int tb = xcd_run((int)bid, (int)n);
-    t = tile_of_groups<BM>(g, tb % tiles_m);
-    n0 = (int64_t)(tb / tiles_m) * bn;
+    t = tiles[tb % tiles.number];
+    n0 = (int64_t)(tb / tiles.number) * bn;
     return true;
 }
 
