@@ -108,6 +108,35 @@ private:
     }
 };
 
+// Group number r (below E), or number r when of each 64 groups those of at
+// least four times `mean` rows come first, then those of at least twice and once
+// that and then the others: where the groups' work is as uneven as they are, the
+// long ones should not be the last to start.
+struct OneGroup {
+    int e, first, count;
+};
+__device__ __forceinline__ OneGroup group_at(const Groups &g, int r, bool by_size, int mean) {
+    int first, count;
+    if (!by_size) {
+        group_rows(g, r, first, count);
+        return {r, __builtin_amdgcn_readfirstlane(first), __builtin_amdgcn_readfirstlane(count)};
+    }
+    const int c = r & ~63, lane = threadIdx.x & 63;
+    group_rows(g, c + lane, first, count);
+    uint64_t among = __ballot(c + lane < g.E);
+    r -= c;
+#pragma unroll
+    for (int shift = 2; shift >= 0; --shift) {
+        const uint64_t large = among & __ballot(count >> shift >= mean);
+        const int n = __popcll(large);
+        among = r < n ? large : among & ~large;
+        r -= r < n ? 0 : n;
+    }
+    const int before = __builtin_amdgcn_mbcnt_hi((unsigned)(among >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)among, 0));
+    const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)(among & __ballot(before == r))) - 1);
+    return {c + l, __builtin_amdgcn_readlane(first, l), __builtin_amdgcn_readlane(count, l)};
+}
+
 // Workgroups in a grid of up to 65,535 x 2^20, and one's number.
 __device__ __forceinline__ int64_t group_number() {
     return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;

@@ -176,6 +176,7 @@ struct GroupedWeights {
     const int32_t *rows;
     float *C;
     int64_t lda, ldb, ldc, stridec;
+    bool by_size;                  // the largest groups first
 };
 
 template <int BM, int BN, int KS, int WPG, Pick PICK>
@@ -186,11 +187,8 @@ __global__ __launch_bounds__(64 * WPG * KS) void grouped_weights_kernel(GroupedW
     if (bid >= n) return;
     // every XCD takes a part of each expert: groups differ in size, so that an
     // expert per XCD would leave most of them waiting for the largest
-    const int e = (int)(bid / per), place = xcd_run((int)(bid % per), per);
-    int first, count;
-    group_rows(a.g, e, first, count);
-    first = __builtin_amdgcn_readfirstlane(first);
-    count = __builtin_amdgcn_readfirstlane(count);
+    const OneGroup g = group_at(a.g, (int)(bid / per), a.by_size, a.g.M / a.g.E);
+    const int e = g.e, first = g.first, count = g.count, place = xcd_run((int)(bid % per), per);
     if (count == 0 && epi.accumulate) return;
     const int lane = threadIdx.x & 63;
     const int wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WPG;
@@ -402,19 +400,26 @@ hipError_t weights_tiles(const GroupedWeights &a, const Store &epi, int64_t n, h
     return launch(grouped_weights_kernel<64, 64, KS, 4, PICK>, grid_of(n), dim3(256 * KS), s, a, epi);
 }
 
-// 64 x 64 tiles; their k-groups by the rows per group, which is how far a tile
-// walks, and by tiles per CU (us in 1 / 2 / 4 k-groups, 8 groups unless said):
-//   rows   768 x 768       1024 x 1024      2048 x 1024
-//   2048   50 / 62 / 58    74 / 77 / 79     107 / 112 / 141
-//   4096   92 / 94 / 82    132 / 123 / 114  204 / 181 / 212
-//   6144   140 / 124 / 107 175 / 168 / 147  278 / 251 / 277
-//   4096 rows of 32 groups, 1024 x 1024: 115 / 144 / 194
+// 64 x 64 tiles, four workgroups of which share a CU, the largest groups' first
+// (4096 rows in 8 groups of 36 to 1632, 2048 x 1024: 160 us, in the groups' order
+// 205); only where a CU has one or
+// two and they walk far, in 4 k-groups (us in 1 / 4, for groups of like size):
+//   4096 rows of one group, 768 x 768 (144 tiles)     104 / 83
+//   16384 of 2, 768 x 768 (288)                       323 / 290, 4096 of 2: 85 / 86
+//   65536 of 8, 512 x 512 (512)                       330 / 304
+//   1000 of 2, 2048 x 1024 (1,024)                    43 / 63,   8192 of 2: 288 / 300
+//   300 of 3, 230 x 230 (48)                          6.8 / 11.4
+// In 2 k-groups no size gained over the better of the two, and tiles of 128 x 64
+// and 128 x 128 took longer but in the largest products (16384 rows of 8, 2048 x
+// 1024: 573, 565 and 577).
 template <Pick PICK>
 hipError_t weights_product(const GroupedWeights &a, const Store &epi, int num_cus, hipStream_t s) {
     const int64_t per = (((int64_t)a.M + 63) / 64) * (((int64_t)a.N + 63) / 64), n = per * a.g.E;
     if (per > INT_MAX / a.g.E) return hipErrorInvalidConfiguration;
-    if (a.g.M / a.g.E < 320) return weights_tiles<1, PICK>(a, epi, n, s);
-    return n <= 8 * (int64_t)num_cus ? weights_tiles<4, PICK>(a, epi, n, s) : weights_tiles<2, PICK>(a, epi, n, s);
+    const int rows = a.g.M / a.g.E;
+    if ((n <= num_cus && rows >= 1024) || (n <= 2 * (int64_t)num_cus && rows >= 4096))
+        return weights_tiles<4, PICK>(a, epi, n, s);
+    return weights_tiles<1, PICK>(a, epi, n, s);
 }
 
 }  // namespace
@@ -458,8 +463,11 @@ hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hip
         if (e != hipSuccess) return e;
     }
     if (a.dW) {
-        GroupedWeights w{g, a.K, a.N, a.T, a.X, dZ, a.rows, a.dW, a.ldx, lddz, a.lddw, a.stridedw};
-        if (a.trans_w) w = {g, a.N, a.K, a.T, dZ, a.X, a.rows, a.dW, lddz, a.ldx, a.lddw, a.stridedw};
+        // finding the order takes 2 to 4% where groups are of like size (64 rows each of
+        // 64, 1024 x 1024: 143 against 137 us; 512 each of 8, 2048 x 1024: 162 / 161)
+        const bool by_size = a.M >= 128 * (int64_t)a.E;
+        GroupedWeights w{g, a.K, a.N, a.T, a.X, dZ, a.rows, a.dW, a.ldx, lddz, a.lddw, a.stridedw, by_size};
+        if (a.trans_w) w = {g, a.N, a.K, a.T, dZ, a.X, a.rows, a.dW, lddz, a.ldx, a.lddw, a.stridedw, by_size};
         const Store st{a.accumulate};
         e = !a.rows ? weights_product<NEITHER>(w, st, num_cus, s)
             : a.trans_w ? weights_product<PICK_B>(w, st, num_cus, s) : weights_product<PICK_A>(w, st, num_cus, s);

@@ -223,6 +223,29 @@ def test_bwd(M, N, K, E, trans_w, gather):
         _check_bwd(d, _bwd(d, act, trans_w), act, trans_w)
 
 
+def _lopsided(M, E, rng):
+    """Sizes from none to many times the mean, in no order."""
+    s = np.bincount(rng.choice(E, M, p=rng.dirichlet(np.full(E, 0.15))), minlength=E)
+    assert E < 8 or (s == 0).any() and s.max() >= 4 * M // E
+    return s.tolist()
+
+
+# groups of unlike size, whose gradients of the weights start with the largest:
+# few, as many as lanes, more; far walks of one or two tiles per CU
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("M,N,K,E", [(300, 70, 40, 2), (2000, 65, 130, 9), (8192, 40, 33, 64), (9000, 33, 20, 70),
+                                     (25700, 20, 24, 200), (2100, 70, 40, 2), (4200, 1100, 1000, 1)])
+def test_bwd_of_groups_of_unlike_size(M, N, K, E, gather):
+    for trans_w in (False, True):
+        d = _inputs(M, N, K, E, trans_w, gather)
+        d["offsets"] = er.sizes_to_offsets(_lopsided(M, E, np.random.default_rng([3, M, E])))
+        got = _bwd(d, "none", trans_w)
+        _check_bwd(d, got, "none", trans_w)
+        dW = torch().full(tuple(got[1].shape), 2.0, device="cuda")
+        _bwd(d, "none", trans_w, dW=dW, want=("dW",), accumulate=True)
+        assert np.array_equal(host(dW), host(got[1]) + np.float32(2))
+
+
 @pytest.mark.parametrize("act", ["none", "silu"])
 @pytest.mark.parametrize("trans_w", [False, True])
 def test_bwd_of_what_is_wanted_and_accumulated(act, trans_w):
