@@ -12,6 +12,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "wave.hpp"
 
 namespace gg {
@@ -25,6 +27,15 @@ struct Groups {
 inline int64_t tiles_most(int64_t M, int64_t E, int64_t BM) {
     const int64_t n = (M + E * (BM - 1)) / BM;
     return n < M ? n : M;
+}
+
+// And how many they are likely to need: one for each group that holds any, which
+// rows on groups at random leave, or a half-empty one for each beside the full
+// tiles.
+inline int64_t tiles_likely(int64_t M, int64_t E, int64_t BM) {
+    const int64_t some = E ? (int64_t)std::ceil((double)E * -std::expm1(-(double)M / (double)E)) : 0;
+    const int64_t full = M / BM + some / 2;
+    return some > full ? some : full;
 }
 
 // The rows of group e, for e < E; none for others.  Whatever the offsets hold,

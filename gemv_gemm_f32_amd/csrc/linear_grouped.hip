@@ -330,15 +330,13 @@ hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
     return launch(grouped_few_kernel<MB, BX, KW, ROWS>, grid_of(n), dim3(64 * KW * ROWS), s, a, epi, (int)most);
 }
 
-// The tile of a product of grouped rows.  How many tiles there will be is only
-// guessed here (groups of like size): one per group that can hold a row, or a
-// half-empty one per group beside the full ones.  Tiles of 32 rows throughout:
-// a group leaves 16 rows of its last tile empty on average, with 64 rows 32, and
-// the last round of tiles is shorter.  (2048 x 1024, us in 32 x 64 against 64 x
-// 64, both in 2 k-groups, for groups of like, not the same size: 2,048 rows of 8
-// groups 83 / 89, 4,096 153 / 157, 8,192 of 8 293 / 295, of 64 351 / 378, of one
-// 286 / 279.)  The k-groups by how many tiles a CU holds at once (us, K = 768,
-// groups of like size):
+// The tile of a product of grouped rows, by how many there are likely to be.
+// Tiles of 32 rows throughout: a group leaves 16 rows of its last tile empty on
+// average, with 64 rows 32, and the last round of tiles is shorter.  (2048 x 1024,
+// us in 32 x 64 against 64 x 64, both in 2 k-groups, for groups of like, not the
+// same size: 2,048 rows of 8 groups 83 / 89, 4,096 153 / 157, 8,192 of 8 293 / 295,
+// of 64 351 / 378, of one 286 / 279.)  The k-groups by how many tiles a CU holds at
+// once (us, K = 768, groups of like size):
 //
 //   rows, groups, N    32 x 64 in 1   in 2   in 4   32 x 32 in 8
 //     64,  8,  768         21.1       14.4   13.3       10.2
@@ -346,6 +344,8 @@ hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
 //    256,  8, 2304         32.9       22.7   25.8       32.5
 //    768,  8, 2304         35.7       43.1   46.0       59.6
 //   1536, 32,  768         35.2       37.6   45.7       53.1
+//     64, 128, 768         29.9       25.9   34.8       46.1
+//    128, 128, 768         33.0       41.0   48.2       63.9
 //
 // One 32 x 32 tile in 8 k-groups, or one 32 x 64 in 4, fills a CU's LDS; 3 in 2
 // k-groups and 6 in 1 do.  Longer grids run in 2 as fast as in 1 or faster (2048
@@ -353,13 +353,12 @@ hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
 // against 292, 16,384 569 against 559; 8,192 rows, 1024 x 2048: 284 against 298).
 template <bool BX, class E>
 hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStream_t s) {
-    const int64_t M = a.g.M, some = M < a.g.E ? M : a.g.E, full = M / 32 + a.g.E / 2;
-    const int64_t rows = some > full ? some : full, cus = num_cus;
+    const int64_t rows = tiles_likely(a.g.M, a.g.E, 32), cus = num_cus;
     const int64_t quarters = rows * (((int64_t)a.N + 31) / 32), tiles = rows * (((int64_t)a.N + 63) / 64);
     const int slabs = slabs_of<32>(a.K);              // a k-group should have one at least
     if (slabs >= 8 && quarters <= cus) return rows_tiles<32, 32, BX, 8, 1>(a, epi, s);
     if (slabs >= 8 && tiles <= cus) return rows_tiles<32, 64, BX, 4, 2>(a, epi, s);
-    if (slabs >= 4 && (tiles <= 3 * cus || 4 * tiles > 17 * cus)) return rows_tiles<32, 64, BX, 2, 2>(a, epi, s);
+    if (slabs >= 4 && (tiles <= 3 * cus || 4 * tiles > 19 * cus)) return rows_tiles<32, 64, BX, 2, 2>(a, epi, s);
     return rows_tiles<32, 64, BX, 1, 2>(a, epi, s);
 }
 

@@ -135,10 +135,7 @@ hipError_t launch_wide(const PackedGrouped &a, hipStream_t s) {
 template <int BITS>
 hipError_t launch_bits(const PackedGrouped &a, int num_cus, hipStream_t s) {
     const int64_t M = a.layer.M, E = a.E, N = a.layer.N, cus = num_cus;
-    const auto tiles = [&](int bm, int bn) {
-        const int64_t some = M < E ? M : E, full = M / bm + E / 2;
-        return (some > full ? some : full) * ((N + bn - 1) / bn);
-    };
+    const auto tiles = [&](int bm, int bn) { return tiles_likely(M, E, bm) * ((N + bn - 1) / bn); };
     const bool lengthy = a.layer.K >= 4096;
     const int64_t sixteens = tiles(16, 16);
     if (M <= 8 * E && sixteens <= 16 * cus) {
