@@ -112,20 +112,23 @@ hipError_t launch_wide(const PackedGrouped &a, hipStream_t s) {
     return launch_tiles(packed_wide_grouped<BM, NW, BITS, MW>, a, BM, 32 * NW, 64 * NW, s);
 }
 
-// The shape by what the groups' sizes are likely to be (rows / groups each) and by
-// how many tiles that makes (2 bits, us):
-//  - up to 8 rows per group in at most 16 tiles of 16 x 16 per CU: the kernel of
-//    few rows. 8 rows of 64 groups, 1536 x 1536: 7.5, in 32 x 128 tiles 12.5; 64 of
-//    16, 2048 x 4096: 22.0 / 26.9; but 8 of 64, 12288 x 1536: 25.1 / 23.7, and 128
-//    of 64, 1536 x 1536: 18.5 / 17.2.  Its runs of k: 4 for up to 4 tiles per CU (8
-//    rows of 64 groups: 7.5, 8.0 in 2, 8.5 in 1, 8.2 in 8), more for long rows where
-//    there is a tile per CU (2 rows, 1536 x 12288: 11.2 in 16, 12.4 in 4), else 1 (64
-//    rows of 16 groups, 2048 x 4096: 22.0 / 22.9 in 4; 32 of 64: 11.2 / 11.8), or 2
-//    with an output in 8 bits.
-//  - long rows and up to 6 cells of 32 x 32 per CU: a wave per run of k in each (400
-//    rows of 16 groups, 2048 x 4096: 28.6, 33.6 in 32 x 128, 36.3 in 64 x 128).
-//  - less than 16 rows per group: 32 x 128 (128 rows of 16 groups, 12288 x 1536:
-//    39.0, in 64 x 128 45.1).
+// The shape by the rows per group and by how many tiles there are likely to be (us,
+// 2 bits; 4 bits ask for the same):
+//  - few rows per group: the kernel of few rows.  Where rows of W are short, that is
+//    up to 8 in up to 12 tiles of 16 x 16 per CU (8 rows of 64 groups, 1536 x 1536:
+//    5.2, in 32 x 128 tiles 10.3; 64 of 64, 15 per CU: 16.0 / 14.9); where they are
+//    long, up to 4 (64 of 64, 1536 x 12288: 82 / 90; 256 of 32, 1536 x 8192: 62, in
+//    32 x 32 cells 53) or, in a tile per CU, 16 (16 rows, 4096 x 4096: 6.7 / 9.0).  A
+//    tile's k in 4 runs, but 16 (8 with an output in 8 bits) for long rows and a
+//    tile per CU (8 rows, 4096 x 4096: 5.9 / 6.2 in 4) and 1 (2) for short ones and
+//    many tiles (32 of 16, 2304 x 768: 7.1 / 7.6 in 4; but 16 of 16, 1536 x 1536: 6.8
+//    / 5.8).
+//  - up to 8 cells of 32 x 32 per CU and long rows, 4 and 1536 columns: a wave per run
+//    of k in each (256 rows of 8 groups, 1536 x 12288: 45, in 32 x 128 66; 512 of 16,
+//    4096 x 4096, 12 per CU: 58 / 54; 256 of 16, 1536 x 1536: 9.4 / 10.6).
+//  - less than 16 rows per group, or up to 2.5 tiles of 64 x 128 per CU: 32 x 128 (1024
+//    rows of 32 groups, 2304 x 2304: 28, in 64 x 128 38; 512 of 16, 2304 x 768: 9.7 /
+//    13.6; 512 of 16, 4096 x 4096: 54 / 50).
 //  - 128 x 256 for large groups and products (4,096 rows of 8 groups, 4096 x 4096:
 //    201 / 217 at 4 bits, 210 / 234 in 64 x 128).
 //  - else 64 x 128, a last tile of up to 32 rows as 32 x 128 (1,000 rows of 16 groups,
@@ -134,20 +137,23 @@ hipError_t launch_wide(const PackedGrouped &a, hipStream_t s) {
 //    and its order is better (4 bits: 84 against 86).
 template <int BITS>
 hipError_t launch_bits(const PackedGrouped &a, int num_cus, hipStream_t s) {
-    const int64_t M = a.layer.M, E = a.E, N = a.layer.N, cus = num_cus;
+    const int64_t M = a.layer.M, E = a.E, N = a.layer.N, K = a.layer.K, cus = num_cus;
     const auto tiles = [&](int bm, int bn) { return tiles_likely(M, E, bm) * ((N + bn - 1) / bn); };
-    const bool lengthy = a.layer.K >= 4096;
+    const bool lengthy = K >= 4096;
     const int64_t sixteens = tiles(16, 16);
-    if (M <= 8 * E && sixteens <= 16 * cus) {
-        if (a.layer.Y8) {
-            if (sixteens > 4 * cus) return launch_rows<BITS, 2, 2>(a, s);
-            return lengthy && sixteens <= cus ? launch_rows<BITS, 2, 8>(a, s) : launch_rows<BITS, 2, 4>(a, s);
-        }
-        if (sixteens > 4 * cus) return launch_rows<BITS, 1, 1>(a, s);
-        return lengthy && sixteens <= cus ? launch_rows<BITS, 1, 16>(a, s) : launch_rows<BITS, 1, 4>(a, s);
+    // (4,096 per CU is out of reach but for huge outputs, which need a grid of larger tiles)
+    const bool few = lengthy ? (M <= 4 * E && sixteens <= 4096 * cus) || (M <= 16 * E && sixteens <= cus)
+                             : M <= 8 * E && sixteens <= 12 * cus;
+    if (few) {
+        const bool one_run = K < 1536 && sixteens > 4 * cus, most_runs = lengthy && sixteens <= cus;
+        if (a.layer.Y8)
+            return one_run ? launch_rows<BITS, 2, 2>(a, s)
+                   : most_runs ? launch_rows<BITS, 2, 8>(a, s) : launch_rows<BITS, 2, 4>(a, s);
+        return one_run ? launch_rows<BITS, 1, 1>(a, s)
+               : most_runs ? launch_rows<BITS, 1, 16>(a, s) : launch_rows<BITS, 1, 4>(a, s);
     }
-    if (a.layer.K >= 2048 && tiles(32, 32) <= 6 * cus) return launch_block<4, BITS, 3>(a, s);
-    if (M < 16 * E) return launch_wide<32, 4, BITS, 3>(a, s);
+    if (K >= 1536 && tiles(32, 32) <= (lengthy ? 8 : 4) * cus) return launch_block<4, BITS, 3>(a, s);
+    if (M < 16 * E || 2 * tiles(64, 128) <= 5 * cus) return launch_wide<32, 4, BITS, 3>(a, s);
     if (M >= 256 * E && tiles(128, 256) >= 2 * cus) return launch_wide<128, 8, BITS, 2>(a, s);
     return launch_wide<64, 4, BITS, 2>(a, s);
 }

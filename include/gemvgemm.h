@@ -525,7 +525,7 @@ int expert_combine_bwd(int64_t T, int64_t k, int64_t M, int64_t K, const float *
  * Limits: leading dimensions of X and W up to 2^22; with rows, the T rows of X
  * within 2 GiB (else GG_ERR_INVALID_ARG); and fewer than 2^31 tiles of 32 x 32
  * ((M / 32 + E) * ceil(N / 32)).  Accuracy and non-finite inputs as linear_f32;
- * results do not depend on the sizes of other groups.
+ * for the same M, N, K and E, results do not depend on the sizes of other groups.
  */
 int linear_f32_grouped(int trans_w, int act, int64_t M, int64_t N, int64_t K, int64_t E, int64_t T,
                        const float *X, int64_t ldx, const int32_t *rows, const int32_t *offsets,

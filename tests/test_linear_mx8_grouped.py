@@ -69,6 +69,28 @@ def test_shapes(bits, M, N, K, E, gather):
         lr.within(host(Y), y, e, kind)
 
 
+# one for each way the tiles are laid out: few rows with their k in 1, 4 and 16 (2, 4
+# and 8) parts, cells of 32 x 32, and 32 to 128 rows by 128 or 256 columns
+WAYS = [(30, 1200, 200, 30), (9, 210, 700, 3), (3, 300, 4200, 2), (100, 130, 1600, 3), (90, 100, 4170, 2),
+        (60, 300, 130, 2), (700, 2100, 130, 40), (2100, 7000, 96, 8)]
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("M,N,K,E", WAYS)
+def test_ways(bits, M, N, K, E, gather):
+    for kind in ("ragged", "even"):
+        d = _inputs(bits, M, N, K, E, gather, kind)
+        kw = dict(rows=_d(d["rows"]), bias=dev(d["b"]), act="relu")
+        Y = FN[bits](*_args(d), **kw)
+        y, e = _ref(bits, d, "relu")
+        lr.within(host(Y), y, e, kind)
+        Y, Y8, YE = FN[bits](*_args(d), **kw, out="both")
+        lr.within(host(Y), y, e, kind)
+        q, ee = lr.to_mx8(host(Y).astype(np.float64))
+        assert np.array_equal(host(YE), ee) and np.array_equal(host(Y8), q), "bytes of Y itself"
+
+
 @pytest.mark.parametrize("bits", [2, 4])
 @pytest.mark.parametrize("act", lr.ACTS)
 @pytest.mark.parametrize("M", [4, 60, 300])
