@@ -74,7 +74,7 @@ struct PickedSlabs {
 
 // C = acc, or C += acc.
 struct Store {
-    bool accumulate;
+    int accumulate;      // (a bool would be kept in scratch memory)
 
     template <int N>
     struct Fetched {};
@@ -457,8 +457,8 @@ hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hip
     }
     if (a.dX) {
         const GroupedRows r{g, a.K, a.N, 0, dZ, a.W, nullptr, a.dX, lddz, a.ldw, a.stridew, a.lddx, 0};
-        e = a.trans_w ? rows_product<false>(r, Store{false}, num_cus, s)
-                      : rows_product<true>(r, Store{false}, num_cus, s);
+        e = a.trans_w ? rows_product<false>(r, Store{0}, num_cus, s)
+                      : rows_product<true>(r, Store{0}, num_cus, s);
         if (e != hipSuccess) return e;
     }
     if (a.dW) {
@@ -467,7 +467,7 @@ hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hip
         const bool by_size = a.M >= 128 * (int64_t)a.E;
         GroupedWeights w{g, a.K, a.N, a.T, a.X, dZ, a.rows, a.dW, a.ldx, lddz, a.lddw, a.stridedw, by_size};
         if (a.trans_w) w = {g, a.N, a.K, a.T, dZ, a.X, a.rows, a.dW, lddz, a.ldx, a.lddw, a.stridedw, by_size};
-        const Store st{a.accumulate};
+        const Store st{a.accumulate ? 1 : 0};
         e = !a.rows ? weights_product<NEITHER>(w, st, num_cus, s)
             : a.trans_w ? weights_product<PICK_B>(w, st, num_cus, s) : weights_product<PICK_A>(w, st, num_cus, s);
     }
