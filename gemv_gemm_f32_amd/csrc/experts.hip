@@ -25,7 +25,7 @@ typedef v4f v4f_any __attribute__((aligned(4)));   // rows may start at any floa
 // scattered stores of rows, a cache line per lane, and are spread over
 // workgroups: one launch counts each workgroup's experts into rows (all of which
 // the last launch writes), a second finds the places, and a third writes rows.
-// (8,192 tokens, 8 of 128 experts: 64.8 us in one workgroup of 16 waves, 14.1 in
+// (8,192 tokens, 8 of 128 experts: 57.5 us in one workgroup of 16 waves, 12.5 in
 // 64; 1,024 tokens, 8 of 64: one workgroup.)
 struct Entries {
     const ExpertGroups &a;
@@ -350,12 +350,16 @@ hipError_t launch_expert_groups(const ExpertGroups &a, hipStream_t s) {
     int bits = 0;
     while (a.E >> bits) ++bits;                       // keys up to E
     const int64_t n = (int64_t)a.T * a.k;
-    // one wave needs no barriers: the better choice for the few entries of
-    // generated tokens
-    if (n <= 512) return launch(expert_groups_kernel<1>, dim3(1), dim3(64), s, a, bits);
-    // workgroups of at least 1,024 entries, as many as their counts fit into rows
-    const int64_t room = n / (a.E + 1), most = n / 1024;
-    const int64_t groups = room < most ? (room < 256 ? room : 256) : (most < 256 ? most : 256);
+    // one workgroup: of four waves for the few entries of generated tokens (8
+    // entries of 64 experts 3.1 us, on 16 waves 3.8; 512 3.8 / 4.2; 768 4.2 / 4.3)
+    if (n <= 768) return launch(expert_groups_kernel<4>, dim3(1), dim3(256), s, a, bits);
+    // or several, of 1,024 entries and more, as many as their counts fit into rows,
+    // where there are 8 at least (8192 entries of 64 experts 9.5 us, 10.2 in one; 4096
+    // 10.2 / 7.2); each reads the counts of all, so up to 128, or one per 4,096
+    // entries (262,144 of 256 experts: 22.4, in 64 23.4, in 256 28.3; 1,048,576 of 128:
+    // 35.3 in 256, in 128 40.4)
+    const int64_t room = n / (a.E + 1), cap = n >= 4096 * 256 ? 256 : n >= 4096 * 128 ? n / 4096 : 128;
+    const int64_t most = n / 1024 < cap ? n / 1024 : cap, groups = room < most ? room : most;
     if (groups < 8) return launch(expert_groups_kernel<16>, dim3(1), dim3(1024), s, a, bits);
     const unsigned per = (unsigned)(((n + groups - 1) / groups + 64 * PW - 1) / (64 * PW) * (64 * PW));
     const unsigned grid = (unsigned)((n + per - 1) / per);

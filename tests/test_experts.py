@@ -54,6 +54,13 @@ def test_groups_of_one_expert(T, one):
     assert np.array_equal(rows, np.arange(2 * T) // 2) and np.array_equal(pos.reshape(-1), np.arange(2 * T))
 
 
+# either side of where more waves and more workgroups take over
+@pytest.mark.parametrize("T,k,E", [(767, 1, 64), (768, 1, 64), (769, 1, 64), (8191, 1, 7), (8192, 1, 7), (8193, 1, 1000),
+                                   (65536, 2, 256), (131072, 4, 64), (131073, 5, 3), (262147, 4, 1024)])
+def test_groups_by_workgroups(T, k, E):
+    test_groups(T, k, E, 0.1)
+
+
 @pytest.mark.parametrize("T,k", [(9, 3), (700, 5)])
 def test_groups_strides_and_what_lies_around(T, k):
     t = torch()
