@@ -53,15 +53,17 @@ __host__ __device__ inline void group_rows(const Groups &g, int e, int &first, i
 template <int BM>
 __device__ __forceinline__ int tiles_in(int count) { return count / BM + (count % BM != 0); }
 
-// Tiles of all groups, and, with `upto` groups, of the first ones.
+// Tiles of the first `upto` groups, of 128 rows or so: 64 groups' then fit 32
+// bits even where offsets that are not in order count rows more than once.
 template <int BM>
-__device__ __forceinline__ int tiles_before(const Groups &g, int upto) {
+__device__ __forceinline__ int64_t tiles_before(const Groups &g, int upto) {
+    static_assert(BM >= 64, "64 groups of 2^31 rows");
     const int lane = threadIdx.x & 63;
-    int sum = 0;
+    int64_t sum = 0;
     for (int c = 0; c < upto; c += 64) {
         int first, count;
         group_rows(g, c + lane < upto ? c + lane : g.E, first, count);
-        sum += __builtin_amdgcn_readlane(wave64_scan(tiles_in<BM>(count)), 63);
+        sum += (unsigned)__builtin_amdgcn_readlane(wave64_scan(tiles_in<BM>(count)), 63);
     }
     return sum;
 }

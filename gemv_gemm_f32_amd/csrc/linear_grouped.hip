@@ -291,10 +291,10 @@ __global__ __launch_bounds__(512) void grouped_bias_kernel(Groups g, int N, cons
     const int64_t blocks = ((int64_t)N + 63) / 64, bid = group_number();
     if (bid >= blocks * g.E) return;
     const int e = (int)(bid / blocks);
-    const int from = min(tiles_before<DZ_ROWS>(g, e), most);
+    const int from = (int)min(tiles_before<DZ_ROWS>(g, e), (int64_t)most);
     int first, count;
     group_rows(g, e, first, count);
-    const int end = min(from + tiles_in<DZ_ROWS>(count), most);
+    const int end = (int)min((int64_t)from + tiles_in<DZ_ROWS>(count), (int64_t)most);
     const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
     const int64_t col = bid % blocks * 64 + tx;
     float sum = 0.f;

@@ -318,6 +318,23 @@ def test_gradients_against_differences():
 
 # ------------------------------------------------------------ large places --
 
+def test_offsets_that_count_rows_too_often():
+    """Groups out of order whose tiles, counted together, pass 2^31: nothing
+    outside of the operands is read for their sums, and offsets in order give
+    theirs afterwards."""
+    t = torch()
+    M, E = 2 ** 29 + 128, 1024
+    dY = t.zeros((M, 1), device="cuda")
+    dY[5], dY[M - 1] = 3.0, 4.0
+    X, W = t.empty((M, 0), device="cuda"), t.empty((E, 0, 1), device="cuda")
+    ws = t.empty(bd.linear_f32_grouped_bwd_ws_size("none", M, 1, E), dtype=t.uint8, device="cuda")
+    o = t.tensor([0, M] * (E // 2) + [0], dtype=t.int32, device="cuda")
+    bd.linear_f32_grouped_bwd(dY, X, W, o, want=("db",), workspace=ws)
+    o = t.tensor([0] + [6] * (E - 1) + [M], dtype=t.int32, device="cuda")
+    db = bd.linear_f32_grouped_bwd(dY, X, W, o, want=("db",), workspace=ws)[2]
+    assert db[0, 0] == 3 and db[E - 1, 0] == 4 and not host(db)[1:-1].any()
+
+
 def test_places_past_32_bit_offsets():
     """Experts 2^31 floats apart, rows at the widest leading dimension, and
     outputs whose rows lie past 2^31 floats."""
