@@ -940,7 +940,7 @@ def _packed_grouped(name, bits, X8, XE, Q, S, offsets, rows, bias, act, Y, Y8, Y
     pb, ldb = _arg(bias, (E, N), f32, "bias", dev)
     py = ldy = p8 = ldy8 = pye = ldye = 0
     if out != "mx8":
-        Y, py, ldy = _out(Y, (M, N), f32, "Y", dev, X8, stream)
+        Y, py, ldy = _out(Y, (M, N), f32, "Y", dev, X8 if bias is None else bias, stream)
     if out != "f32":
         Y8, p8, ldy8 = _out(_bytes(Y8), (M, N), u8, "Y8", dev, X8, stream)
         YE, pye, ldye = _out(_bytes(YE), (M, -(-N // 32)), u8, "YE", dev, X8, stream)
@@ -1020,7 +1020,7 @@ def block_norm_mx8(U, X, gamma_u=None, gamma_s=None, eps=1e-5, gate=None, alpha=
     pg, ldg = _gate(gate, M, K, dev)
     S, ps, lds = _out(S, (M, K), f32, "S", dev, U, stream)
     Q, pq, ldq = _out(_bytes(Q), (M, K), u8, "Q", dev, U, stream)
-    E, pe, lde = _out(_bytes(E), (M, -(-K // 32)), u8, "E", dev, U, stream)
+    E, pe, lde = _out(_bytes(E), (M, -(-K // 32)), u8, "E", dev, Q, stream)
     _check(load().block_norm_mx8(M, K, pu, ldu, px, ldx, pgu, pg, ldg, float(alpha), pgs, float(eps), ps,
                                  lds, pq, ldq, pe, lde, _stream(stream, dev)), "block_norm_mx8")
     return Q, E, S
