@@ -72,6 +72,35 @@ struct PickedSlabs {
     }
 };
 
+// A tile's rows of an output, one float of each row per lane: buffer accesses,
+// which leave out what lies behind the last row by themselves.  (With a branch and
+// a 64-bit address for each row tiles spent a tenth of their time storing.)
+constexpr int64_t NEAR_LD = 1 << 22;                  // 64 such rows are 1 GiB
+struct TileRows {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __amdgpu_buffer_rsrc_t rsrc;
+#endif
+    unsigned ld;         // bytes
+    __device__ __forceinline__ TileRows(float *C, int64_t ldc, int rows) : ld((unsigned)ldc * 4) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(C, (short)0, (int)(min(rows, 64) * ld), 0x00020000);
+#endif
+    }
+    __device__ __forceinline__ unsigned at(int row, int col) const { return (unsigned)row * ld + 4 * (unsigned)col; }
+    __device__ __forceinline__ void store(unsigned at, float x) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), rsrc, at, 0, 0);
+#endif
+    }
+    __device__ __forceinline__ float load(unsigned at) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0));
+#else
+        return 0.f;
+#endif
+    }
+};
+
 // C = acc, or C += acc.
 struct Store {
     int accumulate;      // (a bool would be kept in scratch memory)
@@ -83,6 +112,66 @@ struct Store {
     template <int NS, class Acc, class Row, class Mine>
     __device__ __forceinline__ void block(const Acc &acc, const Fetched<NS> &, int col, int M,
                                           float *C, int64_t ldc, Row row, Mine mine) const {
+        const TileRows c(C, ldc, M);
+        const unsigned first = c.at(row(0), col);
+        if (accumulate) {
+            float old[NS];
+#pragma unroll
+            for (int r = 0; r < NS; ++r) old[r] = mine(r) ? c.load(first + c.at(row(r) - row(0), 0)) : 0.f;
+#pragma unroll
+            for (int r = 0; r < NS; ++r)
+                if (mine(r)) c.store(first + c.at(row(r) - row(0), 0), old[r] + acc[r]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < NS; ++r)
+                if (mine(r)) c.store(first + c.at(row(r) - row(0), 0), acc[r]);
+        }
+    }
+};
+
+// Z = acc + bias (unless NULL), C = act(Z).
+struct TileLayer {
+    const float *bias;   // NULL: none
+    float *Z;
+    int64_t ldz;
+    int act;
+
+    template <int N>
+    struct Fetched {
+        float bias;
+    };
+    template <int NS, class Row, class Mine>
+    __device__ __forceinline__ void fetch(Fetched<NS> &f, int col, int, int N, Row, Mine) const {
+        f.bias = bias && col < N ? bias[col] : 0.f;
+    }
+    template <int NS, class Acc, class Row, class Mine>
+    __device__ __forceinline__ void block(const Acc &acc, const Fetched<NS> &f, int col, int M,
+                                          float *C, int64_t ldc, Row row, Mine mine) const {
+        float z[NS];
+#pragma unroll
+        for (int r = 0; r < NS; ++r) z[r] = acc[r] + f.bias;
+        if (Z) {
+            const TileRows kept(Z, ldz, M);
+            const unsigned first = kept.at(row(0), col);
+#pragma unroll
+            for (int r = 0; r < NS; ++r)
+                if (mine(r)) kept.store(first + kept.at(row(r) - row(0), 0), z[r]);
+        }
+        const TileRows c(C, ldc, M);
+        const unsigned first = c.at(row(0), col);
+        with_act(act, [&](auto a) {
+#pragma unroll
+            for (int r = 0; r < NS; ++r)
+                if (mine(r)) c.store(first + c.at(row(r) - row(0), 0), act_value<decltype(a)::value>(z[r]));
+        });
+    }
+};
+
+// The same for outputs whose rows lie further apart.
+struct FarStore : Store {
+    template <int NS, class Acc, class Row, class Mine>
+    __device__ __forceinline__ void block(const Acc &acc, const Fetched<NS> &, int col, int M,
+                                          float *C, int64_t ldc, Row row, Mine mine) const {
 #pragma unroll
         for (int r = 0; r < NS; ++r) {
             if (!mine(r) || row(r) >= M) continue;
@@ -91,14 +180,23 @@ struct Store {
         }
     }
 };
+struct FarLayer : Layer {};
 
 // The epilogue of a group's tile at (row, n) of the output, with the group's
 // bias `bias` floats on.
 __device__ __forceinline__ Store at_tile(const Store &s, int64_t, int64_t, int64_t) { return s; }
-__device__ __forceinline__ Layer at_tile(const Layer &l, int64_t bias, int64_t row, int64_t n) {
-    return {l.bias ? l.bias + bias + n : nullptr, nullptr, 0,
-            l.Z ? l.Z + row * l.ldz + n : nullptr, l.ldz, l.act};
+__device__ __forceinline__ TileLayer at_tile(const Layer &l, int64_t bias, int64_t row, int64_t n) {
+    return {l.bias ? l.bias + bias + n : nullptr, l.Z ? l.Z + row * l.ldz + n : nullptr, l.ldz, l.act};
 }
+__device__ __forceinline__ FarStore at_tile(const FarStore &s, int64_t, int64_t, int64_t) { return s; }
+__device__ __forceinline__ Layer at_tile(const FarLayer &l, int64_t bias, int64_t row, int64_t n) {
+    const TileLayer t = at_tile(static_cast<const Layer &>(l), bias, row, n);
+    return {t.bias, nullptr, 0, t.Z, t.ldz, t.act};
+}
+inline FarStore far(const Store &s) { return {s}; }
+inline FarLayer far(const Layer &l) { return {l}; }
+inline bool is_far(const Store &, int64_t ldc) { return ldc > NEAR_LD; }
+inline bool is_far(const Layer &l, int64_t ldc) { return ldc > NEAR_LD || l.ldz > NEAR_LD; }
 
 // Rows of a grouped product: C_i = A[rows_i] . B_e.
 struct GroupedRows {
@@ -160,7 +258,8 @@ __global__ __launch_bounds__(64 * KW * ROWS) void grouped_few_kernel(GroupedRows
         return A + (rows ? (int64_t)min((unsigned)rows[m], (unsigned)a.T - 1) : (int64_t)m) * a.lda;
     };
     const float *W = a.B + t.e * a.strideb;
-    const Layer e = at_tile(epi, t.e * a.ldbias, t.row, 0);
+    const TileLayer l = at_tile(epi, t.e * a.ldbias, t.row, 0);
+    const Layer e{l.bias, nullptr, 0, l.Z, l.ldz, l.act};
     float *Y = a.C + t.row * a.ldc;
     if constexpr (BX) few_nk<MB, KW, ROWS>(left, a.N, a.K, x, W, a.ldb, Y, a.ldc, e, n0);
     else few_kn<MB, KW>(left, a.N, a.K, x, W, a.ldb, Y, a.ldc, e, n0);
@@ -179,8 +278,8 @@ struct GroupedWeights {
     bool by_size;                  // the largest groups first
 };
 
-template <int BM, int BN, int KS, int WPG, Pick PICK>
-__global__ __launch_bounds__(64 * WPG * KS) void grouped_weights_kernel(GroupedWeights a, Store epi) {
+template <int BM, int BN, int KS, int WPG, Pick PICK, class E>
+__global__ __launch_bounds__(64 * WPG * KS) void grouped_weights_kernel(GroupedWeights a, E epi) {
     using S = TileShape<BM, BN, false, false, KS, WPG, false, 32>;
     const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN, per = tiles_m * tiles_n;
     const int64_t bid = group_number(), n = (int64_t)per * a.g.E;
@@ -356,6 +455,7 @@ hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStre
     const int64_t rows = tiles_likely(a.g.M, a.g.E, 32), cus = num_cus;
     const int64_t quarters = rows * (((int64_t)a.N + 31) / 32), tiles = rows * (((int64_t)a.N + 63) / 64);
     const int slabs = slabs_of<32>(a.K);              // a k-group should have one at least
+    if (is_far(epi, a.ldc)) return rows_tiles<32, 64, BX, 1, 2>(a, far(epi), s);
     if (slabs >= 8 && quarters <= cus) return rows_tiles<32, 32, BX, 8, 1>(a, epi, s);
     if (slabs >= 8 && tiles <= cus) return rows_tiles<32, 64, BX, 4, 2>(a, epi, s);
     if (slabs >= 4 && (tiles <= 3 * cus || 4 * tiles > 19 * cus)) return rows_tiles<32, 64, BX, 2, 2>(a, epi, s);
@@ -394,9 +494,9 @@ hipError_t layer_product(const GroupedRows &a, const Layer &epi, int num_cus, hi
     return few_rows(a, BX) ? few_product<BX>(a, epi, num_cus, s) : rows_product<BX>(a, epi, num_cus, s);
 }
 
-template <int KS, Pick PICK>
-hipError_t weights_tiles(const GroupedWeights &a, const Store &epi, int64_t n, hipStream_t s) {
-    return launch(grouped_weights_kernel<64, 64, KS, 4, PICK>, grid_of(n), dim3(256 * KS), s, a, epi);
+template <int KS, Pick PICK, class E>
+hipError_t weights_tiles(const GroupedWeights &a, const E &epi, int64_t n, hipStream_t s) {
+    return launch(grouped_weights_kernel<64, 64, KS, 4, PICK, E>, grid_of(n), dim3(256 * KS), s, a, epi);
 }
 
 // 64 x 64 tiles, four workgroups of which share a CU, the largest groups' first
@@ -416,6 +516,7 @@ hipError_t weights_product(const GroupedWeights &a, const Store &epi, int num_cu
     const int64_t per = (((int64_t)a.M + 63) / 64) * (((int64_t)a.N + 63) / 64), n = per * a.g.E;
     if (per > INT_MAX / a.g.E) return hipErrorInvalidConfiguration;
     const int rows = a.g.M / a.g.E;
+    if (is_far(epi, a.ldc)) return weights_tiles<1, PICK>(a, far(epi), n, s);
     if ((n <= num_cus && rows >= 1024) || (n <= 2 * (int64_t)num_cus && rows >= 4096))
         return weights_tiles<4, PICK>(a, epi, n, s);
     return weights_tiles<1, PICK>(a, epi, n, s);
