@@ -433,8 +433,8 @@ hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
 // Tiles of 32 rows throughout: a group leaves 16 rows of its last tile empty on
 // average, with 64 rows 32, and the last round of tiles is shorter.  (2048 x 1024,
 // us in 32 x 64 against 64 x 64, both in 2 k-groups, for groups of like, not the
-// same size: 2,048 rows of 8 groups 83 / 89, 4,096 153 / 157, 8,192 of 8 293 / 295,
-// of 64 351 / 378, of one 286 / 279.)  The k-groups by how many tiles a CU holds at
+// same size: 2,048 rows of 8 groups 83 / 89, 4,096 153 / 157, 8,192 of 8 284 / 290,
+// of 64 342 / 375, of one 286 / 279.)  The k-groups by how many tiles a CU holds at
 // once (us, K = 768, groups of like size):
 //
 //   rows, groups, N    32 x 64 in 1   in 2   in 4   32 x 32 in 8
@@ -447,9 +447,10 @@ hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
 //    128, 128, 768         33.0       41.0   48.2       63.9
 //
 // One 32 x 32 tile in 8 k-groups, or one 32 x 64 in 4, fills a CU's LDS; 3 in 2
-// k-groups and 6 in 1 do.  Longer grids run in 2 as fast as in 1 or faster (2048
-// x 1024: 2,048 rows of 8 groups 83 against 89, 4,096 153 against 158, 8,192 293
-// against 292, 16,384 569 against 559; 8,192 rows, 1024 x 2048: 284 against 298).
+// k-groups and 6 in 1 do.  Longer grids run in 2 as fast as in 1 or faster where K
+// is long enough for its tiles' ends not to matter (8192 rows of 8 groups, 2048
+// outputs: K = 256 93 against 84, 512 157 / 151, 768 221 / 218, 1024 282 / 285, 2048
+// 544 / 557; 4096 rows, 1024 outputs, K = 512 45.6 / 46.6, 2048 151 / 167).
 template <bool BX, class E>
 hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStream_t s) {
     const int64_t rows = tiles_likely(a.g.M, a.g.E, 32), cus = num_cus;
@@ -458,7 +459,8 @@ hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStre
     if (is_far(epi, a.ldc)) return rows_tiles<32, 64, BX, 1, 2>(a, far(epi), s);
     if (slabs >= 8 && quarters <= cus) return rows_tiles<32, 32, BX, 8, 1>(a, epi, s);
     if (slabs >= 8 && tiles <= cus) return rows_tiles<32, 64, BX, 4, 2>(a, epi, s);
-    if (slabs >= 4 && (tiles <= 3 * cus || 4 * tiles > 19 * cus)) return rows_tiles<32, 64, BX, 2, 2>(a, epi, s);
+    if (slabs >= 4 && (tiles <= 3 * cus || (4 * tiles > 19 * cus && slabs >= 20)))
+        return rows_tiles<32, 64, BX, 2, 2>(a, epi, s);
     return rows_tiles<32, 64, BX, 1, 2>(a, epi, s);
 }
 

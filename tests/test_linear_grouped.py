@@ -71,7 +71,7 @@ def test_forward(M, N, K, E, trans_w, gather):
 # one for each way the tiles are laid out: one and two rows per group with 16 and 8
 # runs of k, and 32 rows by 32 columns with k in 8 parts and by 64 in 4, 2 and 1
 WAYS = [(5, 90, 130, 9), (11, 1300, 100, 12), (8, 70, 131, 5), (14, 1200, 100, 8), (70, 300, 270, 2), (40, 1100, 260, 9),
-        (40, 1100, 263, 9), (40, 263, 1100, 9), (700, 4200, 140, 4), (600, 2900, 141, 4), (600, 140, 2900, 4)]
+        (40, 1100, 263, 9), (40, 263, 1100, 9), (700, 4200, 140, 4), (700, 4200, 670, 4), (600, 2900, 141, 4), (600, 140, 2900, 4)]
 
 
 @pytest.mark.parametrize("trans_w", [False, True])
@@ -356,6 +356,30 @@ def test_places_past_32_bit_offsets():
     dW = t.zeros(2 * (1 << 31) + K * N, device="cuda").as_strided((E, K, N), (1 << 31, N, 1))
     got = bd.linear_f32_grouped_bwd(dev(d["dY"]), X, W, dev(d["offsets"]), Z=dev(d["Z"]), act="silu", dW=dW)
     _check_bwd(d, got, "silu", False)
+
+
+@pytest.mark.parametrize("trans_w", [False, True])
+@pytest.mark.parametrize("ld", [1 << 22, (1 << 22) + 5])
+def test_outputs_with_rows_far_apart(ld, trans_w):
+    """At the widest leading dimension whose tiles are 32-bit offsets, and past it."""
+    t = torch()
+    M, N, K, E = 70, 40, 30, 2
+    d = _inputs(M, N, K, E, trans_w, True)
+    far = lambda rows, cols: t.full((rows * ld,), 7.0, device="cuda").as_strided((rows, cols), (ld, 1))   # noqa: E731
+    Y, Z = far(M, N), far(M, N)
+    bd.linear_f32_grouped(dev(d["X"]), dev(d["W"]), dev(d["offsets"]), rows=dev(d["rows"]), bias=dev(d["b"]), act="silu",
+                          Z=Z, Y=Y, trans_w=trans_w)
+    _check(d, Y, Z, "silu", trans_w)
+    assert (Y.as_strided((M, 9), (ld, 1), N) == 7).all() and (Z.as_strided((M, 9), (ld, 1), N) == 7).all()
+    del Y, Z
+    r, c = d["W"].shape[1:]
+    dX, dW = far(M, K), far(E * r, c).as_strided((E, r, c), (r * ld, ld, 1))
+    got = _bwd(d, "silu", trans_w, dX=dX, dW=dW)
+    _check_bwd(d, got, "silu", trans_w)
+    assert (dX.as_strided((M, 9), (ld, 1), K) == 7).all() and (dW.as_strided((E * r, 9), (ld, 1), c) == 7).all()
+    once = host(dW)
+    _bwd(d, "silu", trans_w, dX=dX, dW=dW, want=("dW",), accumulate=True)
+    assert np.array_equal(host(dW), once + once)
 
 
 def test_picked_rows_up_to_2_gib():
