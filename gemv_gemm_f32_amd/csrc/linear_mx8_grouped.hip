@@ -132,9 +132,7 @@ hipError_t launch_wide(const PackedGrouped &a, hipStream_t s) {
 //  - 128 x 256 for large groups and products (4,096 rows of 8 groups, 4096 x 4096:
 //    201 / 217 at 4 bits, 210 / 234 in 64 x 128).
 //  - else 64 x 128, a last tile of up to 32 rows as 32 x 128 (1,000 rows of 16 groups,
-//    12288 x 1536: 76, all in 64 x 128 89, all in 32 x 128 88).  Asked for two
-//    waves per SIMD the compiler still takes no more registers than three leave,
-//    and its order is better (4 bits: 84 against 86).
+//    12288 x 1536: 78, all in 64 x 128 89, all in 32 x 128 88).
 template <int BITS>
 hipError_t launch_bits(const PackedGrouped &a, int num_cus, hipStream_t s) {
     const int64_t M = a.layer.M, E = a.E, N = a.layer.N, K = a.layer.K, cus = num_cus;
@@ -155,7 +153,7 @@ hipError_t launch_bits(const PackedGrouped &a, int num_cus, hipStream_t s) {
     if (K >= 1536 && tiles(32, 32) <= (lengthy ? 8 : 4) * cus) return launch_block<4, BITS, 3>(a, s);
     if (M < 16 * E || 2 * tiles(64, 128) <= 5 * cus) return launch_wide<32, 4, BITS, 3>(a, s);
     if (M >= 256 * E && tiles(128, 256) >= 2 * cus) return launch_wide<128, 8, BITS, 2>(a, s);
-    return launch_wide<64, 4, BITS, 2>(a, s);
+    return launch_wide<64, 4, BITS, 3>(a, s);
 }
 
 }  // namespace

@@ -253,32 +253,42 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
     constexpr int PER_ROW = BN / 4;                    // threads along a row
     constexpr int USED = THREADS < BM * PER_ROW ? THREADS : BM * PER_ROW;
     if (tid >= USED) return;                           // whole waves
-    const int col = tid % PER_ROW * 4;
-    const int64_t n = n0 + col;
-    const int live = (int)min(max((int64_t)a.N - n, (int64_t)0), (int64_t)4);
+    constexpr int ROWS = USED / PER_ROW;               // rows at a time
+    const int col = tid % PER_ROW * 4, rows = (int)min((int64_t)a.M - m0, (int64_t)BM);
+    const int64_t n = n0 + col, m = m0 + tid / PER_ROW;
+    const bool whole = n0 + BN <= a.N;                 // uniform
+    const int live = whole ? 4 : (int)min(max((int64_t)a.N - n, (int64_t)0), (int64_t)4);
     v4f bias = {0.f, 0.f, 0.f, 0.f};
-    if (a.bias)
+    if (a.bias) {
+        if (whole) {
+            bias = *reinterpret_cast<const v4f_any *>(a.bias + n);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (c < live) bias[c] = a.bias[n + c];
+            for (int c = 0; c < 4; ++c)
+                if (c < live) bias[c] = a.bias[n + c];
+        }
+    }
+    // a thread's first row, and ROWS rows on from there with each step
+    const float *pr = a.R + m * a.ldr + n;
+    float *py = a.Y + m * a.ldy + n;
+    uint8_t *p8 = a.Y8 + m * a.ldy8 + n, *pe = a.YE + m * a.ldye + n / 32;
     with_act(a.act, [&](auto act) {
-        constexpr int ROWS = USED / PER_ROW;               // rows at a time
 #pragma unroll 4
         for (int i = 0; i < BM / ROWS; ++i) {
             const int row = tid / PER_ROW + ROWS * i;
-            const int64_t m = m0 + row;
             v4f y = at(row, col);
-            const int w = m < a.M ? live : 0;          // columns to store
+            const bool there = row < rows;
+            const int w = there ? live : 0;            // columns to store
             v4f res = {0.f, 0.f, 0.f, 0.f};
             if (a.R) {
-                const float *p = a.R + m * a.ldr + n;
                 if (w == 4) {
-                    res = *reinterpret_cast<const v4f_any *>(p);
-                } else {
+                    res = *reinterpret_cast<const v4f_any *>(pr);
+                } else if (!whole) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (c < w) res[c] = p[c];
+                        if (c < w) res[c] = pr[c];
                 }
+                pr += ROWS * a.ldr;
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -286,14 +296,14 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
                 if (a.R) y[c] += res[c];
             }
             if (a.Y) {
-                float *p = a.Y + m * a.ldy + n;
                 if (w == 4) {
-                    *reinterpret_cast<v4f_any *>(p) = y;
-                } else {
+                    *reinterpret_cast<v4f_any *>(py) = y;
+                } else if (!whole) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (c < w) p[c] = y[c];
+                        if (c < w) py[c] = y[c];
                 }
+                py += ROWS * a.ldy;
             }
             if (a.Y8) {
                 unsigned top = 0;                      // 8 lanes hold a block of 32
@@ -301,15 +311,16 @@ __device__ __forceinline__ void finish_tile(const PackedLinear &a, int64_t m0, i
                 for (int c = 0; c < 4; ++c) top = max(top, c < w ? mag(y[c]) : 0u);
                 const int e = mx8_exponent(oct_max(top));
                 const unsigned q = mx8_pack4(y[0], y[1], y[2], y[3], e);
-                uint8_t *p = a.Y8 + m * a.ldy8 + n;
                 if (w == 4) {
-                    *reinterpret_cast<u32_any *>(p) = q;
-                } else {
+                    *reinterpret_cast<u32_any *>(p8) = q;
+                } else if (!whole) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (c < w) p[c] = (uint8_t)(q >> (8 * c));
+                        if (c < w) p8[c] = (uint8_t)(q >> (8 * c));
                 }
-                if (w > 0 && n % 32 == 0) a.YE[m * a.ldye + n / 32] = (uint8_t)e;
+                if (w > 0 && n % 32 == 0) *pe = (uint8_t)e;
+                p8 += ROWS * a.ldy8;
+                pe += ROWS * a.ldye;
             }
         }
     });
@@ -664,9 +675,9 @@ __device__ __forceinline__ void packed_block(const PackedLinear &a, int64_t m0, 
 // by turn: 2048 x 4096 x 4096 takes 73-77 us at 2 bits and 78-82 at 4 (890-940
 // and 840-880 TFLOP/s; at 4 bits vector issue is busy for 65% of the time and
 // the matrix unit for 44%), 89 and 93 with a block's products before its vector
-// work.  Four waves of 64 rows (three workgroups per CU) leave 168 registers, of
-// which 4 (2 bits) and 6 (4 bits) spill; 500 x 1536 x 12288 takes 31.5 and 34.5
-// us, a residual 2 and 2.5 more (vector issue 63 and 65%, matrix unit 29 and 25%).  MW: waves
+// work.  Four waves of 64 rows (three workgroups per CU) leave 168 registers; 500
+// x 1536 x 12288 with a residual takes 31.7 and 34.1 us (vector issue 63 and 65%,
+// matrix unit 29 and 25%; 32.6 and 35.6 with a 64-bit product per stored row).  MW: waves
 // per SIMD that the registers leave room for; a SIMD issues vector
 // instructions of one wave every 7 cycles, of two or more every 3 to 4.
 //
