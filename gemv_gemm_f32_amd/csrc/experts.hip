@@ -148,9 +148,9 @@ __global__ __launch_bounds__(64 * W) void expert_groups_kernel(ExpertGroups a, i
 }
 
 // The same over workgroups of PW waves, each with `per` entries, a multiple of
-// 64 PW.
-constexpr int PW = 4;
-
+// 64 PW.  Every workgroup adds up the counts of all: a thread per expert, or with 16
+// waves as many as there are, so that few loads follow each other.
+template <int PW>
 __global__ __launch_bounds__(64 * PW) void expert_count_kernel(ExpertGroups a, unsigned per) {
     __shared__ int count[MAX_EXPERTS + 1];
     for (int b = threadIdx.x; b <= a.E; b += 64 * PW) count[b] = 0;
@@ -163,32 +163,48 @@ __global__ __launch_bounds__(64 * PW) void expert_count_kernel(ExpertGroups a, u
     for (int b = threadIdx.x; b <= a.E; b += 64 * PW) a.rows[(int64_t)blockIdx.x * (a.E + 1) + b] = count[b];
 }
 
+template <int PW>
 __global__ __launch_bounds__(64 * PW) void expert_place_kernel(ExpertGroups a, unsigned per, int bits) {
-    __shared__ int count[PW * (MAX_EXPERTS + 1)], earlier[MAX_EXPERTS + 1];
+    constexpr int THREADS = 64 * PW, SUMS = (PW > 4 ? THREADS : 0) + MAX_EXPERTS + 1;
+    __shared__ int count[PW * (MAX_EXPERTS + 1)], total[PW > 4 ? SUMS : 1], earlier[SUMS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int bins = a.E + 1;
-    for (int i = threadIdx.x; i < PW * bins; i += 64 * PW) count[i] = 0;
+    const int bins = a.E + 1, parts = PW > 4 ? max(THREADS / bins, 1) : 1;
+    for (int i = threadIdx.x; i < PW * bins; i += THREADS) count[i] = 0;
+    // entry i of a table of parts x bins: all entries of expert i % bins in each
+    // parts-th workgroup, and those of them in earlier ones
+    const auto add_up = [&](int i) {
+        const int b = parts > 1 ? i % bins : i;
+        int sum = 0, before = 0;
+#pragma unroll 8
+        for (int g = parts > 1 ? i / bins : 0; g < (int)gridDim.x; g += parts) {
+            const int c = a.rows[(int64_t)g * bins + b];
+            sum += c;
+            before += g < (int)blockIdx.x ? c : 0;
+        }
+        earlier[i] = before;
+        return sum;
+    };
+    if constexpr (PW > 4)
+        for (int i = threadIdx.x; i < parts * bins; i += THREADS) total[i] = add_up(i);
     __syncthreads();
     const Entries all(a);
     const unsigned first = min(per * blockIdx.x + per / PW * wave, all.number());
     const unsigned end = min(first + per / PW, all.number());
     int *mine = count + wave * bins;
     all.count(mine, first, end);
-    // all entries of an expert, and those of earlier workgroups
-    const auto over_groups = [&](int b) {
-        int total = 0, before = 0;
-#pragma unroll 8
-        for (int g = 0; g < (int)gridDim.x; ++g) {
-            const int c = a.rows[(int64_t)g * bins + b];
-            total += c;
-            before += g < (int)blockIdx.x ? c : 0;
+    const auto all_of = [&](int b) {
+        if constexpr (PW > 4) {
+            int sum = total[b];
+            for (int p = 1; p < parts; ++p) sum += total[p * bins + b];
+            return sum;
+        } else {
+            return add_up(b);
         }
-        earlier[b] = before;
-        return total;
     };
-    scan_bins<PW>(bins, over_groups, [&](int b, int start) {
+    scan_bins<PW>(bins, all_of, [&](int b, int start) {
         if (blockIdx.x == 0) a.offsets[b] = start;
-        int at = start + earlier[b];                  // this thread's own value
+        int at = start;
+        for (int p = 0; p < parts; ++p) at += earlier[p * bins + b];
 #pragma unroll
         for (int w = 0; w < PW; ++w) {
             const int c = count[w * bins + b];
@@ -344,6 +360,14 @@ __global__ __launch_bounds__(256) void expert_combine_bwd_kernel(ExpertCombineBw
 constexpr int64_t MAX_GROUPS = 1 << 20;
 inline unsigned groups(int64_t n) { return (unsigned)(n < MAX_GROUPS ? n : MAX_GROUPS); }
 
+template <int PW>
+hipError_t count_and_place(const ExpertGroups &a, int64_t n, int64_t groups, int bits, hipStream_t s) {
+    const unsigned per = (unsigned)(((n + groups - 1) / groups + 64 * PW - 1) / (64 * PW) * (64 * PW));
+    const unsigned grid = (unsigned)((n + per - 1) / per);
+    const hipError_t e = launch(expert_count_kernel<PW>, dim3(grid), dim3(64 * PW), s, a, per);
+    return e == hipSuccess ? launch(expert_place_kernel<PW>, dim3(grid), dim3(64 * PW), s, a, per, bits) : e;
+}
+
 }  // namespace
 
 hipError_t launch_expert_groups(const ExpertGroups &a, hipStream_t s) {
@@ -356,15 +380,16 @@ hipError_t launch_expert_groups(const ExpertGroups &a, hipStream_t s) {
     // or several, of 1,024 entries and more, as many as their counts fit into rows,
     // where there are 8 at least (8192 entries of 64 experts 9.5 us, 10.2 in one; 4096
     // 10.2 / 7.2); each reads the counts of all, so up to 128, or one per 4,096
-    // entries (262,144 of 256 experts: 22.4, in 64 23.4, in 256 28.3; 1,048,576 of 128:
-    // 35.3 in 256, in 128 40.4)
+    // entries (on 4 waves each, 262,144 of 256 experts 22.4, in 64 23.4, in 256 28.3;
+    // 1,048,576 of 128 in 256 35.3, in 128 40.4)
     const int64_t room = n / (a.E + 1), cap = n >= 4096 * 256 ? 256 : n >= 4096 * 128 ? n / 4096 : 128;
     const int64_t most = n / 1024 < cap ? n / 1024 : cap, groups = room < most ? room : most;
     if (groups < 8) return launch(expert_groups_kernel<16>, dim3(1), dim3(1024), s, a, bits);
-    const unsigned per = (unsigned)(((n + groups - 1) / groups + 64 * PW - 1) / (64 * PW) * (64 * PW));
-    const unsigned grid = (unsigned)((n + per - 1) / per);
-    hipError_t e = launch(expert_count_kernel, dim3(grid), dim3(64 * PW), s, a, per);
-    if (e == hipSuccess) e = launch(expert_place_kernel, dim3(grid), dim3(64 * PW), s, a, per, bits);
+    // 16 waves each where entries or experts are many (262,144 entries of 256 experts
+    // 17.0 us, 22.5 on 4; 100,000 of 64 12.4 / 14.9; 65,536 of 1,000 16.4 / 23.7, of 128
+    // 13.2 / 12.5; 8192 of 8 11.2 / 8.9; 96,000 of 64 12.1 / 13.9)
+    hipError_t e = n >= 81920 || a.E >= 512 ? count_and_place<16>(a, n, groups, bits, s)
+                                            : count_and_place<4>(a, n, groups, bits, s);
     if (e == hipSuccess)
         e = launch(expert_rows_kernel, dim3((unsigned)(n < (1 << 20) ? (n + 255) / 256 : 4096)), dim3(256), s, a);
     return e;

@@ -55,7 +55,8 @@ def test_groups_of_one_expert(T, one):
 
 
 # either side of where more waves and more workgroups take over
-@pytest.mark.parametrize("T,k,E", [(767, 1, 64), (768, 1, 64), (769, 1, 64), (8191, 1, 7), (8192, 1, 7), (8193, 1, 1000),
+@pytest.mark.parametrize("T,k,E", [(767, 1, 64), (768, 1, 64), (769, 1, 64), (8191, 1, 7), (8192, 1, 7), (8193, 1, 1000), (9000, 1, 511),
+                                   (9000, 1, 512), (81919, 1, 40), (81920, 1, 40),
                                    (65536, 2, 256), (131072, 4, 64), (131073, 5, 3), (262147, 4, 1024)])
 def test_groups_by_workgroups(T, k, E):
     test_groups(T, k, E, 0.1)
