@@ -457,12 +457,16 @@ hipError_t norm(const BlockNorm &a, hipStream_t s) {
 
 // Threads and chunks per row (16 bytes per chunk) by the row's length: as few idle
 // threads as there can be, and no more than two chunks, whose loads are all in
-// flight at once (us, fp32 / 8 bits: 65536 x 256 46 / 41, on two chunks 51 / 50; 32768
-// x 768 81 / 75 on 256 threads, 85 / 82 on a wave with four chunks, 104 / 112 on 256
-// threads with two; 8192 x 4096 115 / 93 on 512, 136 / 146 on 1,024 threads; 1024 x
-// 16384 66 / 53 read twice, 57 / 65 on four chunks of 1,024 threads).
+// flight at once (us, fp32 / 8 bits: 100000 x 64 21 / 20 on 16 threads, 37 / 40 on a
+// wave; 30000 x 100 11.4 / 10.0 on 32, 14.8 / 14.9; 65536 x 256 46 / 41, on two
+// chunks 51 / 50; 32768 x 768 81 / 75 on 256 threads, 85 / 82 on a wave with four
+// chunks, 104 / 112 on 256 threads with two; 8192 x 4096 115 / 93 on 512, 136 / 146 on
+// 1,024 threads; 1024 x 16384 66 / 53 read twice, 57 / 65 on four chunks of 1,024
+// threads).
 template <Fit F>
 hipError_t norm_of(const BlockNorm &a, hipStream_t s) {
+    if (a.K <= 64) return norm<16, 1, F>(a, s);
+    if (a.K <= 128) return norm<32, 1, F>(a, s);
     if (a.K <= 256) return norm<64, 1, F>(a, s);
     if (a.K <= 512) return norm<64, 2, F>(a, s);
     if (a.K <= 1024) return norm<256, 1, F>(a, s);
@@ -474,7 +478,7 @@ hipError_t norm_of(const BlockNorm &a, hipStream_t s) {
                : launch(block_norm_long_kernel<F, false>, grid, dim3(1024), s, a);
 }
 
-// The same for the gradients, and how many workgroups (rows of the workspace)
+// The same for the gradients (100000 x 64 31 us, on a wave 72), and how many workgroups (rows of the workspace)
 // they take: two per CU, one of 1,024 threads (16384 x 2048: 153 us on 512, 159 on
 // 768, 162 on 1,024; 4096 x 8192: 161 on 256, 170 on 512, 182 on 1,024).  Up to
 // 16,384 columns rows are read once (2048 x 12288: 145 us, in three passes 245).
@@ -489,6 +493,8 @@ hipError_t norm_bwd(const BlockNormBwd &a, int &groups, hipStream_t s) {
 
 template <Fit F>
 hipError_t norm_bwd_of(const BlockNormBwd &a, int &groups, hipStream_t s) {
+    if (a.K <= 64) return norm_bwd<16, 1, F>(a, groups, s);
+    if (a.K <= 128) return norm_bwd<32, 1, F>(a, groups, s);
     if (a.K <= 256) return norm_bwd<64, 1, F>(a, groups, s);
     if (a.K <= 512) return norm_bwd<64, 2, F>(a, groups, s);
     if (a.K <= 1024) return norm_bwd<256, 1, F>(a, groups, s);
@@ -504,14 +510,14 @@ hipError_t norm_bwd_of(const BlockNormBwd &a, int &groups, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_block_norm(const BlockNorm &a, hipStream_t s) {
-    if (a.K < 4) return norm<64, 1, TINY>(a, s);
+    if (a.K < 4) return norm<16, 1, TINY>(a, s);
     return a.K % 4 ? norm_of<CUT>(a, s) : norm_of<WHOLE>(a, s);
 }
 
 hipError_t launch_block_norm_bwd(const BlockNormBwd &a, hipStream_t s) {
     int groups = 0;
     if (a.M > 0) {
-        const hipError_t e = a.K < 4    ? norm_bwd<64, 1, TINY>(a, groups, s)
+        const hipError_t e = a.K < 4    ? norm_bwd<16, 1, TINY>(a, groups, s)
                              : a.K % 4 ? norm_bwd_of<CUT>(a, groups, s) : norm_bwd_of<WHOLE>(a, groups, s);
         if (e != hipSuccess) return e;
     }

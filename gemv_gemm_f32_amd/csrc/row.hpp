@@ -26,6 +26,8 @@ constexpr int group_threads() { return T > WG ? T : WG; }
 // one barrier per call is enough (`flip` alternates).
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float (*red)[16], int flip) {
+    if constexpr (T == 16) return row16_sum(v);
+    if constexpr (T == 32) return half32_sum(v);
     v = wave64_sum(v);
     if constexpr (T == 64) return v;
     const int wave = threadIdx.x >> 6;

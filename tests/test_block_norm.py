@@ -12,12 +12,13 @@ from gpu_util import canaries_intact, dev, guarded, host, torch
 pytestmark = pytest.mark.gpu
 
 EPS = 1e-5
-# columns around every border of the row kernels: 4, 256 and its doubles up to
+# columns around every border of the row kernels: 4, 64 and its doubles up to
 # 16,384, 12,288
 SHAPES = [(5, 255), (5, 256), (70, 257), (3, 1023), (4, 1024), (9, 1025), (2, 4096), (3, 4097), (2, 12288), (3, 12289),
           (2, 16384), (2, 16385), (700, 1000), (1, 1), (3, 2), (2, 3), (1, 4), (2, 5), (1, 1536), (2, 31), (3, 32), (5, 33), (4, 100), (9, 511),
           (6, 512), (3, 513), (346, 768), (5, 2047), (4, 2048), (3, 2052), (2, 4099), (3, 8192), (2, 8193),
-          (2, 8196), (2, 40001), (1000, 36), (1100, 13), (2500, 260)]
+          (2, 8196), (2, 40001), (1000, 36), (1100, 13), (2500, 260), (37, 64), (19, 65), (9001, 63), (11, 127), (8, 128),
+          (4100, 128), (7, 129), (9001, 2)]
 GATES = ("none", "columns", "rows")
 
 
