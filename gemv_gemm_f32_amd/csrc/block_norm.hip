@@ -226,8 +226,8 @@ __global__ __launch_bounds__(group_threads<T>()) void block_norm_bwd_kernel(Bloc
         const int64_t want = base + threadIdx.x / T;
         const bool live = want < a.M;                 // uniform per team
         const int64_t row = live ? want : a.M - 1;
-        // a team without a row adds zeros: both of its norms' factors are 0
-        const float rs = live ? a.rs[row] : 0.f, ru = live ? a.ru[row] : 0.f;
+        // a team without a row takes the last one again, and neither adds nor stores it
+        const float rs = a.rs[row], ru = a.ru[row];
         v4f d[NV], s[NV], u[NV], in[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -239,17 +239,13 @@ __global__ __launch_bounds__(group_threads<T>()) void block_norm_bwd_kernel(Bloc
             if (a.dS) in[j] = take<F>(a.dS + row * a.ldds, col, a.K);
             if (a.own && !FULL) gt[j] = take<F>(a.gate + row * a.ldg, col, a.K);
         }
-        if (!live) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) d[j] = s[j] = u[j] = in[j] = zero;
-        }
         float dot = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const v4f g = vec(gs, a.gs, j);
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[j][c] *= rs;
-            add(qs, 0, j, d[j], s[j]);
+            if (ROWS == 1 || live) add(qs, 0, j, d[j], s[j]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 d[j][c] *= g[c];
@@ -271,7 +267,7 @@ __global__ __launch_bounds__(group_threads<T>()) void block_norm_bwd_kernel(Bloc
                 s[j][c] = dv[c] * g[c];                                                           // h
                 dot_u = __builtin_fmaf(s[j][c], u[j][c], dot_u);
             }
-            add(qu, 1, j, a.own ? dv : d[j], u[j]);
+            if (ROWS == 1 || live) add(qu, 1, j, a.own ? dv : d[j], u[j]);
         }
         if (a.dU) dot_u = row_sum<T>(dot_u, red, 1) * invk;    // uniform
         else if (T > 64) __syncthreads();                      // red[0] is used again

@@ -211,6 +211,19 @@ def test_bwd(M, K, carried, gate):
         assert got["dgate"] is None
 
 
+@pytest.mark.parametrize("K", [40, 100, 200, 700])
+def test_bwd_infinity_in_the_last_row_counts_once(K):
+    """An infinite gate in the last row makes one entry of dgamma_u infinite, not
+    NaN, however many rows a workgroup could hold."""
+    d = _bwd_inputs(3, K, "rows")
+    ref = _bwd_ref(d)["dgamma_u"]
+    d["gate"][2, 5] = np.inf
+    got = host(_bwd(d, want=("dgamma_u",))["dgamma_u"])
+    rest = np.arange(K) != 5
+    assert np.isinf(got[5])
+    lr.within(got[rest], ref[0][rest], ref[1][rest])
+
+
 @pytest.mark.parametrize("K", [40, 700, 2100, 8200])
 @pytest.mark.parametrize("gate", GATES)
 def test_bwd_of_what_is_wanted(K, gate):
