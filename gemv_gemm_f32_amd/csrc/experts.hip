@@ -357,6 +357,78 @@ __global__ __launch_bounds__(256) void expert_combine_bwd_kernel(ExpertCombineBw
     }
 }
 
+// Short rows, of up to 4 TEAM columns: TEAM lanes per token, so that a wave's loads
+// serve 64 / TEAM of them.  Entries without a row load row 0 (of one at least) and
+// leave it out.
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v) {
+    return TEAM == 16 ? row16_sum(v) : half32_sum(v);
+}
+
+template <int TEAM>
+__global__ __launch_bounds__(256) void expert_combine_short_kernel(ExpertCombine a) {
+    constexpr int TOKENS = 256 / TEAM;
+    const int col = threadIdx.x % TEAM * 4;
+    for (int64_t base = (int64_t)blockIdx.x * TOKENS; base < a.T; base += (int64_t)gridDim.x * TOKENS) {
+        const int64_t want = base + threadIdx.x / TEAM, t = min(want, (int64_t)a.T - 1);
+        v4f sum = {0.f, 0.f, 0.f, 0.f};
+        if (a.R) sum = get(a.R + t * a.ldr, col, a.K);
+        if (a.M > 0)
+#pragma unroll 4
+            for (int j = 0; j < a.k; ++j) {
+                const int p = a.pos[t * a.ldp + j];
+                const float f = a.w ? a.w[t * a.ldw + j] : 1.f;
+                const bool there = p >= 0 && p < a.M;
+                const v4f y = get(a.Y + (there ? (int64_t)p : 0) * a.ldy, col, a.K);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sum[c] = there ? __builtin_fmaf(f, y[c], sum[c]) : sum[c];
+            }
+        if (want < a.T) put(a.out + t * a.ldo, col, a.K, sum);
+    }
+}
+
+template <int TEAM>
+__global__ __launch_bounds__(256) void expert_combine_bwd_short_kernel(ExpertCombineBwd a) {
+    constexpr int TOKENS = 256 / TEAM, J = 4;
+    const int col = threadIdx.x % TEAM * 4;
+    const bool read = a.dw && a.M > 0;
+    for (int64_t base = (int64_t)blockIdx.x * TOKENS; base < a.T; base += (int64_t)gridDim.x * TOKENS) {
+        const int64_t want = base + threadIdx.x / TEAM, t = min(want, (int64_t)a.T - 1);
+        const v4f d = get(a.dO + t * a.ldo, col, a.K);
+        for (int j0 = 0; j0 < a.k; j0 += J) {
+            int p[J];
+            v4f y[J];
+            float f[J];
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+                const int j = min(j0 + i, a.k - 1);
+                p[i] = a.pos[t * a.ldp + j];
+                f[i] = a.w ? a.w[t * a.ldw + j] : 1.f;
+                if (want >= a.T || j0 + i >= a.k || p[i] >= a.M) p[i] = -1;
+            }
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+                y[i] = v4f{0.f, 0.f, 0.f, 0.f};
+                if (read) y[i] = get(a.Y + (int64_t)max(p[i], 0) * a.ldy, col, a.K);
+            }
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+                v4f o;
+                float dot = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    o[c] = f[i] * d[c];
+                    dot = __builtin_fmaf(d[c], y[i][c], dot);
+                }
+                if (a.dY && p[i] >= 0) put(a.dY + (int64_t)p[i] * a.lddy, col, a.K, o);
+                if (a.dw == nullptr) continue;        // uniform
+                dot = team_sum<TEAM>(dot);
+                if (want < a.T && j0 + i < a.k && col == 0) a.dw[t * a.lddw + j0 + i] = p[i] < 0 ? 0.f : dot;
+            }
+        }
+    }
+}
+
 constexpr int64_t MAX_GROUPS = 1 << 20;
 inline unsigned groups(int64_t n) { return (unsigned)(n < MAX_GROUPS ? n : MAX_GROUPS); }
 
@@ -395,7 +467,16 @@ hipError_t launch_expert_groups(const ExpertGroups &a, hipStream_t s) {
     return e;
 }
 
+// Threads per token where rows are short (us, 8192 tokens of 8 entries, on 16 or 32
+// threads and on a wave: K = 64 5.6 / 13.0, gradients 7.6 / 21.9; K = 128 7.9 / 17.9,
+// gradients 13.6 / 25.5; one token of 8, K = 64: 3.5 / 3.9, gradients 4.2 / 6.1).
+int team_of(int K) { return K <= 64 ? 16 : K <= 128 ? 32 : 0; }
+
 hipError_t launch_expert_combine(const ExpertCombine &a, hipStream_t s) {
+    if (const int team = team_of(a.K)) {
+        const dim3 grid(groups(((int64_t)a.T * team + 255) / 256));
+        return launch(team == 16 ? expert_combine_short_kernel<16> : expert_combine_short_kernel<32>, grid, dim3(256), s, a);
+    }
     // four spans per wave where that still gives every SIMD a wave, else one
     const int64_t wide = ((int64_t)a.K + 1023) / 1024, narrow = ((int64_t)a.K + 255) / 256;
     if (wide * a.T >= 4096)
@@ -413,6 +494,11 @@ hipError_t combine_bwd(const ExpertCombineBwd &a, hipStream_t s) {
 }
 
 hipError_t launch_expert_combine_bwd(const ExpertCombineBwd &a, hipStream_t s) {
+    if (const int team = team_of(a.K)) {
+        const dim3 grid(groups(((int64_t)a.T * team + 255) / 256));
+        return launch(team == 16 ? expert_combine_bwd_short_kernel<16> : expert_combine_bwd_short_kernel<32>, grid,
+                      dim3(256), s, a);
+    }
     // four waves per token where each has a span, or where tokens are few (us, in
     // one wave / in four: 8192 tokens, 2 entries, 2048 columns 70 / 62; 8192, 8, 512
     // 58 / 88; 2048, 2, 768 6.5 / 7.8; 346, 2, 768 4.5 / 4.0; 1, 8, 1536 12.6 / 7.3)

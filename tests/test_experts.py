@@ -82,7 +82,8 @@ def test_groups_strides_and_what_lies_around(T, k):
 # --------------------------------------------------------------- combine --
 
 COMBINE = [(1, 1, 1), (1, 8, 768), (3, 2, 255), (2, 3, 256), (5, 4, 257), (346, 2, 768), (70, 5, 1000),
-           (33, 9, 1025), (600, 3, 2048), (9, 1, 4099), (2000, 2, 36), (1200, 4, 1031)]
+           (33, 9, 1025), (600, 3, 2048), (9, 1, 4099), (2000, 2, 36), (1200, 4, 1031), (40, 8, 64), (17, 5, 65),
+           (9, 3, 128), (8, 4, 129), (1100, 7, 101), (3, 9, 3), (2, 1, 64)]
 
 
 def _combine_inputs(T, k, K, seed=0, missing=0.0):
