@@ -438,13 +438,12 @@ hipError_t few_tiles(const GroupedRows &a, const Layer &epi, hipStream_t s) {
 // once (us, K = 768, groups of like size):
 //
 //   rows, groups, N    32 x 64 in 1   in 2   in 4   32 x 32 in 8
-//     64,  8,  768         21.1       14.4   13.3       10.2
-//    192,  8,  768         20.9       14.3   13.2       17.1
-//    256,  8, 2304         32.9       22.7   25.8       32.5
-//    768,  8, 2304         35.7       43.1   46.0       59.6
-//   1536, 32,  768         35.2       37.6   45.7       53.1
-//     64, 128, 768         29.9       25.9   34.8       46.1
-//    128, 128, 768         33.0       41.0   48.2       63.9
+//     64,  8,  768         17.1       11.0   10.2        7.3
+//    256,  8, 2304         27.0       17.2   20.8       26.6
+//    768,  8, 2304         30.6       35.4   38.5       50.6
+//   1536, 32,  768         29.9       31.8   40.1       44.5
+//     64, 128, 768         28.5       24.9   34.0       43.1
+//    128, 128, 768         32.6       40.3   47.5       60.6
 //
 // One 32 x 32 tile in 8 k-groups, or one 32 x 64 in 4, fills a CU's LDS; 3 in 2
 // k-groups and 6 in 1 do.  Longer grids run in 2 as fast as in 1 or faster where K
@@ -467,13 +466,15 @@ hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStre
 // Up to 16 rows, where groups have one or two at most: a kernel that reads each
 // group's matrix once, without tiles (us, 8 groups of N x K = 2304 x 768 /
 // 768 x 2304, against the best tile):
-//   W stored K x N   2 rows 6.9 / 9.4 against 9.7 / 16.3, 4 rows 8.1 / - against
-//                    10.1, 8 rows 9.6 / 9.9 against 9.9 / 16.7, 16 rows 12.0 / 14.5
-//                    against 13.3 / 17.1, 32 rows 19.6 / 21.7 against 14.7 / 17.5
-//   W stored N x K   2 rows 6.7 / 7.1 against 9.1 / 15.3, 8 rows 10.0 / 8.2 against
-//                    9.5 / 15.3, 16 rows 14.4 / 11.0 against 12.7 / 15.4
-// K x N: 16 waves per 32 columns where that is a workgroup per CU at most, else
-// 8 (2 rows, 2304 x 768: 6.9 against 7.3; 4 rows 10.3 against 8.1).
+//   W stored K x N   2 rows 5.1 / 7.7 against 7.5 / 13.5, 4 rows 6.5 / 7.9 against
+//                    11.1 / 14.1, 8 rows 10.9 / 11.3 against 12.4 / 14.5, 16 rows 11.0 /
+//                    13.0 against 12.3 / 14.5, 32 rows 17.5 / 16.7 against 16.8 / 15.3
+//   W stored N x K   2 rows 4.4 / 3.9 against 7.2 / 12.9, 8 rows 10.0 / 8.8 against
+//                    13.1 / 14.2, 16 rows 13.4 / 10.0 against 13.0 / 14.1
+// K x N: 16 waves per 32 columns where that is a workgroup per CU at most, else 8 (2
+// rows, 2304 x 768: 5.1 against 5.3; 4 rows 7.0 / 6.5).  N x K: one row at a time
+// where few groups have more (2 rows 4.4 against 4.8 and 3.9 / 4.5, 8 rows 11.1 /
+// 10.0 and 8.3 / 8.8).
 inline bool few_rows(const GroupedRows &a, bool nk) {
     const int64_t M = a.g.M, E = a.g.E;
     return M <= 16 && (M <= E || (M <= 2 * E && (!nk || a.N <= 2048)));
@@ -482,7 +483,7 @@ inline bool few_rows(const GroupedRows &a, bool nk) {
 template <bool BX>
 hipError_t few_product(const GroupedRows &a, const Layer &epi, int num_cus, hipStream_t s) {
     if constexpr (BX) {
-        return few_tiles<2, true, 1, 4>(a, epi, s);
+        return 2 * (int64_t)a.g.M <= a.g.E ? few_tiles<1, true, 1, 4>(a, epi, s) : few_tiles<2, true, 1, 4>(a, epi, s);
     } else {
         const int64_t M = a.g.M, slabs = ((int64_t)a.N + 31) / 32;
         const bool wide = M * slabs <= num_cus;

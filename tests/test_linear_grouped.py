@@ -70,7 +70,7 @@ def test_forward(M, N, K, E, trans_w, gather):
 
 # one for each way the tiles are laid out: one and two rows per group with 16 and 8
 # runs of k, and 32 rows by 32 columns with k in 8 parts and by 64 in 4, 2 and 1
-WAYS = [(5, 90, 130, 9), (11, 1300, 100, 12), (8, 70, 131, 5), (14, 1200, 100, 8), (70, 300, 270, 2), (40, 1100, 260, 9),
+WAYS = [(5, 90, 130, 9), (5, 300, 700, 10), (11, 1300, 100, 12), (8, 70, 131, 5), (14, 1200, 100, 8), (70, 300, 270, 2), (40, 1100, 260, 9),
         (40, 1100, 263, 9), (40, 263, 1100, 9), (700, 4200, 140, 4), (700, 4200, 670, 4), (600, 2900, 141, 4), (600, 140, 2900, 4)]
 
 
