@@ -265,6 +265,43 @@ __global__ __launch_bounds__(64 * KW * ROWS) void grouped_few_kernel(GroupedRows
     else few_kn<MB, KW>(left, a.N, a.K, x, W, a.ldb, Y, a.ldc, e, n0);
 }
 
+// Gradients of the weights and, of the tiles of DZ_ROWS rows that the element pass
+// summed, of the biases.
+constexpr int DZ_ROWS = 128;
+
+// db_e: a wave adds 64 columns' sums over its group's tiles, in 8 interleaved runs.
+struct BiasSums {
+    const float *partial;          // most x N
+    float *db;                     // NULL: not wanted
+    int64_t lddb;
+    int N, most, accumulate;
+    __host__ __device__ int64_t waves(int E) const { return db ? ((int64_t)N + 63) / 64 * E : 0; }
+    __device__ __forceinline__ void columns(const Groups &g, int64_t wave) const {
+        if (wave >= waves(g.E)) return;
+        const int64_t blocks = ((int64_t)N + 63) / 64;
+        const int e = (int)(wave / blocks);
+        const int from = (int)min(tiles_before<DZ_ROWS>(g, e), (int64_t)most);
+        int first, count;
+        group_rows(g, e, first, count);
+        const int end = (int)min((int64_t)from + tiles_in<DZ_ROWS>(count), (int64_t)most);
+        const int64_t col = wave % blocks * 64 + (threadIdx.x & 63);
+        if (col >= N) return;
+        float run[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int i = from; i < end; i += 8) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = partial[(int64_t)min(i + u, end - 1) * N + col];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) run[u] += i + u < end ? v[u] : 0.f;
+        }
+        float sum = run[0];
+#pragma unroll
+        for (int u = 1; u < 8; ++u) sum += run[u];
+        float *to = db + e * lddb + col;
+        *to = accumulate ? *to + sum : sum;
+    }
+};
+
 // dW_e = A_e^T . B_e over the rows of group e, A and B stored row by row; PICK:
 // which of them is read through `rows`.
 enum Pick { NEITHER, PICK_A, PICK_B };
@@ -276,14 +313,20 @@ struct GroupedWeights {
     float *C;
     int64_t lda, ldb, ldc, stridec;
     bool by_size;                  // the largest groups first
+    BiasSums bias;                 // what the first workgroups do, if anything
+    int bias_groups;
 };
 
 template <int BM, int BN, int KS, int WPG, Pick PICK, class E>
 __global__ __launch_bounds__(64 * WPG * KS) void grouped_weights_kernel(GroupedWeights a, E epi) {
     using S = TileShape<BM, BN, false, false, KS, WPG, false, 32>;
     const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN, per = tiles_m * tiles_n;
-    const int64_t bid = group_number(), n = (int64_t)per * a.g.E;
+    const int64_t bid = group_number() - a.bias_groups, n = (int64_t)per * a.g.E;
     if (bid >= n) return;
+    if (bid < 0) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        return a.bias.columns(a.g, group_number() * (KS * WPG) + wave);
+    }
     // every XCD takes a part of each expert: groups differ in size, so that an
     // expert per XCD would leave most of them waiting for the largest
     const OneGroup g = group_at(a.g, (int)(bid / per), a.by_size, a.g.M / a.g.E);
@@ -320,7 +363,6 @@ __global__ __launch_bounds__(64 * WPG * KS) void grouped_weights_kernel(GroupedW
 // dZ = dY * act'(Z) and the column sums of each tile of DZ_ROWS rows, as the
 // dense layer's element pass (linear_bwd.hip): 64 columns per workgroup, 16
 // lanes of 4 columns by 16 rows at a time.
-constexpr int DZ_ROWS = 128;
 
 __global__ __launch_bounds__(256) void grouped_dz_kernel(Groups g, int act, int N, const float *dY,
                                                          int64_t lddy, const float *Z, int64_t ldz,
@@ -382,31 +424,8 @@ __global__ __launch_bounds__(256) void grouped_dz_kernel(Groups g, int act, int 
     }
 }
 
-// db_e: the sums of its group's tiles, 8 interleaved runs of tiles per column,
-// then the runs in order.
-__global__ __launch_bounds__(512) void grouped_bias_kernel(Groups g, int N, const float *partial, bool accumulate,
-                                                           float *db, int64_t lddb, int most) {
-    __shared__ float red[8][64];
-    const int64_t blocks = ((int64_t)N + 63) / 64, bid = group_number();
-    if (bid >= blocks * g.E) return;
-    const int e = (int)(bid / blocks);
-    const int from = (int)min(tiles_before<DZ_ROWS>(g, e), (int64_t)most);
-    int first, count;
-    group_rows(g, e, first, count);
-    const int end = (int)min((int64_t)from + tiles_in<DZ_ROWS>(count), (int64_t)most);
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    const int64_t col = bid % blocks * 64 + tx;
-    float sum = 0.f;
-    if (col < N)
-#pragma unroll 4
-        for (int i = from + ty; i < end; i += 8) sum += partial[(int64_t)i * N + col];
-    red[ty][tx] = sum;
-    __syncthreads();
-    if (ty > 0 || col >= N) return;
-#pragma unroll
-    for (int y = 1; y < 8; ++y) sum += red[y][tx];
-    float *to = db + e * lddb + col;
-    *to = accumulate ? *to + sum : sum;
+__global__ __launch_bounds__(256) void grouped_bias_kernel(Groups g, BiasSums b) {
+    b.columns(g, group_number() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
 }
 
 // ---------------------------------------------------------------------------
@@ -498,8 +517,9 @@ hipError_t layer_product(const GroupedRows &a, const Layer &epi, int num_cus, hi
 }
 
 template <int KS, Pick PICK, class E>
-hipError_t weights_tiles(const GroupedWeights &a, const E &epi, int64_t n, hipStream_t s) {
-    return launch(grouped_weights_kernel<64, 64, KS, 4, PICK, E>, grid_of(n), dim3(256 * KS), s, a, epi);
+hipError_t weights_tiles(GroupedWeights a, const E &epi, int64_t n, hipStream_t s) {
+    a.bias_groups = (int)((a.bias.waves(a.g.E) + 4 * KS - 1) / (4 * KS));
+    return launch(grouped_weights_kernel<64, 64, KS, 4, PICK, E>, grid_of(a.bias_groups + n), dim3(256 * KS), s, a, epi);
 }
 
 // 64 x 64 tiles, four workgroups of which share a CU, the largest groups' first
@@ -541,6 +561,7 @@ hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hip
     hipError_t e = hipSuccess;
     const float *dZ = a.dY;
     int64_t lddz = a.lddy;
+    BiasSums bias{};
     if (a.N > 0 && (a.act != GG_ACT_NONE || a.db != nullptr)) {
         const int64_t most = grouped_dz_tiles(a.M, a.E), cols = ((int64_t)a.N + 63) / 64;
         float *out = a.ws, *partial = a.ws;
@@ -554,9 +575,11 @@ hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hip
             e = launch(grouped_dz_kernel, grid_of(most * cols), dim3(256), s, g, a.act, a.N, a.dY, a.lddy, a.Z, a.ldz,
                        out, lddz, a.db ? partial : nullptr, (int)most);
         if (e != hipSuccess) return e;
-        if (a.db)
-            e = launch(grouped_bias_kernel, grid_of(cols * a.E), dim3(512), s, g, a.N, partial, a.accumulate, a.db,
-                       a.lddb, (int)most);
+        // in the launch of dW where there is one (all gradients of 64 rows of 8 groups, 768
+        // x 768: 21.2 us, 23.3 in one of its own)
+        if (a.db) bias = {partial, a.db, a.lddb, a.N, (int)most, a.accumulate ? 1 : 0};
+        if (a.db && !a.dW)
+            e = launch(grouped_bias_kernel, grid_of((bias.waves(a.E) + 3) / 4), dim3(256), s, g, bias);
         if (e != hipSuccess) return e;
     }
     if (a.dX) {
@@ -569,8 +592,8 @@ hipError_t launch_linear_grouped_bwd(const LinearGroupedBwd &a, int num_cus, hip
         // finding the order takes 2 to 4% where groups are of like size (64 rows each of
         // 64, 1024 x 1024: 143 against 137 us; 512 each of 8, 2048 x 1024: 162 / 161)
         const bool by_size = a.M >= 128 * (int64_t)a.E;
-        GroupedWeights w{g, a.K, a.N, a.T, a.X, dZ, a.rows, a.dW, a.ldx, lddz, a.lddw, a.stridedw, by_size};
-        if (a.trans_w) w = {g, a.N, a.K, a.T, dZ, a.X, a.rows, a.dW, lddz, a.ldx, a.lddw, a.stridedw, by_size};
+        GroupedWeights w{g, a.K, a.N, a.T, a.X, dZ, a.rows, a.dW, a.ldx, lddz, a.lddw, a.stridedw, by_size, bias, 0};
+        if (a.trans_w) w = {g, a.N, a.K, a.T, dZ, a.X, a.rows, a.dW, lddz, a.ldx, a.lddw, a.stridedw, by_size, bias, 0};
         const Store st{a.accumulate ? 1 : 0};
         e = !a.rows ? weights_product<NEITHER>(w, st, num_cus, s)
             : a.trans_w ? weights_product<PICK_B>(w, st, num_cus, s) : weights_product<PICK_A>(w, st, num_cus, s);
