@@ -168,9 +168,10 @@ def test_grids_of_the_layer(record, M, N, K, E, v):
     (name, groups), = record("forward", M, N, K, E, v)
     assert "grouped_" in name and groups >= -(-M // 64) * -(-N // 64)
     launches = record("backward", M, N, K, E, v)
-    assert len(launches) == 4 and "dz" in launches[0][0] and "bias" in launches[1][0]
-    assert launches[1][1] >= -(-N // 64) * E
-    assert launches[2][1] >= -(-M // 64) * -(-K // 64) and launches[3][1] >= E * -(-N // 64) * -(-K // 64)
+    # the biases' sums are a wave each of 64 columns in the last launch's first workgroups
+    assert len(launches) == 3 and "dz" in launches[0][0]
+    assert launches[1][1] >= -(-M // 64) * -(-K // 64)
+    assert launches[2][1] >= E * -(-N // 64) * -(-K // 64) + -(-E * -(-N // 64) // 16)
 
 
 @pytest.mark.parametrize("bits", [2, 4])
