@@ -50,8 +50,14 @@ __host__ __device__ inline void group_rows(const Groups &g, int e, int &first, i
     }
 }
 
+// Tiles of `size` that n rows or columns need, for any n below 2^31 (n + size - 1 may
+// lie past it).
+__host__ __device__ inline int tiles_of(int n, int size) {
+    return (int)(((unsigned)n + (unsigned)size - 1) / (unsigned)size);
+}
+
 template <int BM>
-__device__ __forceinline__ int tiles_in(int count) { return count / BM + (count % BM != 0); }
+__device__ __forceinline__ int tiles_in(int count) { return tiles_of(count, BM); }
 
 // Tiles of the first `upto` groups, of 128 rows or so: 64 groups' then fit 32
 // bits even where offsets that are not in order count rows more than once.

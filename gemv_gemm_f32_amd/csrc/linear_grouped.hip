@@ -211,7 +211,7 @@ struct GroupedRows {
 template <int BM, int BN, bool BX, int KS, int WPG, bool KT, class E>
 __global__ __launch_bounds__(64 * WPG * KS) void grouped_rows_kernel(GroupedRows a, E epi, int most) {
     using S = TileShape<BM, BN, true, BX, KS, WPG, KT, 32>;
-    const int tiles_n = (a.N + BN - 1) / BN;
+    const int tiles_n = tiles_of(a.N, BN);
     GroupTiles<BM> tiles(a.g, most);
     const int64_t bid = group_number(), n = (int64_t)tiles.number * tiles_n;
     if (bid >= n) return;
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(64 * WPG * KS) void grouped_rows_kernel(GroupedRows
 template <int MB, bool BX, int KW, int ROWS>
 __global__ __launch_bounds__(64 * KW * ROWS) void grouped_few_kernel(GroupedRows a, Layer epi, int most) {
     constexpr int COLS = BX ? ROWS : 32;
-    const int tiles_n = (a.N + COLS - 1) / COLS;
+    const int tiles_n = tiles_of(a.N, COLS);
     GroupTiles<MB> tiles(a.g, most);
     const int64_t bid = group_number();
     if (bid >= (int64_t)tiles.number * tiles_n) return;
@@ -320,7 +320,7 @@ struct GroupedWeights {
 template <int BM, int BN, int KS, int WPG, Pick PICK, class E>
 __global__ __launch_bounds__(64 * WPG * KS) void grouped_weights_kernel(GroupedWeights a, E epi) {
     using S = TileShape<BM, BN, false, false, KS, WPG, false, 32>;
-    const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN, per = tiles_m * tiles_n;
+    const int tiles_m = tiles_of(a.M, BM), tiles_n = tiles_of(a.N, BN), per = tiles_m * tiles_n;
     const int64_t bid = group_number() - a.bias_groups, n = (int64_t)per * a.g.E;
     if (bid >= n) return;
     if (bid < 0) {
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(256) void grouped_dz_kernel(Groups g, int act, int 
                                                          int64_t lddy, const float *Z, int64_t ldz,
                                                          float *dZ, int64_t lddz, float *partial, int most) {
     __shared__ v4f red[256];
-    const int tiles_n = (N + 63) / 64;
+    const int tiles_n = tiles_of(N, 64);
     GroupTiles<DZ_ROWS> tiles(g, most);
     const int64_t bid = group_number();
     if (bid >= (int64_t)tiles.number * tiles_n) return;

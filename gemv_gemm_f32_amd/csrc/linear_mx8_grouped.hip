@@ -47,7 +47,7 @@ template <int BM>
 __device__ __forceinline__ bool find_tile(const PackedGrouped &a, int bn, int most, GroupTile &t, int64_t &n0) {
     const Groups g{a.offsets, a.E, a.layer.M};
     GroupTiles<BM> tiles(g, most);
-    const int tiles_n = (a.layer.N + bn - 1) / bn;
+    const int tiles_n = tiles_of(a.layer.N, bn);
     const int64_t bid = group_number(), n = (int64_t)tiles.number * tiles_n;
     if (bid >= n) return false;
     const int tb = xcd_run((int)bid, (int)n);
