@@ -100,6 +100,15 @@ __host__ __device__ __forceinline__ int clamp_k(int k0, int k, int last) {
     return (int)(sum < (unsigned)last ? sum : (unsigned)last);
 }
 
+// The same for the direct path, in the type Place that holds places along k and a
+// few slabs behind K: int for whole matrices, which end within 2 GiB, and unsigned
+// for the rows of a group, which may be 2^31 - 1.
+template <int BK, class Place>
+__host__ __device__ __forceinline__ int slabs_to(int K) { return (int)(((Place)K + BK - 1) / BK); }
+// whether the n places from k on reach behind K
+template <class Place>
+__host__ __device__ __forceinline__ bool past_k(Place k, int n, int K) { return k + n > (Place)K; }
+
 template <int TX, int BK, bool XMAJOR>
 constexpr int tile_words() { return XMAJOR ? TX * xstride<BK>() : BK * kstride<TX>(); }
 
@@ -412,16 +421,17 @@ struct DirectOperand {
     // after this wave's loads of the slab at k0 have landed: zero what lies at
     // k >= K (whole chunks, and in x-major rows the part of a chunk past K
     // when K is not a multiple of 4)
+    template <class Place>
     __device__ __forceinline__ void zero_tail(char *stage, int k0, int K, int wave, int lane) const {
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
             if (!has(j, wave)) continue;
             float *p = reinterpret_cast<float *>(stage + (WPG * j + wave) * 1024 + lane * 16);
-            const int k = k0 + kof[j];
-            if (k >= K) {
+            const Place k = (Place)k0 + kof[j];
+            if (k >= (Place)K) {
                 *reinterpret_cast<v4f *>(p) = v4f{0.f, 0.f, 0.f, 0.f};
-            } else if (XMAJOR && KT && k + 4 > K) {
-                for (int e = K - k; e < 4; ++e) p[e] = 0.f;
+            } else if (XMAJOR && KT && past_k<Place>(k, 4, K)) {
+                for (int e = (int)((Place)K - k); e < 4; ++e) p[e] = 0.f;
             }
         }
     }
@@ -446,9 +456,10 @@ struct DirectOperand {
 
 // One operand of a whole matrix, as direct_tile takes it: start() and issue()
 // are given the slab they are for, and the slab that the same k-group takes
-// after it.
+// after it, which may lie behind K.
 template <class OP>
 struct Slabs {
+    using Place = int;
     OP op;
     const float *P;
     int ext;
@@ -566,7 +577,8 @@ __device__ __forceinline__ void direct_tile(int M, int N, int K, SA &sa, SB &sb,
 #pragma unroll
         for (int j = 0; j < JB; ++j) epi.fetch(pre[i][j], col_of(j), M, N, row_of(i), mine(i, j));
 
-    const int nk = (K + BK - 1) / BK;
+    using Place = typename SA::Place;
+    const int nk = slabs_to<BK, Place>(K);
     const int rounds = (nk + KS - 1) / KS;        // the same for every group
     if (rounds > 0) {
         if (grp < nk) {
@@ -575,9 +587,9 @@ __device__ __forceinline__ void direct_tile(int M, int N, int K, SA &sa, SB &sb,
             sa.issue(stage_a(0), grp * BK, (grp + KS) * BK, wq);
             sb.issue(stage_b(0), grp * BK, (grp + KS) * BK, wq);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            if (grp * BK + BK > K) {
-                sa.op.zero_tail(stage_a(0), grp * BK, K, wq, lane);
-                sb.op.zero_tail(stage_b(0), grp * BK, K, wq, lane);
+            if (past_k<Place>(grp * BK, BK, K)) {
+                sa.op.template zero_tail<Place>(stage_a(0), grp * BK, K, wq, lane);
+                sb.op.template zero_tail<Place>(stage_b(0), grp * BK, K, wq, lane);
             }
         }
         __syncthreads();
@@ -586,13 +598,13 @@ __device__ __forceinline__ void direct_tile(int M, int N, int K, SA &sa, SB &sb,
         const int buf = r & 1;
         const int kt = r * KS + grp;              // this group's slab in round r
         const int kn = kt + KS;                   // and in round r + 1
-        const int k1 = kn * BK;
+        const int k1 = kn * BK, k2 = (int)((Place)k1 + KS * BK);
         const bool more = r + 1 < rounds;
         // slab kn goes to the stage last read in round r-1, whose reads all
         // finished before the previous barrier
         if (!LATE && more && kn < nk) {
-            sa.issue(stage_a(buf ^ 1), k1, k1 + KS * BK, wq);
-            sb.issue(stage_b(buf ^ 1), k1, k1 + KS * BK, wq);
+            sa.issue(stage_a(buf ^ 1), k1, k2, wq);
+            sb.issue(stage_b(buf ^ 1), k1, k2, wq);
         }
         if (kt < nk) {
             const char *as = stage_a(buf), *bs = stage_b(buf);
@@ -645,8 +657,8 @@ __device__ __forceinline__ void direct_tile(int M, int N, int K, SA &sa, SB &sb,
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 if (LATE && g == 0 && more && kn < nk) {
-                    sa.issue(stage_a(buf ^ 1), k1, k1 + KS * BK, wq);
-                    sb.issue(stage_b(buf ^ 1), k1, k1 + KS * BK, wq);
+                    sa.issue(stage_a(buf ^ 1), k1, k2, wq);
+                    sb.issue(stage_b(buf ^ 1), k1, k2, wq);
                     __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
@@ -659,9 +671,9 @@ __device__ __forceinline__ void direct_tile(int M, int N, int K, SA &sa, SB &sb,
             // the loads into LDS are tracked by vmcnt; the compiler does not
             // wait for them, so wait here before publishing the slab
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            if (kn < nk && k1 + BK > K) {
-                sa.op.zero_tail(stage_a(buf ^ 1), k1, K, wq, lane);
-                sb.op.zero_tail(stage_b(buf ^ 1), k1, K, wq, lane);
+            if (kn < nk && past_k<Place>(k1, BK, K)) {
+                sa.op.template zero_tail<Place>(stage_a(buf ^ 1), k1, K, wq, lane);
+                sb.op.template zero_tail<Place>(stage_b(buf ^ 1), k1, K, wq, lane);
             }
             // A k-group of one wave reads only the stages it fills itself:
             // its own wait above publishes the slab to it, and its reads of

@@ -30,6 +30,7 @@ namespace {
 // slab are 32 bits.
 template <class OP, bool XMAJOR>
 struct NearSlabs {
+    using Place = unsigned;
     OP op;
     const float *P;      // x-major: the tile's first row; k-major: its first column
     int64_t ld, X, K;    // x-major: rows from P on; k-major: columns
@@ -45,6 +46,7 @@ struct NearSlabs {
 // numbers are fetched with each slab, so that no load waits for them.
 template <class OP>
 struct PickedSlabs {
+    using Place = unsigned;
     OP op;
     const float *P;
     int64_t ld, X;

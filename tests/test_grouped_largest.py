@@ -13,6 +13,7 @@ from test_largest_sizes import MOST, _e4m3, _equal, _pattern
 HOST = r"""
 #include <stdio.h>
 #include <stdlib.h>
+#include "gemm_f32_tile.hpp"
 #include "groups.hpp"
 using namespace gg;
 #define CHECK(c) do { if (!(c)) { printf("FAIL line %d: %s\n", __LINE__, #c); exit(1); } } while (0)
@@ -23,12 +24,21 @@ int main() {
             const int64_t tiles = tiles_of((int)n, size);
             CHECK(tiles == n / size + (n % size != 0));
         }
+    /* the walk along k: slabs, and which places of the last one lie behind K */
+    for (int64_t K : {int64_t(1), int64_t(31), int64_t(32), int64_t(33), int64_t(1) << 30, int64_t(INT32_MAX) - 32,
+                      int64_t(INT32_MAX) - 31, int64_t(INT32_MAX) - 30, int64_t(INT32_MAX) - 1, int64_t(INT32_MAX)}) {
+        const int64_t slabs = slabs_to<32, unsigned>((int)K);
+        CHECK(slabs == K / 32 + (K % 32 != 0));
+        const int64_t k0 = (slabs - 1) * 32;
+        for (int k = 0; k < 32; ++k)
+            for (int n : {1, 4, 32}) CHECK(past_k<unsigned>((unsigned)k0 + k, n, (int)K) == (k0 + k + n > K));
+    }
     printf("ALL OK\n");
 }
 """
 
 
-def test_tiles_of_any_size(tmp_path):
+def test_tiles_and_slabs_of_any_size(tmp_path):
     src, obj, exe = tmp_path / "host.cpp", tmp_path / "host.o", tmp_path / "host"
     src.write_text(HOST)
     _hipcc(src, obj)
