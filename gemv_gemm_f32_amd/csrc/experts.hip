@@ -3,6 +3,7 @@
 // results with its gradients.
 #include <hip/hip_runtime.h>
 
+#include "groups.hpp"
 #include "kernels.hpp"
 #include "wave.hpp"
 
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(256) void expert_combine_bwd_kernel(ExpertCombineBw
         const bool live = base + sub < a.T;
         const int64_t t = live ? base + sub : a.T - 1;
         const float *dO = a.dO + t * a.ldo;
-        for (int j0 = 0; j0 < a.k; j0 += J) {
+        for (int j0 = 0; j0 < a.k; j0 = next_run<J>(j0, a.k)) {
             int p[J];
             float f[J], dot[J];
 #pragma unroll
@@ -395,7 +396,7 @@ __global__ __launch_bounds__(256) void expert_combine_bwd_short_kernel(ExpertCom
     for (int64_t base = (int64_t)blockIdx.x * TOKENS; base < a.T; base += (int64_t)gridDim.x * TOKENS) {
         const int64_t want = base + threadIdx.x / TEAM, t = min(want, (int64_t)a.T - 1);
         const v4f d = get(a.dO + t * a.ldo, col, a.K);
-        for (int j0 = 0; j0 < a.k; j0 += J) {
+        for (int j0 = 0; j0 < a.k; j0 = next_run<J>(j0, a.k)) {
             int p[J];
             v4f y[J];
             float f[J];

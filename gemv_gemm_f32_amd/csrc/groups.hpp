@@ -156,6 +156,11 @@ __device__ __forceinline__ OneGroup group_at(const Groups &g, int r, bool by_siz
     return {c + l, __builtin_amdgcn_readlane(first, l), __builtin_amdgcn_readlane(count, l)};
 }
 
+// The run of J entries behind the one at j0, of k entries; k behind the last one (j0 +
+// J may lie past 2^31).
+template <int J>
+__host__ __device__ __forceinline__ int next_run(int j0, int k) { return k - j0 > J ? j0 + J : k; }
+
 // Workgroups in a grid of up to 65,535 x 2^20, and one's number.
 __device__ __forceinline__ int64_t group_number() {
     return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;

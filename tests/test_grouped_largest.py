@@ -17,6 +17,11 @@ HOST = r"""
 #include "groups.hpp"
 using namespace gg;
 #define CHECK(c) do { if (!(c)) { printf("FAIL line %d: %s\n", __LINE__, #c); exit(1); } } while (0)
+template <int J> void runs(int64_t k) {
+    int64_t n = 0;
+    for (int j0 = 0; j0 < k; j0 = next_run<J>(j0, (int)k)) CHECK(j0 == n++ * J && (int64_t)j0 + J - 1 <= INT32_MAX);
+    CHECK(n == k / J + (k % J != 0));
+}
 int main() {
     for (int64_t n : {int64_t(0), int64_t(1), int64_t(31), int64_t(32), int64_t(33), int64_t(1) << 30, int64_t(INT32_MAX) - 128,
                       int64_t(INT32_MAX) - 127, int64_t(INT32_MAX) - 63, int64_t(INT32_MAX) - 1, int64_t(INT32_MAX)})
@@ -33,12 +38,17 @@ int main() {
         for (int k = 0; k < 32; ++k)
             for (int n : {1, 4, 32}) CHECK(past_k<unsigned>((unsigned)k0 + k, n, (int)K) == (k0 + k + n > K));
     }
+    /* a token's entries, J at a time */
+    for (int64_t k : {0, 1, 7, 8, 9, 1 << 20, INT32_MAX - 8, INT32_MAX - 7, INT32_MAX - 3, INT32_MAX - 1, INT32_MAX}) {
+        runs<4>(k);
+        runs<8>(k);
+    }
     printf("ALL OK\n");
 }
 """
 
 
-def test_tiles_and_slabs_of_any_size(tmp_path):
+def test_counts_of_any_size(tmp_path):
     src, obj, exe = tmp_path / "host.cpp", tmp_path / "host.o", tmp_path / "host"
     src.write_text(HOST)
     _hipcc(src, obj)
