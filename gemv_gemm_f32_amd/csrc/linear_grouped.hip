@@ -495,9 +495,11 @@ hipError_t rows_product(const GroupedRows &a, const E &epi, int num_cus, hipStre
 // K x N: 16 waves per 32 columns where that is a workgroup per CU at most, else 8 (2
 // rows, 2304 x 768: 5.1 against 5.3; 4 rows 7.0 / 6.5).  N x K: one row at a time
 // where few groups have more (2 rows 4.4 against 4.8 and 3.9 / 4.5, 8 rows 11.1 /
-// 10.0 and 8.3 / 8.8).
+// 10.0 and 8.3 / 8.8).  Its workgroups have 4 or 32 columns: outputs of so many that
+// a grid does not hold them go to the tiles, of 32 rows by 32 columns at least.
 inline bool few_rows(const GroupedRows &a, bool nk) {
     const int64_t M = a.g.M, E = a.g.E;
+    if (M * tiles_of(a.N, nk ? 4 : 32) > INT_MAX) return false;      // a row per group at most
     return M <= 16 && (M <= E || (M <= 2 * E && (!nk || a.N <= 2048)));
 }
 

@@ -7,7 +7,7 @@ import pytest
 
 from gemv_gemm_f32_amd import binding as bd
 from gpu_util import torch
-from test_groups_host import _hipcc
+from test_groups_host import _hipcc, record  # noqa: F401 (a fixture)
 from test_largest_sizes import MOST, _e4m3, _equal, _pattern
 
 HOST = r"""
@@ -58,6 +58,16 @@ def test_counts_of_any_size(tmp_path):
     assert r.returncode == 0 and "ALL OK" in r.stdout, r.stdout + r.stderr
 
 
+# (W stored N x K, or K x N where it has rows of up to 2^22 columns or none)
+@pytest.mark.parametrize("M,N,K,E,v", [(16, 1 << 29, 1, 16, 1), (8, 1 << 30, 1, 8, 1), (8, (1 << 30) - 4, 1, 8, 1),
+                                       (4, MOST, 1, 4, 1), (1, MOST, 1, 1, 1), (16, 1 << 29, 1, 1024, 1),
+                                       (16, MOST, 0, 16, 0), (1, MOST, 0, 1, 0), (16, 1 << 22, 3, 16, 0)])
+def test_few_rows_over_many_columns(record, M, N, K, E, v):  # noqa: F811
+    """Fewer than 2^31 tiles of 32 x 32 are one launch, whatever its kernel."""
+    (name, groups), = record("forward", M, N, K, E, v)
+    assert "grouped_" in name and groups >= -(-N // 64) * (1 if E == 1 else min(M, 16))
+
+
 def _columns():
     """A vector of MOST columns."""
     t = torch()
@@ -85,6 +95,22 @@ def test_layer_of_most_columns(M):
     X = t.arange(1, M + 1, device="cuda").float()[:, None].contiguous()
     Y = t.full((M, MOST), -1.0, device="cuda")
     bd.linear_f32_grouped(X, W[None, :, None], _ints(0, M), Y=Y, trans_w=True)
+    ok = _every_row(Y, lambda m, i, j: _pattern(i, j) * (m + 1))
+    del W, Y
+    t.cuda.empty_cache()
+    assert ok
+
+
+@pytest.mark.gpu
+def test_rows_of_sixteen_experts_over_many_columns():
+    """More columns than a grid of the kernel for few rows holds; one matrix for
+    all experts."""
+    t = torch()
+    N = 1 << 29
+    W = _columns()[:N].clone()
+    Y = t.full((16, N), -1.0, device="cuda")
+    bd.linear_f32_grouped(t.arange(1, 17, device="cuda").float()[:, None].contiguous(), W[None, :, None].expand(16, N, 1),
+                          _ints(*range(17)), Y=Y, trans_w=True)
     ok = _every_row(Y, lambda m, i, j: _pattern(i, j) * (m + 1))
     del W, Y
     t.cuda.empty_cache()
