@@ -22,12 +22,13 @@ typedef v4f v4f_any __attribute__((aligned(4)));   // rows may start at any floa
 // number of earlier lanes among them.  Entries without an expert have the key E
 // and come last.
 //
-// Few entries are one workgroup's work, in one launch.  More are bound by the
-// scattered stores of rows, a cache line per lane, and are spread over
-// workgroups: one launch counts each workgroup's experts into rows (all of which
-// the last launch writes), a second finds the places, and a third writes rows.
-// (8,192 tokens, 8 of 128 experts: 57.5 us in one workgroup of 16 waves, 12.5 in
-// 64; 1,024 tokens, 8 of 64: one workgroup.)
+// Few entries are one workgroup's work, in one launch (512 tokens, 8 of 64 experts).
+// More are bound by the scattered stores of rows, a cache line per lane, and are
+// spread over workgroups: one launch counts each workgroup's experts into rows (all
+// of which the last launch writes), a second finds the places, and a third writes
+// rows: the call has no workspace, so that rows holds the counts until every
+// workgroup has read them (8,192 tokens, 8 of 128 experts: 12.8 us in 64 workgroups).
+// launch_expert_groups has the border, with both sides' times.
 struct Entries {
     const ExpertGroups &a;
     unsigned k;
